@@ -58,6 +58,15 @@ extern "C" {
 #define SGD_ERR_DOC_TOO_LONG  0x10u /* ingest: doc + sentinel exceeds the ring; skipped */
 #define SGD_ERR_LOOKBACK      0x20u /* suffix sort: a radix look-back gave up waiting */
 #define SGD_ERR_INGEST_WAIT   0x40u /* sgd_step: a doc's row update never showed; doc skipped */
+#define SGD_ERR_VERIFY_ROWS   0x80u /* sgd_verify: num_valid outside [0, k] (clamped) or a row of
+                                       logits outside [0, num_rows) (the row is not verified) */
+#define SGD_ERR_NO_TOKEN      0x100u /* sgd_verify: no token of a position has a probability; -1 */
+#define SGD_ERR_TEMPERATURE   0x200u /* sgd_verify: a negative or NaN temperature; taken as 0   */
+
+/* ---- element types of the floating tensors that a caller passes ---------- */
+#define SGD_F32   0
+#define SGD_F16   1
+#define SGD_BF16  2
 
 typedef struct sgd_ctx sgd_ctx; /* opaque, library-owned */
 
@@ -292,6 +301,44 @@ int sgd_step_host(sgd_ctx *ctx, int32_t *token_ids, int32_t *num_tokens, const i
                   int32_t *h_num_valid, float *h_score, float *h_probs, int32_t *h_match_info,
                   void *stream);
 
+/* Verifies a step's drafts against the target's probabilities and draws one
+ * more token per row, from given random numbers (speculative sampling): the
+ * accepted prefix and that token are together distributed as if the target
+ * had sampled them one by one.  Row b has v = num_valid[b] drafts and v + 1
+ * rows of logits; with l a row of logits, t the temperature, p = softmax(l / t):
+ *   draft x_i is accepted iff u[b, i] q_i(x_i) < p_i(x_i) and all before it
+ *   were; q = 1 without draft_probs (the suffix drafter proposes x_i outright);
+ *   at position a, the first not accepted, or v: the token argmax_j w_j /
+ *   noise[b, j], ties to the lowest j, with w = p for a = v, else max(p - q, 0),
+ *   without draft_probs p without x_a (w = p, should nothing of that be left);
+ *   t < 1e-5: x_i is accepted iff it is the lowest index of the largest logit,
+ *   and that index is the token.
+ * Logits of -inf (a sampler's cut) and NaN have probability 0; +inf ones share
+ * all of it.
+ *   logits     DEVICE dtype [num_rows, V], `row_stride` elements between rows.
+ *   row_start  DEVICE int32 [B]: row b's first row of logits, or NULL: b (k + 1).
+ *   drafts     DEVICE int32 [B, k];  num_valid DEVICE int32 [B] (as proposed).
+ *   active     DEVICE uint8 [B] or NULL; a 0 row accepts nothing and draws nothing.
+ *   temperature DEVICE float [B] or NULL (1).
+ *   uniform    DEVICE float [B, k] in [0, 1).
+ *   noise      DEVICE float [B, V], `noise_stride` between rows: Exp(1) draws
+ *              (values below 2^-60 count as 2^-60).
+ *   draft_probs DEVICE float or NULL: q, in the same rows as logits,
+ *              `probs_stride` between rows.
+ *   sampled    DEVICE int32 [B, k + 1]: the accepted drafts, the token, then -1:
+ *              the `sampled` of sgd_update_state and the calls that include it.
+ *   num_accepted DEVICE int32 [B]: accepted drafts (without the token).
+ *   logprobs   DEVICE float [B, k + 1] or NULL: log p of each emitted token (at
+ *              temperature 1 for a row with t < 1e-5), 0 after.
+ * V and k are the context's.  Two launches on `stream`; calls of one context
+ * must not overlap.  SGD_EINVAL for sizes or NULL arguments. */
+int sgd_verify(sgd_ctx *ctx, const void *logits, int32_t dtype, int64_t row_stride,
+               int64_t num_rows, const int32_t *row_start, const int32_t *drafts,
+               const int32_t *num_valid, const uint8_t *active, int32_t B,
+               const float *temperature, const float *uniform, const float *noise,
+               int64_t noise_stride, const float *draft_probs, int64_t probs_stride,
+               int32_t *sampled, int32_t *num_accepted, float *logprobs, void *stream);
+
 /* Appends finished responses to the corpus ring ([PYPI] Quickstart:
  * harvest_finished; How it works, step 4: oldest documents are evicted when
  * the ring is full; [DOCS] Model Runner V2: oldest first out).
@@ -461,6 +508,96 @@ int sgd_reset_rows(sgd_ctx *ctx, const int32_t *token_ids, const int32_t *num_to
  * device bytes (ring, both snapshots with their indexes, sort scratch,
  * staging) and page-locked host bytes.  Either pointer may be null. */
 int sgd_memory(sgd_ctx *ctx, int64_t *device_bytes, int64_t *pinned_bytes);
+
+/* ---- the target's cache: paged, 8 bits ----------------------------------
+ *
+ * What the target's verification pass needs next to the drafts: the keys and
+ * values of a row's 1 + num_valid new tokens enter a paged cache, and those
+ * tokens attend over it.  The cache's memory is the caller's, one sgd_kv_layer
+ * per layer; a handle holds the geometry that its layers share, the workspace
+ * of the attention and a sticky error word.  Positions are a row's own, from
+ * 0; position j of row b lives in page block_table[b, j / page_size], slot
+ * j % page_size.  A rejected draft needs no call: the next write starts at its
+ * position.  All calls can be captured in a CUDA graph; calls of one handle
+ * must not overlap. */
+typedef struct sgd_kv sgd_kv; /* opaque, library-owned */
+
+typedef struct {
+  int32_t num_pages;          /* pages of a layer                                     */
+  int32_t page_size;          /* tokens of a page: 16, 32, 64 or 128                  */
+  int32_t kv_heads;           /* heads of keys and values (<= 1024)                   */
+  int32_t q_heads;            /* query heads: a multiple of kv_heads, at most 64 times;
+                                 head h reads keys and values of h / (q_heads / kv_heads) */
+  int32_t head_dim;           /* 64 or 128                                            */
+  int32_t max_batch;          /* rows of a call                                       */
+  int32_t max_pages_per_row;  /* row stride of block_table                            */
+} sgd_kv_config;              /* num_pages kv_heads page_size < 2^31                   */
+
+/* One layer, all DEVICE memory of the caller: keys and values as e4m3 bytes
+ * [num_pages, kv_heads, page_size, head_dim] (16-byte aligned), and a float
+ * scale for each block of a page's tokens and head, [num_pages, kv_heads]:
+ * value = byte * scale.  Scales are powers of two, 2^-48 .. 2^48. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+} sgd_kv_layer;
+
+/* ---- sticky device error bits of a handle (sgd_kv_get_error) ------------ */
+#define SGD_KV_ERR_PAGE      0x1u /* a page id outside [0, num_pages) or past the table: its
+                                     tokens are not written, read as 0, not attended to  */
+#define SGD_KV_ERR_LENGTH    0x2u /* fewer tokens in a row than new ones, or more than its
+                                     table holds, or tokens past the last row: skipped   */
+#define SGD_KV_ERR_NONFINITE 0x4u /* written as the largest magnitude (infinities) or 0 (NaN) */
+
+/* SGD_EINVAL for a geometry outside the limits above. */
+int sgd_kv_create(const sgd_kv_config *cfg, int device, sgd_kv **out);
+int sgd_kv_destroy(sgd_kv *kv);
+
+/* Writes new keys and values.  The N tokens of a call are packed: row b's are
+ * q_start[b] .. q_start[b + 1], the last ones of its seq_lens[b] tokens (the
+ * new ones included).
+ *   k, v        DEVICE dtype [N, kv_heads, head_dim], strides in elements
+ *               between tokens and heads, the last dimension contiguous (parts
+ *               of one projection's output are taken as they are).
+ *   block_table DEVICE int32 [B, max_pages_per_row], seq_lens DEVICE int32 [B],
+ *   q_start     DEVICE int32 [B + 1], ascending from 0 to N.
+ * A block's scale is the smallest power of two that brings its largest
+ * magnitude, over the entries before the first new token and the new ones, to
+ * at most 448; entries already there are encoded again where that changes it.
+ * Pages that two rows share must not be written by both. */
+int sgd_kv_write(sgd_kv *kv, const sgd_kv_layer *layer, const void *k, const void *v,
+                 int32_t dtype, int64_t k_token_stride, int64_t k_head_stride,
+                 int64_t v_token_stride, int64_t v_head_stride, const int32_t *block_table,
+                 const int32_t *seq_lens, const int32_t *q_start, int32_t B, int32_t N,
+                 void *stream);
+
+/* Reads positions back as dtype: row b's from[b], from[b] + 1, .. are the
+ * outputs out_start[b] .. out_start[b + 1] (ascending from 0 to N).
+ *   k, v DEVICE dtype [N, kv_heads, head_dim], contiguous, 16-byte aligned. */
+int sgd_kv_read(sgd_kv *kv, const sgd_kv_layer *layer, const int32_t *block_table,
+                const int32_t *from, const int32_t *out_start, int32_t B, int32_t N, void *k,
+                void *v, int32_t dtype, void *stream);
+
+/* Attention of the N packed new tokens (rows as in sgd_kv_write, which comes
+ * first) over their rows' cache: the token at position p sees positions j <= p;
+ * with window > 0 those with j > p - window or j < sinks (the first tokens,
+ * which stay visible).
+ *   q    DEVICE dtype (SGD_F16 or SGD_BF16) [N, q_heads, head_dim], strides in
+ *        elements, the last dimension contiguous.
+ *   max_q  the most new tokens of any row (rows with more are cut to it).
+ *   scale  of the products before the softmax.
+ *   out  DEVICE dtype [N, q_heads, head_dim], contiguous, 16-byte aligned; 0 for
+ *        a token that sees nothing. */
+int sgd_kv_attend(sgd_kv *kv, const sgd_kv_layer *layer, const void *q, int32_t dtype,
+                  int64_t q_token_stride, int64_t q_head_stride, const int32_t *block_table,
+                  const int32_t *seq_lens, const int32_t *q_start, int32_t B, int32_t N,
+                  int32_t max_q, float scale, int32_t window, int32_t sinks, void *out,
+                  void *stream);
+
+/* As sgd_get_error, sgd_memory and sgd_launch_count, of a cache handle. */
+int sgd_kv_get_error(sgd_kv *kv, uint32_t *flags, int clear);
+int sgd_kv_memory(sgd_kv *kv, int64_t *device_bytes);
+int sgd_kv_launch_count(sgd_kv *kv, uint64_t *count);
 
 const char *sgd_strerror(int status);
 int sgd_version(void); /* major * 10000 + minor * 100 + patch */

@@ -30,6 +30,16 @@ ERR_DOC_TOKEN = 0x8
 ERR_DOC_TOO_LONG = 0x10
 ERR_LOOKBACK = 0x20
 ERR_INGEST_WAIT = 0x40
+ERR_VERIFY_ROWS = 0x80
+ERR_NO_TOKEN = 0x100
+ERR_TEMPERATURE = 0x200
+KV_ERR_PAGE = 0x1
+KV_ERR_LENGTH = 0x2
+KV_ERR_NONFINITE = 0x4
+
+F32 = 0
+F16 = 1
+BF16 = 2
 
 INJECT_NONE = 0
 INJECT_BUILD_FAIL = 1
@@ -83,6 +93,27 @@ class SgdBuildInfo(ctypes.Structure):
     ]
 
 
+class SgdKvConfig(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("max_batch", ctypes.c_int32),
+        ("max_pages_per_row", ctypes.c_int32),
+    ]
+
+
+class SgdKvLayer(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
 class SgdError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -113,6 +144,18 @@ def load() -> ctypes.CDLL:
         "sgd_update_state": (ctypes.c_int, [P, P, P, P, i32, i32, P]),
         "sgd_propose": (ctypes.c_int, [P, P, P, P, i32, P, P, P, P, P, P]),
         "sgd_propose_with_update": (ctypes.c_int, [P, P, P, P, i32, P, i32, P, P, P, P, P, P]),
+        "sgd_verify": (ctypes.c_int, [P, P, i32, i64, i64, P, P, P, P, i32, P, P, P, i64, P, i64,
+                                      P, P, P, P]),
+        "sgd_kv_create": (ctypes.c_int, [ctypes.POINTER(SgdKvConfig), ctypes.c_int,
+                                         ctypes.POINTER(P)]),
+        "sgd_kv_destroy": (ctypes.c_int, [P]),
+        "sgd_kv_write": (ctypes.c_int, [P, P, P, P, i32, i64, i64, i64, i64, P, P, P, i32, i32, P]),
+        "sgd_kv_read": (ctypes.c_int, [P, P, P, P, P, i32, i32, P, P, i32, P]),
+        "sgd_kv_attend": (ctypes.c_int, [P, P, P, i32, i64, i64, P, P, P, i32, i32, i32,
+                                         ctypes.c_float, i32, i32, P, P]),
+        "sgd_kv_get_error": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]),
+        "sgd_kv_memory": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_int64)]),
+        "sgd_kv_launch_count": (ctypes.c_int, [P, u64p]),
         "sgd_ingest": (ctypes.c_int, [P, P, P, i32, P, P, P, i32, P]),
         "sgd_step": (ctypes.c_int, [P, P, P, P, i32, P, i32, P, P, P, P, P, P, P, P, i32, P]),
         "sgd_step_host": (ctypes.c_int, [P, P, P, P, i32, i32, P, P, P, i32, P, P, P, P, P, P]),

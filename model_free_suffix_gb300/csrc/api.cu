@@ -45,6 +45,7 @@ struct sgd_ctx {
   int32_t *d_hin = nullptr;         // sgd_step_host inputs: sampled, rows, starts, lengths
   int32_t *d_hout = nullptr;        // sgd_step_host outputs: drafts, num_valid, score, probs, match_info
   int32_t *d_self_res = nullptr;    // two-launch propose: per-row self results
+  unsigned char *d_verify = nullptr; // sgd_verify's workspace (verify_layout)
   int32_t *d_row_stats = nullptr;   // caller's [max_batch, 4] statistics buffer, or null
   int64_t dev_bytes = 0;            // device memory the context allocated
   int64_t pinned_bytes = 0;         // page-locked host memory the context allocated
@@ -159,6 +160,7 @@ void free_ctx(sgd_ctx *x) {
   cudaFree(x->d_ri_claim);
   cudaFree(x->d_step_ready);
   cudaFree(x->d_hin);
+  cudaFree(x->d_verify);
   cudaFree(x->d_self_res);
   cudaFree(x->d_hout);
   cudaFree(x->d_rec[0]);
@@ -395,6 +397,16 @@ int sgd_create(const sgd_config *cfg, int device, sgd_ctx **out) {
   }
   if (e == cudaSuccess) e = cudaMemset(x->d_err, 0, 4);
   if (e == cudaSuccess) e = cudaMemset(x->d_build_err, 0, 4);
+  {
+    // no position counted yet, no row ended
+    const VerifyLayout l = verify_layout(cfg->max_batch, cfg->k);
+    al((void **)&x->d_verify, l.bytes);
+    if (e == cudaSuccess) e = cudaMemset(x->d_verify, 0, l.bytes);
+    if (e == cudaSuccess) {
+      const std::vector<int32_t> none((size_t)cfg->max_batch, 0x7fffffff);
+      e = cudaMemcpy(x->d_verify + l.stop, none.data(), none.size() * 4, cudaMemcpyHostToDevice);
+    }
+  }
   if (cfg->row_index) {
     // every entry empty (generation 0); every row invalid until it is reset
     const size_t Bm = (size_t)cfg->max_batch;
@@ -777,6 +789,53 @@ int sgd_step_host(sgd_ctx *x, int32_t *token_ids, int32_t *num_tokens, const int
   if (e == cudaSuccess && h_match_info && run <= 2 * Bk + 2 * (size_t)B)
     e = cudaMemcpyAsync(h_match_info, d_mi, (size_t)B * 8, d2h, st);
   return check_cuda(e);
+}
+
+int sgd_verify(sgd_ctx *x, const void *logits, int32_t dtype, int64_t row_stride, int64_t num_rows,
+               const int32_t *row_start, const int32_t *drafts, const int32_t *num_valid,
+               const uint8_t *active, int32_t B, const float *temperature, const float *uniform,
+               const float *noise, int64_t noise_stride, const float *draft_probs,
+               int64_t probs_stride, int32_t *sampled, int32_t *num_accepted, float *logprobs,
+               void *stream) {
+  if (!x || B < 0 || B > x->cfg.max_batch) return SGD_EINVAL;
+  if (dtype != SGD_F32 && dtype != SGD_F16 && dtype != SGD_BF16) return SGD_EINVAL;
+  if (B == 0) return SGD_OK;
+  if (!logits || !drafts || !num_valid || !uniform || !noise || !sampled || !num_accepted)
+    return SGD_EINVAL;
+  const int V = x->cfg.vocab_size;
+  if (num_rows < 0 || row_stride < V || noise_stride < V || (draft_probs && probs_stride < V))
+    return SGD_EINVAL;
+  if (((uintptr_t)logits & (dtype == SGD_F32 ? 3u : 1u)) != 0) return SGD_EINVAL;
+  const VerifyLayout l = verify_layout(x->cfg.max_batch, x->cfg.k);
+  VerifyArgs a{};
+  a.logits = logits;
+  a.stride = row_stride;
+  a.rows = num_rows;
+  a.row_start = row_start;
+  a.drafts = drafts;
+  a.num_valid = num_valid;
+  a.active = active;
+  a.B = B;
+  a.V = V;
+  a.k = x->cfg.k;
+  a.temp = temperature;
+  a.uniform = uniform;
+  a.noise = noise;
+  a.noise_stride = noise_stride;
+  a.q = draft_probs;
+  a.q_stride = probs_stride;
+  a.sampled = sampled;
+  a.accepted = num_accepted;
+  a.logprobs = logprobs;
+  a.err = x->d_err;
+  a.part = reinterpret_cast<float4 *>(x->d_verify + l.part);
+  a.draw_part = reinterpret_cast<float4 *>(x->d_verify + l.draw_part);
+  a.stat = reinterpret_cast<float4 *>(x->d_verify + l.stat);
+  a.count = reinterpret_cast<unsigned *>(x->d_verify + l.count);
+  a.draw_count = reinterpret_cast<unsigned *>(x->d_verify + l.draw_count);
+  a.stop = reinterpret_cast<int *>(x->d_verify + l.stop);
+  x->launches += 2;
+  return check_cuda(launch_verify(a, dtype, (cudaStream_t)stream));
 }
 
 int sgd_ingest(sgd_ctx *x, const int32_t *token_ids, const int32_t *num_tokens, int32_t B,

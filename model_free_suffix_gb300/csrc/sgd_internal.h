@@ -205,6 +205,36 @@ cudaError_t propose_set_smem_limit(size_t bytes);
 cudaError_t launch_backoff(const ProposeArgs &a, cudaStream_t st);
 cudaError_t backoff_set_smem_limit();  // the backoff kernel's dynamic shared memory (its row-length cache)
 
+// verify.cu
+struct VerifyArgs {
+  const void *logits;
+  long long stride, rows;
+  const int32_t *row_start, *drafts, *num_valid;
+  const uint8_t *active;
+  int B, V, k;
+  const float *temp, *uniform, *noise;
+  long long noise_stride;
+  const float *q;  // draft probabilities, or null
+  long long q_stride;
+  int32_t *sampled, *accepted;
+  float *logprobs;
+  uint32_t *err;
+  // workspace (verify_layout)
+  float4 *part;         // [positions][splits] {m, Z, argmax}
+  float4 *draw_part;    // [B][draw_splits]
+  float4 *stat;         // [B][k + 1] {m, Z, argmax}
+  unsigned *count;      // [B][k + 1] splits done; 0 between calls
+  unsigned *draw_count; // [B]
+  int *stop;            // [B] first position not accepted; 2^31 - 1 between calls
+  int splits, draw_splits;
+};
+struct VerifyLayout {
+  size_t part, draw_part, stat, count, draw_count, stop, bytes;
+};
+VerifyLayout verify_layout(int max_batch, int k);
+// dtype: SGD_F32, SGD_F16 or SGD_BF16
+cudaError_t launch_verify(const VerifyArgs &a, int dtype, cudaStream_t st);
+
 // corpus.cu
 struct IngestScratch {
   int32_t *eff;     // [max_ingest_docs] effective doc length (-1: skip)

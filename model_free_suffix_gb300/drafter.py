@@ -48,6 +48,16 @@ class Proposal:
     match_info: torch.Tensor   # [B, 2] int32: {match length, source (0 none, 1 self, 2 corpus)}
 
 
+@dataclass
+class Verdict:
+    sampled: torch.Tensor       # [B, k + 1] int32: accepted drafts, one more token, then -1
+    num_accepted: torch.Tensor  # [B] int32
+    logprobs: torch.Tensor      # [B, k + 1] float32: of each emitted token, 0 after
+
+
+_DTYPES = {torch.float32: L.F32, torch.float16: L.F16, torch.bfloat16: L.BF16}
+
+
 class SuffixDrafter:
     """One libsgd context on one GPU.
 
@@ -242,6 +252,66 @@ class SuffixDrafter:
                 raise L.SgdError(st, "sgd_step_host")
 
         return step_bound
+
+    # -- verification ---------------------------------------------------------
+    def new_verdict(self, B: int) -> Verdict:
+        d = self.device
+        return Verdict(torch.empty((B, self.k + 1), dtype=torch.int32, device=d),
+                       torch.empty(B, dtype=torch.int32, device=d),
+                       torch.empty((B, self.k + 1), dtype=torch.float32, device=d))
+
+    def verify(self, logits: torch.Tensor, drafts: torch.Tensor, num_valid: torch.Tensor,
+               uniform: torch.Tensor, noise: torch.Tensor, row_start: Optional[torch.Tensor] = None,
+               temperature: Optional[torch.Tensor] = None,
+               draft_probs: Optional[torch.Tensor] = None, active: Optional[torch.Tensor] = None,
+               out: Optional[Verdict] = None, stream=None) -> Verdict:
+        """Verifies a step's drafts against the target's logits and draws one
+        more token per row; `sampled` of the result is what update_state,
+        propose_with_update and step take.
+
+        logits [rows, V] (float32, float16 or bfloat16; any row stride): row b's
+        num_valid[b] + 1 positions are its rows row_start[b], row_start[b] + 1,
+        ... (row_start=None: b (k + 1), ...).  uniform [B, k] in [0, 1) and noise
+        [B, V], Exp(1) draws (``tensor.exponential_()``), are the random
+        numbers; draft_probs [rows, V] float32 are the probabilities the drafts
+        were drawn from (None: proposed outright, as by this drafter).
+        temperature [B] float32 (None: 1; below 1e-5: greedy)."""
+        B = num_valid.shape[0]
+        if logits.dtype not in _DTYPES or logits.dim() != 2:
+            raise ValueError("logits must be a [rows, V] tensor of float32, float16 or bfloat16")
+        if logits.shape[1] != self.V or noise.shape != (B, self.V) or uniform.shape != (B, self.k) \
+                or drafts.shape != (B, self.k):
+            raise ValueError("logits [rows, V], noise [B, V], uniform [B, k] and drafts [B, k] must "
+                             "agree with the context's V = %d and k = %d" % (self.V, self.k))
+        if draft_probs is not None and draft_probs.shape != logits.shape:
+            raise ValueError("draft_probs must have the shape of logits")
+        for t, n in ((row_start, "row_start"), (temperature, "temperature"), (active, "active")):
+            if t is not None and t.shape[0] < B:
+                raise ValueError("%s must have an entry per row" % n)
+        out = out or self.new_verdict(B)
+        self._check(self._lib.sgd_verify(
+            self._h, self._rows(logits, logits.dtype, "logits"), _DTYPES[logits.dtype],
+            logits.stride(0) if logits.shape[0] > 1 else self.V, logits.shape[0],
+            self._t(row_start, name="row_start"), self._t(drafts, name="drafts"),
+            self._t(num_valid, name="num_valid"), self._t(active, torch.uint8, "active"), B,
+            self._t(temperature, torch.float32, "temperature"),
+            self._t(uniform, torch.float32, "uniform"), self._rows(noise, torch.float32, "noise"),
+            noise.stride(0) if B > 1 else self.V, self._rows(draft_probs, torch.float32, "draft_probs"),
+            (draft_probs.stride(0) if draft_probs.shape[0] > 1 else self.V)
+            if draft_probs is not None else 0,
+            self._t(out.sampled), self._t(out.num_accepted), self._t(out.logprobs, torch.float32),
+            _stream_handle(stream)), "sgd_verify")
+        return out
+
+    def _rows(self, t: Optional[torch.Tensor], dtype, name: str):
+        """The address of a tensor whose rows may be apart but are contiguous themselves."""
+        if t is None:
+            return None
+        if t.device != self.device:
+            raise ValueError("%s must be on %s" % (name, self.device))
+        if t.dtype != dtype or (t.stride(1) != 1 and t.shape[1] > 1):
+            raise ValueError("%s must be a %s tensor with contiguous rows" % (name, dtype))
+        return t.data_ptr()
 
     # -- corpus ---------------------------------------------------------------
     def ingest(self, token_ids: torch.Tensor, rows: torch.Tensor, starts: torch.Tensor,
