@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(THREADS) kv_attend_kernel(KvAttendArgs a) {
       L += sl[w] * c;
       x += so[w][d] * c;
     }
-    out[d] = from_f32<T>(L > 0.f ? x / L : 0.f);
+    out[d] = from_f32<T>(L == 0.f ? 0.f : x / L);
   }
 }
 
