@@ -547,6 +547,7 @@ typedef struct {
                                      tokens are not written, read as 0, not attended to  */
 #define SGD_KV_ERR_LENGTH    0x2u /* fewer tokens in a row than new ones, or more than its
                                      table holds, or tokens past the last row: skipped   */
+#define SGD_KV_ERR_WAIT      0x8u /* sgd_kv_attend: a copy never arrived; results are not valid */
 #define SGD_KV_ERR_NONFINITE 0x4u /* written as the largest magnitude (infinities) or 0 (NaN) */
 
 /* SGD_EINVAL for a geometry outside the limits above. */

@@ -36,6 +36,7 @@ ERR_TEMPERATURE = 0x200
 KV_ERR_PAGE = 0x1
 KV_ERR_LENGTH = 0x2
 KV_ERR_NONFINITE = 0x4
+KV_ERR_WAIT = 0x8
 
 F32 = 0
 F16 = 1

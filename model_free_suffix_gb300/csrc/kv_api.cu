@@ -12,6 +12,7 @@ using namespace sgd;
 struct sgd_kv {
   sgd_kv_config cfg;
   int device = 0;
+  int sms = 0;
   uint32_t *d_err = nullptr;
   unsigned char *d_work = nullptr;
   size_t work_bytes = 0;
@@ -67,11 +68,12 @@ int sgd_kv_create(const sgd_kv_config *cfg, int device, sgd_kv **out) {
   if (!x) return SGD_ENOMEM;
   x->cfg = *cfg;
   x->device = device;
-  x->work_bytes = kv_attend_workspace(*cfg);
+  x->work_bytes = kv_attend_workspace();
   cudaError_t e = cudaMalloc((void **)&x->d_err, 4);
   if (e == cudaSuccess) e = cudaMemset(x->d_err, 0, 4);
   if (e == cudaSuccess) e = cudaMalloc((void **)&x->d_work, x->work_bytes);
   if (e == cudaSuccess) e = cudaMemset(x->d_work, 0, x->work_bytes);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&x->sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) e = kv_attend_set_limits();
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
@@ -170,6 +172,7 @@ int sgd_kv_attend(sgd_kv *x, const sgd_kv_layer *layer, const void *q, int32_t d
   a.scale = scale;
   a.window = window;
   a.sinks = sinks;
+  a.sms = x->sms;
   a.work = x->d_work;
   a.err = x->d_err;
   int launches = 0;

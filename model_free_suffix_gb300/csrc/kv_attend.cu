@@ -3,104 +3,642 @@
 //   o_r = sum_j softmax_j(scale q_r . k_j) v_j   over the positions j that row
 //   r's token, at position p, sees: j <= p, and with a window j > p - window or
 //   j < sinks.
+//
+// One pass over keys and values with a running maximum m and sum l per row: a
+// tile's products s give m' = max(m, max s), and l and o are scaled by
+// 2^(m - m') before the tile's 2^(s - m') are added (s in units of log 2).
+// Rows of the query heads that share a head of keys and values go together, so
+// that each byte of the cache is read once for all of them.
 #include <math_constants.h>
 
+#include <type_traits>
+
+#include "async_copy.cuh"
 #include "kv_internal.h"
+#include "kv_sched.cuh"
 #include "num_types.cuh"
 #include "sgd_internal.h"
 
 namespace sgd {
 namespace {
 
-constexpr int THREADS = 128;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_CTAS = 152 * 3;
+constexpr float LAZY = 8.f;  // o and l are scaled once the maximum has grown by 2^8
 
-// One CTA per new token and query head; its warps take every fourth position.
-template <typename T>
-__global__ void __launch_bounds__(THREADS) kv_attend_kernel(KvAttendArgs a) {
-  __shared__ float so[THREADS / 32][128];
-  __shared__ float sm[THREADS / 32], sl[THREADS / 32];
-  const int i = blockIdx.x, hq = blockIdx.y, h = hq / a.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int D = a.c.dim, P = a.c.page, per = D / 32;
-  const int b = row_of_token(a.r.q_start, a.r.B, i);
-  T *out = static_cast<T *>(a.out) + ((long long)i * a.q_heads + hq) * D;
-  int p = -1;
-  if (b < a.r.B) {
-    const int q0 = a.r.q_start[b], q1 = a.r.q_start[b + 1], n = a.r.seq_lens[b];
-    p = n - (q1 - q0) + (i - q0);
-    if (n < q1 - q0 || (long long)n > (long long)a.r.max_pages * P) p = -1;
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// Where the parts of split units and their counters lie in the workspace.
+template <int M, int D>
+__device__ __forceinline__ float *part_of(const KvAttendArgs &a, int slot) {
+  return reinterpret_cast<float *>(a.work + MAX_CTAS * 8) + (long long)slot * (M * (D + 2));
+}
+
+// Few rows (M = 16 MT <= 32 a unit), bound by reading the cache.  Each warp
+// streams its own 32-token tiles through a ring of TMA loads, S deep, and keeps
+// m, l and o of all the unit's rows in registers; warps meet only where a unit
+// ends.  e4m3 is taken to f16, exactly, on the way into the registers that
+// feed the matrix instructions, so the products carry no rounding of the
+// cache's; q goes to f16 after each row is scaled to [1, 2) by a power of two
+// (bf16 has fewer bits than f16: only elements 2^-24 times the row's largest
+// lose any), and the probabilities to f16 (relative 2^-12 each, in values up to
+// 2^8; the sum l is taken before that rounding).  The scales of a block of
+// keys multiply its products; o is held in units of a recent block's value
+// scale, and probabilities of blocks with another one are scaled by the ratio.
+//
+// The order of the elements of a product's long axis is free as long as both
+// sides use the same: a lane takes 2 (D = 128) or 1 (D = 64) whole 16-byte
+// chunks of a key, so all shared-memory reads are 16 bytes wide and, with the
+// 128-byte swizzle of the TMA load, without bank conflicts.
+template <typename T, int D, int MT, int S>
+__global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, const __grid_constant__ CUtensorMap kmap,
+                                                             const __grid_constant__ CUtensorMap vmap) {
+  constexpr int M = 16 * MT;
+  constexpr int KS = D / 16;                 // k steps of q . k
+  constexpr int HALF = KV_TILE * D;          // bytes of a tile's keys (or values)
+  constexpr int NJ = D / 16;                 // 16-dim groups of the output
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  __shared__ __align__(8) unsigned long long bars[WARPS * S];
+  __shared__ float s_f[M];
+  __shared__ float s_m[WARPS][M], s_l[WARPS][M];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t bits = 0;
+  const KvShare share = kv_share<THREADS>(a, M, WARPS, &bits);
+  if (share.begin >= share.end) {
+    if (bits && tid == 0) atomicOr(a.err, bits);
+    return;
   }
-  if (p < 0 && threadIdx.x == 0) atomicOr(a.err, SGD_KV_ERR_LENGTH);
-  const T *q = static_cast<const T *>(a.q) + i * a.q_token + hq * a.q_head;
-  float qr[4], o[4];
-  for (int e = 0; e < per; ++e) {
-    qr[e] = to_f32(q[lane * per + e]);
-    o[e] = 0.f;
-  }
-  float m = -CUDART_INF_F, l = 0.f;
-  const int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  for (int j = warp; j <= p; j += THREADS / 32) {
-    if (j < lo && j >= a.sinks) continue;
-    const int page = a.r.table[(long long)b * a.r.max_pages + j / P];
-    if (page < 0 || page >= a.c.num_pages) {
-      if (lane == 0) atomicOr(a.err, SGD_KV_ERR_PAGE);
-      continue;
-    }
-    const long long at = (long long)page * a.c.heads + h;
-    const uint8_t *k = a.c.k + (at * P + j % P) * D + lane * per;
-    const uint8_t *v = a.c.v + (at * P + j % P) * D + lane * per;
-    float s = 0.f, x[4];
-    for (int e = 0; e < per; e += 2) {
-      const uint32_t w = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(k + e));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-      s += qr[e] * f.x + qr[e + 1] * f.y;
-      const uint32_t u = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(v + e));
-      const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&u));
-      x[e] = g.x;
-      x[e + 1] = g.y;
-    }
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(FULL, s, d);
-    s *= a.scale * a.c.ks[at];
-    const float m2 = fmaxf(m, s), c = __expf(m - m2), w = __expf(s - m2);
-    l = l * c + w;
-    const float wv = w * a.c.vs[at];
-    for (int e = 0; e < per; ++e) o[e] = o[e] * c + wv * x[e];
-    m = m2;
-  }
-  for (int e = 0; e < per; ++e) so[warp][lane * per + e] = o[e];
+  const uint32_t ring = smem_addr(smem) + warp * S * 2 * HALF;
+  const uint32_t q_at = smem_addr(smem) + WARPS * S * 2 * HALF;
+  const uint32_t bar0 = smem_addr(bars) + warp * S * 8;
   if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    for (int i = 0; i < S; ++i) bar_init(bar0 + 8 * i, 1);
+    bar_init_fence();
   }
-  __syncthreads();
-  float M = -CUDART_INF_F;
-  for (int w = 0; w < THREADS / 32; ++w) M = fmaxf(M, sm[w]);
-  for (int d = threadIdx.x; d < D; d += THREADS) {
-    float L = 0.f, x = 0.f;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (sl[w] == 0.f) continue;
-      const float c = __expf(sm[w] - M);
-      L += sl[w] * c;
-      x += so[w][d] * c;
+  __syncwarp();
+  uint32_t filled = 0, drained = 0;  // tiles of this warp loaded and consumed
+
+  const int P = a.c.page, H = a.c.heads;
+  const int halves = P < KV_TILE ? 2 : 1;  // pages of a tile
+  long long at = share.begin, b_begin = share.b_begin;
+  int b = share.b;
+  KvJob job = kv_job(a, b, M, &bits);
+  while (at < share.end) {
+    while (at >= b_begin + kv_work(job, H)) {
+      b_begin += kv_work(job, H);
+      ++b;
+      job = kv_job(a, b, M, &bits);
     }
-    out[d] = from_f32<T>(L == 0.f ? 0.f : x / L);
+    // the unit and the range of its tiles that this share holds
+    const int u = (int)((at - b_begin) / job.tiles);
+    const long long u_begin = b_begin + (long long)u * job.tiles, u_end = u_begin + job.tiles;
+    const int t0 = (int)(at - u_begin);
+    const int t1 = (int)(min(u_end, share.end) - u_begin);
+    at = u_begin + t1;
+    const int h = u % H, rt = u / H;
+    const int r0 = rt * M, nrows = min(M, job.ql * a.group - r0);
+    const int p_first = job.n - job.ql + r0 / a.group;
+    const int p_last = job.n - job.ql + (r0 + nrows - 1) / a.group;
+    const int32_t *table = a.r.table + (long long)b * a.r.max_pages;
+
+    // ---- this warp's tiles: t0 + warp, + WARPS, ...; those that no row of the
+    // unit sees are passed over
+    auto seen = [&](int j) {
+      const int x = job.tile(j) * KV_TILE;
+      if (x > p_last) return false;
+      return a.window == 0 || x + KV_TILE - 1 > p_first - a.window || x < a.sinks;
+    };
+    // lane i holds what the i-th of the next 32 needs
+    int page[2], ahead_page[2];
+    float ks[2], vs[2];
+    auto look = [&](int j0, int (&pg)[2]) {
+      const int j = j0 + WARPS * lane;
+      pg[0] = pg[1] = -1;
+      if (j >= t1 || job.n == 0) return;
+      const int x = job.tile(j) * KV_TILE;
+      for (int i = 0; i < halves; ++i) {
+        const int block = x / P + i;
+        if (block < a.r.max_pages && block * P < job.n) {
+          pg[i] = __ldg(table + block);
+          if (pg[i] < 0 || pg[i] >= a.c.num_pages) {
+            pg[i] = -1;
+            bits |= SGD_KV_ERR_PAGE;
+          }
+        }
+      }
+      if (halves == 1) pg[1] = pg[0];
+    };
+    auto load = [&](int j, int p0, int p1) {  // by one lane
+      const uint32_t slot = filled % S;
+      const uint32_t dst = ring + slot * 2 * HALF, bar = bar0 + 8 * slot;
+      constexpr int PACK = 128 / D;  // tokens of a 128-byte line
+      bar_expect(bar, 2 * HALF);
+      const int x = job.tile(j) * KV_TILE;
+      if (halves == 1) {
+        const int y = ((max(p0, 0) * H + h) * P + x % P) / PACK;
+        tma_load_2d(dst, &kmap, 0, y, bar);
+        tma_load_2d(dst + HALF, &vmap, 0, y, bar);
+      } else {
+        const int y0 = (max(p0, 0) * H + h) * P / PACK, y1 = (max(p1, 0) * H + h) * P / PACK;
+        tma_load_2d(dst, &kmap, 0, y0, bar);
+        tma_load_2d(dst + HALF / 2, &kmap, 0, y1, bar);
+        tma_load_2d(dst + HALF, &vmap, 0, y0, bar);
+        tma_load_2d(dst + HALF + HALF / 2, &vmap, 0, y1, bar);
+      }
+    };
+    int next = t0 + warp, next_i = 0;  // the next tile to load, its lane in ahead_page
+    look(next, ahead_page);
+    auto advance = [&]() {  // loads the next tile that is seen, if any
+      while (next < t1) {
+        const int j = next, i = next_i;
+        const int p0 = __shfl_sync(FULL, ahead_page[0], i), p1 = __shfl_sync(FULL, ahead_page[1], i);
+        next += WARPS;
+        if (++next_i == 32) {
+          next_i = 0;
+          look(next, ahead_page);
+        }
+        if (!seen(j)) continue;
+        if (lane == 0) load(j, p0, p1);
+        ++filled;
+        return;
+      }
+    };
+    for (int i = 0; i < S; ++i) advance();
+
+    // ---- the unit's queries, as the matrix instructions take them
+    for (int r = warp; r < M; r += WARPS) {
+      const bool on = r < nrows;
+      const int row = r0 + r;
+      const T *q = static_cast<const T *>(a.q) + (long long)(job.q0 + row / a.group) * a.q_token +
+                   (long long)(h * a.group + row % a.group) * a.q_head;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      const bool mine = lane * 4 < D;
+      if (on && mine) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = to_f32(q[lane * 4 + e]);
+      }
+      float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bad = bad || !(fabsf(x[e]) < CUDART_INF_F);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+      const bool poison = __any_sync(FULL, bad);  // (a bad element makes its row NaN)
+      const int e2 = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+      const float inv = poison ? CUDART_NAN_F : pow2(-min(e2, 126));
+      if (lane == 0) s_f[r] = a.scale * LOG2E * pow2(min(e2, 126));
+      if (mine) {
+        constexpr int DPT = D / 4;  // dims of a lane
+        const int d = lane * 4, qc = d / DPT, s = d % DPT / 4;
+        const uint32_t w = q_at + (((r / 16) * KS + s) * 32 + (r % 8) * 4 + qc) * 16 + (r % 16) / 8 * 4;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(w), "r"(pack2<__half>(x[0] * inv, x[1] * inv)) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(w + 8), "r"(pack2<__half>(x[2] * inv, x[3] * inv)) : "memory");
+      }
+    }
+    __syncthreads();
+
+    float o[MT][2 * NJ][4];
+    float m[MT][2], l[MT][2], f[MT][2];
+    int pos[MT][2];
+    float unit = 0.f;  // o is in units of this value scale
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = mt * 16 + x * 8 + g;
+        m[mt][x] = -CUDART_INF_F;
+        l[mt][x] = 0.f;
+        f[mt][x] = s_f[r];
+        pos[mt][x] = r < nrows ? job.n - job.ql + (r0 + r) / a.group : -1;
+      }
+#pragma unroll
+      for (int n = 0; n < 2 * NJ; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+    }
+
+    int batch = 0;
+    for (int j = t0 + warp; j < t1; j += WARPS, ++batch) {
+      if ((batch & 31) == 0) {
+        look(j, page);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const long long s = (long long)max(page[i], 0) * H + h;
+          ks[i] = page[i] >= 0 ? __ldg(a.c.ks + s) : 0.f;
+          vs[i] = page[i] >= 0 ? __ldg(a.c.vs + s) : 1.f;
+        }
+      }
+      const int src = batch & 31;
+      const float kh[2] = {__shfl_sync(FULL, ks[0], src), __shfl_sync(FULL, ks[1], src)};
+      float vh[2] = {__shfl_sync(FULL, vs[0], src), __shfl_sync(FULL, vs[1], src)};
+      const bool ok[2] = {__shfl_sync(FULL, page[0], src) >= 0, __shfl_sync(FULL, page[1], src) >= 0};
+      if (!ok[0]) vh[0] = vh[1];
+      if (!ok[1]) vh[1] = vh[0];
+      if (!seen(j)) continue;
+      const int x0 = job.tile(j) * KV_TILE;
+      const uint32_t slot = drained % S, kt = ring + slot * 2 * HALF, vt = kt + HALF;
+      if (!bar_wait(bar0 + 8 * slot, (drained / S) & 1)) bits |= SGD_KV_ERR_WAIT;
+      // ---- s = q . k: rows g, g + 8; tokens 8 nt + 2 c, + 1
+      float s[MT][4][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+      for (int ch = 0; ch < D / 64; ++ch) {
+        uint4 kw[4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          const int t = nt * 8 + g;
+          if (D == 128)
+            kw[nt] = lds128(kt + t * 128 + (((2 * c + ch) ^ (t & 7)) << 4));
+          else
+            kw[nt] = lds128(kt + (t >> 1) * 128 + ((((t & 1) * 4 + c) ^ ((t >> 1) & 7)) << 4));
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t qa[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint4 v = lds128(q_at + ((mt * KS + ch * 4 + q4) * 32 + lane) * 16);
+            qa[mt][0] = v.x;
+            qa[mt][1] = v.y;
+            qa[mt][2] = v.z;
+            qa[mt][3] = v.w;
+          }
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const uint32_t w = q4 == 0 ? kw[nt].x : q4 == 1 ? kw[nt].y : q4 == 2 ? kw[nt].z : kw[nt].w;
+            const uint32_t b0 = e4m3x2_to_f16x2(w & 0xffff), b1 = e4m3x2_to_f16x2(w >> 16);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              if (mt == 0 || mt * 16 < nrows) mma(s[mt][nt], qa[mt], b0, b1);
+          }
+        }
+      }
+      // ---- masks, maxima, probabilities
+      const bool edge = x0 + KV_TILE - 1 > p_first || !ok[0] || !ok[1] ||
+                        (a.window > 0 && x0 <= p_last - a.window && x0 + KV_TILE > a.sinks);
+      uint32_t pa[MT][2][4];
+      float scale_o[MT][2];
+      // the value scale of o's units follows the blocks' where they differ by
+      // more than 2^4: probabilities keep f16's bits
+      const bool two = vh[1] > 16.f * vh[0] || vh[1] < 0.0625f * vh[0];
+      float ratio = 1.f;
+      if (vh[0] > 16.f * unit || vh[0] < 0.0625f * unit) {
+        ratio = unit / vh[0];
+        unit = vh[0];
+      }
+      const float vr[2] = {vh[0] / unit, two ? 1.f : vh[1] / unit};
+      bool rescale = ratio != 1.f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float z = s[mt][nt][e] * (f[mt][e >> 1] * kh[nt >> 1]);
+            if (edge) {
+              const int x = x0 + nt * 8 + 2 * c + (e & 1), p = pos[mt][e >> 1];
+              const bool vis = x <= p && ok[nt >> 1] && (a.window == 0 || x > p - a.window || x < a.sinks);
+              z = vis ? z : -CUDART_INF_F;
+            }
+            s[mt][nt][e] = z;
+            top[e >> 1] = fmaxf(top[e >> 1], z);
+          }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 1));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 2));
+          scale_o[mt][x] = ratio;
+          if (top[x] > m[mt][x] + LAZY || (m[mt][x] == -CUDART_INF_F && top[x] > m[mt][x])) {
+            const float k = m[mt][x] == -CUDART_INF_F ? 0.f : ex2_approx(m[mt][x] - top[x]);
+            l[mt][x] *= k;
+            scale_o[mt][x] *= k;
+            m[mt][x] = top[x];
+            rescale = true;
+          }
+        }
+      }
+      if (__any_sync(FULL, rescale)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2 * NJ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][n][e] *= scale_o[mt][e >> 1];
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float p[4][4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float base = m[mt][e >> 1] == -CUDART_INF_F ? 0.f : m[mt][e >> 1];
+            const float w = ex2_approx(s[mt][nt][e] - base);
+            l[mt][e >> 1] += w;
+            p[nt][e] = w * vr[nt >> 1];
+          }
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc) {
+          pa[mt][kc][0] = pack2<__half>(p[2 * kc][0], p[2 * kc][1]);
+          pa[mt][kc][1] = pack2<__half>(p[2 * kc][2], p[2 * kc][3]);
+          pa[mt][kc][2] = pack2<__half>(p[2 * kc + 1][0], p[2 * kc + 1][1]);
+          pa[mt][kc][3] = pack2<__half>(p[2 * kc + 1][2], p[2 * kc + 1][3]);
+        }
+      }
+      // ---- o += p v: dims 16 j + 4 c .. + 3 of rows g, g + 8.  Slots that no
+      // token has reached may hold anything, NaN among it: they count as 0.
+      const bool tail = x0 + KV_TILE > job.n || !ok[0] || !ok[1];
+      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+      if (tail) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = x0 + i * 8 + 2 * c;
+          keep[i] = !ok[i >> 1] ? 0u : (x < job.n ? 0x0000ffffu : 0u) | (x + 1 < job.n ? 0xffff0000u : 0u);
+        }
+      }
+      auto add = [&](auto lo, auto hi) {  // blocks of 16 tokens lo .. hi
+#pragma unroll
+        for (int jd = 0; jd < NJ; ++jd) {
+          const int t = (lane >> 3) * 8 + (lane & 7);
+          uint32_t w[4];
+          if (D == 128)
+            ldmatrix_x4_trans(w, vt + t * 128 + ((jd ^ (t & 7)) << 4));
+          else
+            ldmatrix_x4_trans(w, vt + (t >> 1) * 128 + ((((t & 1) * 4 + jd) ^ ((t >> 1) & 7)) << 4));
+#pragma unroll
+          for (int kc = decltype(lo)::value; kc < decltype(hi)::value; ++kc) {
+            uint32_t even[2], odd[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (tail) w[2 * kc + i] &= keep[2 * kc + i];
+              const uint32_t x = __byte_perm(w[2 * kc + i], 0, 0x3120);
+              even[i] = e4m3x2_to_f16x2(x & 0xffff);
+              odd[i] = e4m3x2_to_f16x2(x >> 16);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if (mt != 0 && mt * 16 >= nrows) continue;
+              mma(o[mt][2 * jd], pa[mt][kc], even[0], even[1]);
+              mma(o[mt][2 * jd + 1], pa[mt][kc], odd[0], odd[1]);
+            }
+          }
+        }
+      };
+      using std::integral_constant;
+      const integral_constant<int, 0> i0;
+      const integral_constant<int, 1> i1;
+      const integral_constant<int, 2> i2;
+      if (!two) {
+        add(i0, i2);
+      } else {  // (pages of 16 tokens whose value scales are far apart)
+        add(i0, i1);
+        const float k = unit / vh[1];
+        unit = vh[1];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2 * NJ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][n][e] *= k;
+        add(i1, i2);
+      }
+      ++drained;
+      __syncwarp();
+      advance();
+    }
+
+    // ---- the warps' parts together
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float t = l[mt][x];
+        t += __shfl_xor_sync(FULL, t, 1);
+        t += __shfl_xor_sync(FULL, t, 2);
+        const int r = mt * 16 + x * 8 + g;
+        if (c == 0) {
+          s_m[warp][r] = m[mt][x];
+          s_l[warp][r] = t;
+        }
+      }
+    __syncthreads();  // (every warp's ring is drained)
+    float *so = reinterpret_cast<float *>(smem) + warp * M * D;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = mt * 16 + x * 8 + g;
+        if (r < nrows) {
+#pragma unroll
+          for (int jd = 0; jd < NJ; ++jd)
+            *reinterpret_cast<float4 *>(so + r * D + jd * 16 + 4 * c) =
+                make_float4(o[mt][2 * jd][2 * x] * unit, o[mt][2 * jd + 1][2 * x] * unit,
+                            o[mt][2 * jd][2 * x + 1] * unit, o[mt][2 * jd + 1][2 * x + 1] * unit);
+        }
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == job.tiles;
+    T *out = static_cast<T *>(a.out);
+    const bool starts = t0 == 0;
+    float *part = part_of<M, D>(a, 2 * blockIdx.x + (starts ? 1 : 0));
+    const float *all = reinterpret_cast<const float *>(smem);
+    for (int i = tid; i < nrows * (D / 4); i += THREADS) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float top = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_m[w][r]);
+      const float base = top == -CUDART_INF_F ? 0.f : top;
+      float sum = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float k = ex2_approx(s_m[w][r] - base);
+        const float4 v = *reinterpret_cast<const float4 *>(all + (w * M + r) * D + d);
+        if (s_l[w][r] != 0.f) {
+          sum += s_l[w][r] * k;
+          x.x += v.x * k;
+          x.y += v.y * k;
+          x.z += v.z * k;
+          x.w += v.w * k;
+        }
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int row = r0 + r;
+        T *dst = out + ((long long)(job.q0 + row / a.group) * a.q_heads + h * a.group + row % a.group) * D + d;
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
+      } else {
+        *reinterpret_cast<float4 *>(part + r * D + d) = x;
+        if (d == 0) {
+          part[M * D + r] = top;
+          part[M * D + M + r] = sum;
+        }
+      }
+    }
+    if (!whole) {
+      // ---- the unit's parts together, by the CTA that is last
+      const int g0 = kv_cta_of(share.total, share.ctas, u_begin);
+      const int g1 = kv_cta_of(share.total, share.ctas, u_end - 1);
+      unsigned *count = reinterpret_cast<unsigned *>(a.work) + g0;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(count, 1) == (unsigned)(g1 - g0);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        if (tid == 0) *count = 0;
+        for (int i = tid; i < nrows * (D / 4); i += THREADS) {
+          const int r = i / (D / 4), d = i % (D / 4) * 4;
+          float top = -CUDART_INF_F;
+          for (int p = g0; p <= g1; ++p)
+            top = fmaxf(top, __ldcg(part_of<M, D>(a, 2 * p + (p == g0 ? 1 : 0)) + M * D + r));
+          const float base = top == -CUDART_INF_F ? 0.f : top;
+          float sum = 0.f;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p = g0; p <= g1; ++p) {
+            const float *from = part_of<M, D>(a, 2 * p + (p == g0 ? 1 : 0));
+            const float k = ex2_approx(__ldcg(from + M * D + r) - base), ll = __ldcg(from + M * D + M + r);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + r * D + d));
+            if (ll != 0.f) {
+              sum += ll * k;
+              x.x += v.x * k;
+              x.y += v.y * k;
+              x.z += v.z * k;
+              x.w += v.w * k;
+            }
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int row = r0 + r;
+          T *dst = out + ((long long)(job.q0 + row / a.group) * a.q_heads + h * a.group + row % a.group) * D + d;
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
+        }
+      }
+    }
+    // (generic reads and writes of the ring's memory come before the next copies into it)
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
   }
+  if (bits) atomicOr(a.err, bits);
+}
+
+// ---- host --------------------------------------------------------------------
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                 CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return (EncodeTiled) nullptr;
+    }
+    return (EncodeTiled)p;
+  }();
+  return fn;
+}
+
+// Keys or values as lines of 128 bytes (one token, or two of 64 bytes), in
+// boxes of `tokens`, with the 128-byte swizzle.
+bool make_map(CUtensorMap *map, const KvView &c, void *base, int tokens) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t lines = (cuuint64_t)c.num_pages * c.heads * c.page * c.dim / 128;
+  const cuuint64_t dims[2] = {128, lines}, strides[1] = {128};
+  const cuuint32_t box[2] = {128, (cuuint32_t)(tokens * c.dim / 128)}, step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int MT, int S>
+constexpr int few_smem() {
+  return 1024 + WARPS * S * 2 * KV_TILE * D + MT * D / 16 * 512;
+}
+
+template <typename T, int D, int MT, int S, int PER_SM>
+cudaError_t launch_few(const KvAttendArgs &a, cudaStream_t st) {
+  CUtensorMap k, v;
+  const int tokens = a.c.page < KV_TILE ? a.c.page : KV_TILE;
+  if (!make_map(&k, a.c, a.c.k, tokens) || !make_map(&v, a.c, a.c.v, tokens)) return cudaErrorInvalidValue;
+  attend_few_kernel<T, D, MT, S><<<a.sms * PER_SM, THREADS, few_smem<D, MT, S>(), st>>>(a, k, v);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int MT, int S>
+cudaError_t limit_few() {
+  return cudaFuncSetAttribute(attend_few_kernel<T, D, MT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              few_smem<D, MT, S>());
+}
+
+template <typename T>
+cudaError_t limits() {
+  cudaError_t e = limit_few<T, 128, 1, 2>();
+  if (e == cudaSuccess) e = limit_few<T, 128, 2, 3>();
+  if (e == cudaSuccess) e = limit_few<T, 64, 1, 4>();
+  if (e == cudaSuccess) e = limit_few<T, 64, 2, 6>();
+  return e;
+}
+
+template <typename T>
+cudaError_t attend(const KvAttendArgs &a, cudaStream_t st) {
+  const bool one = (long long)a.max_q * a.group <= 16;
+  if (a.c.dim == 128) return one ? launch_few<T, 128, 1, 2, 3>(a, st) : launch_few<T, 128, 2, 3, 2>(a, st);
+  return one ? launch_few<T, 64, 1, 4, 3>(a, st) : launch_few<T, 64, 2, 6, 2>(a, st);
 }
 
 }  // namespace
 
-size_t kv_attend_workspace(const sgd_kv_config &) { return 256; }
+size_t kv_attend_workspace() {
+  return (size_t)MAX_CTAS * 8 + (size_t)MAX_CTAS * 2 * 32 * (128 + 2) * 4;
+}
 
-cudaError_t kv_attend_set_limits() { return cudaSuccess; }
+cudaError_t kv_attend_set_limits() {
+  cudaError_t e = limits<__half>();
+  if (e == cudaSuccess) e = limits<__nv_bfloat16>();
+  return e;
+}
 
 cudaError_t launch_kv_attend(KvAttendArgs a, int dtype, cudaStream_t st, int *launches) {
-  const dim3 grid(a.r.N, a.q_heads);
-  if (dtype == SGD_F16)
-    kv_attend_kernel<__half><<<grid, THREADS, 0, st>>>(a);
-  else
-    kv_attend_kernel<__nv_bfloat16><<<grid, THREADS, 0, st>>>(a);
+  if (a.sms > MAX_CTAS / 3) a.sms = MAX_CTAS / 3;
   *launches = 1;
-  return cudaGetLastError();
+  return dtype == SGD_F16 ? attend<__half>(a, st) : attend<__nv_bfloat16>(a, st);
 }
 
 }  // namespace sgd

@@ -53,13 +53,14 @@ struct KvAttendArgs {
   int max_q;
   float scale;
   int window, sinks;
+  int sms;              // SMs of the device
   unsigned char *work;  // kv_attend_workspace bytes, 0 at creation
   uint32_t *err;
 };
 
 cudaError_t launch_kv_write(KvWriteArgs a, int dtype, cudaStream_t st);
 cudaError_t launch_kv_read(KvReadArgs a, int dtype, cudaStream_t st);
-size_t kv_attend_workspace(const sgd_kv_config &c);
+size_t kv_attend_workspace();
 cudaError_t kv_attend_set_limits();
 cudaError_t launch_kv_attend(KvAttendArgs a, int dtype, cudaStream_t st, int *launches);
 

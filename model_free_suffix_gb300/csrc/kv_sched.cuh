@@ -1,0 +1,134 @@
+// kv_sched.cuh -- how the attention's work is cut: rows, units, tiles, shares.
+//
+// A unit is up to M rows (new token, query head of the group) of one batch row
+// and one head of keys and values; its work is the list of key tiles that the
+// batch row's new tokens see.  All tiles of all units, one after the other, are
+// cut into equal shares, one per CTA, wherever the cut falls: rows of very
+// unequal length keep every SM busy to the end.  A unit that a cut goes through
+// is joined from its parts by the CTA that finishes last, in the order of the
+// parts, so that the result does not depend on which CTA that is.
+#pragma once
+
+#include "kv_internal.h"
+#include "sgd_internal.h"
+
+namespace sgd {
+
+constexpr int KV_TILE = 32;  // tokens
+
+// What one batch row asks for.
+struct KvJob {
+  int q0, ql, n;       // first packed token, new tokens, cached tokens
+  int sink_tiles;      // tiles of first tokens before the others
+  int lo_tile, tiles;  // the others start at lo_tile; all tiles
+  int units;           // of one head
+
+  // the token tile of the j-th tile of the list
+  __device__ __forceinline__ int tile(int j) const { return j < sink_tiles ? j : lo_tile + j - sink_tiles; }
+};
+
+__device__ __forceinline__ KvJob kv_job(const KvAttendArgs &a, int b, int M, uint32_t *bits) {
+  KvJob r;
+  const int q0 = __ldg(a.r.q_start + b), q1 = __ldg(a.r.q_start + b + 1);
+  r.n = __ldg(a.r.seq_lens + b);
+  r.q0 = q0;
+  r.ql = q1 - q0;
+  if (q0 < 0 || q1 > a.r.N || r.ql < 0) {
+    *bits |= SGD_KV_ERR_LENGTH;
+    r.ql = 0;
+  }
+  r.units = (int)(((long long)r.ql * a.group + M - 1) / M);
+  r.sink_tiles = r.lo_tile = 0;
+  if (r.ql > 0 && (r.n < r.ql || (long long)r.n > (long long)a.r.max_pages * a.c.page)) {
+    *bits |= SGD_KV_ERR_LENGTH;  // sees nothing: one tile, which no token sees
+    r.n = 0;
+    r.tiles = 1;
+    return r;
+  }
+  const int first = r.n - r.ql;  // position of the first new token
+  int lo = 0;
+  if (a.window > 0) lo = max(0, first - a.window + 1);
+  r.lo_tile = lo / KV_TILE;
+  r.sink_tiles = min((int)(((long long)min(a.sinks, r.n) + KV_TILE - 1) / KV_TILE), r.lo_tile);
+  r.tiles = r.sink_tiles + (r.n + KV_TILE - 1) / KV_TILE - r.lo_tile;
+  return r;
+}
+
+__device__ __forceinline__ long long kv_work(const KvJob &j, int heads) {
+  return (long long)j.units * heads * j.tiles;
+}
+
+// A CTA's share [begin, end) of the work, and the batch row where it begins.
+struct KvShare {
+  long long begin, end, total;
+  long long per;        // shares are [g * total / ctas, (g + 1) * total / ctas)
+  int ctas;
+  int b;                // batch row of `begin`
+  long long b_begin;    // the work before row b
+};
+
+__device__ __forceinline__ long long kv_cut(long long total, int ctas, int g) { return total * g / ctas; }
+
+// The CTA whose share holds `at`.
+__device__ __forceinline__ int kv_cta_of(long long total, int ctas, long long at) {
+  int g = (int)(at * ctas / total);
+  while (g + 1 < ctas && kv_cut(total, ctas, g + 1) <= at) ++g;
+  while (g > 0 && kv_cut(total, ctas, g) > at) --g;
+  return g;
+}
+
+// By all threads of the block.  `least`: tiles that make a share worth a CTA.
+template <int THREADS>
+__device__ KvShare kv_share(const KvAttendArgs &a, int M, int least, uint32_t *bits) {
+  __shared__ long long s_warp[THREADS / 32];
+  __shared__ long long s_before;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.r.B + THREADS - 1) / THREADS;
+  const int b0 = min(a.r.B, tid * per), b1 = min(a.r.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += kv_work(kv_job(a, b, M, bits), a.c.heads);
+  long long scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(FULL, scan, o);
+    if (lane >= o) scan += t;
+  }
+  if (lane == 31) s_warp[warp] = scan;
+  __syncthreads();
+  long long before = scan - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  KvShare s;
+  s.total = total;
+  const long long most = (total + least - 1) / least;
+  s.ctas = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
+  const int g = blockIdx.x;
+  if (g >= s.ctas) {
+    s.begin = s.end = 0;
+    s.b = a.r.B;
+    return s;
+  }
+  s.begin = kv_cut(total, s.ctas, g);
+  s.end = kv_cut(total, s.ctas, g + 1);
+  if (before <= s.begin && s.begin < before + mine) {
+    for (int b = b0; b < b1; ++b) {
+      const long long w = kv_work(kv_job(a, b, M, bits), a.c.heads);
+      if (s.begin < before + w) {
+        s_b = b;
+        s_before = before;
+        break;
+      }
+      before += w;
+    }
+  }
+  __syncthreads();
+  s.b = s_b;
+  s.b_begin = s_before;
+  return s;
+}
+
+}  // namespace sgd
