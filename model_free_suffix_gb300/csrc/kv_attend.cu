@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
     bar_init_fence();
   }
   __syncwarp();
-  uint32_t filled = 0, drained = 0;  // tiles of this warp loaded and consumed
+  uint32_t in_slot = 0, out_slot = 0, parity = 0;  // of the ring: to load, to consume
 
   const int P = a.c.page, H = a.c.heads;
   const int halves = P < KV_TILE ? 2 : 1;  // pages of a tile
@@ -126,67 +126,59 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
     const int p_last = job.n - job.ql + (r0 + nrows - 1) / a.group;
     const int32_t *table = a.r.table + (long long)b * a.r.max_pages;
 
-    // ---- this warp's tiles: t0 + warp, + WARPS, ...; those that no row of the
-    // unit sees are passed over
+    // ---- this warp's tiles, t0 + warp, + WARPS, ..., 32 at a time: lane i holds
+    // what the i-th of them needs.  Those that no row of the unit sees are
+    // passed over.
+    struct Ahead {
+      int y[2];   // lines of the tile's page(s) in the maps
+      bool on;    // some row sees it
+    };
+    auto page_of = [&](int x, int i) {  // of the tile at position x, its i-th page
+      const int block = x / P + i;
+      if (block >= a.r.max_pages || block * P >= job.n) return -1;
+      const int pg = __ldg(table + block);
+      if (pg >= 0 && pg < a.c.num_pages) return pg;
+      bits |= SGD_KV_ERR_PAGE;
+      return -1;
+    };
     auto seen = [&](int j) {
+      if (j >= t1) return false;
       const int x = job.tile(j) * KV_TILE;
-      if (x > p_last) return false;
-      return a.window == 0 || x + KV_TILE - 1 > p_first - a.window || x < a.sinks;
+      return x <= p_last && (a.window == 0 || x + KV_TILE - 1 > p_first - a.window || x < a.sinks);
     };
-    // lane i holds what the i-th of the next 32 needs
-    int page[2], ahead_page[2];
-    float ks[2], vs[2];
-    auto look = [&](int j0, int (&pg)[2]) {
-      const int j = j0 + WARPS * lane;
-      pg[0] = pg[1] = -1;
-      if (j >= t1 || job.n == 0) return;
-      const int x = job.tile(j) * KV_TILE;
-      for (int i = 0; i < halves; ++i) {
-        const int block = x / P + i;
-        if (block < a.r.max_pages && block * P < job.n) {
-          pg[i] = __ldg(table + block);
-          if (pg[i] < 0 || pg[i] >= a.c.num_pages) {
-            pg[i] = -1;
-            bits |= SGD_KV_ERR_PAGE;
-          }
-        }
+    constexpr int PACK = 128 / D;  // tokens of a 128-byte line
+    auto look = [&](int j, Ahead &w) {
+      w.on = seen(j);
+      w.y[0] = w.y[1] = 0;
+      if (w.on) {
+        const int x = job.tile(j) * KV_TILE;
+        w.y[0] = ((max(page_of(x, 0), 0) * H + h) * P + (x & (P - 1))) / PACK;
+        if (halves == 2) w.y[1] = (max(page_of(x, 1), 0) * H + h) * P / PACK;
       }
-      if (halves == 1) pg[1] = pg[0];
+      return __ballot_sync(FULL, w.on);
     };
-    auto load = [&](int j, int p0, int p1) {  // by one lane
-      const uint32_t slot = filled % S;
-      const uint32_t dst = ring + slot * 2 * HALF, bar = bar0 + 8 * slot;
-      constexpr int PACK = 128 / D;  // tokens of a 128-byte line
-      bar_expect(bar, 2 * HALF);
-      const int x = job.tile(j) * KV_TILE;
-      if (halves == 1) {
-        const int y = ((max(p0, 0) * H + h) * P + x % P) / PACK;
-        tma_load_2d(dst, &kmap, 0, y, bar);
-        tma_load_2d(dst + HALF, &vmap, 0, y, bar);
-      } else {
-        const int y0 = (max(p0, 0) * H + h) * P / PACK, y1 = (max(p1, 0) * H + h) * P / PACK;
-        tma_load_2d(dst, &kmap, 0, y0, bar);
-        tma_load_2d(dst + HALF / 2, &kmap, 0, y1, bar);
-        tma_load_2d(dst + HALF, &vmap, 0, y0, bar);
-        tma_load_2d(dst + HALF + HALF / 2, &vmap, 0, y1, bar);
-      }
-    };
-    int next = t0 + warp, next_i = 0;  // the next tile to load, its lane in ahead_page
-    look(next, ahead_page);
+    Ahead ahead;
+    int next = t0 + warp;  // the first tile of the batch being loaded
+    uint32_t to_load = look(next + WARPS * lane, ahead);
     auto advance = [&]() {  // loads the next tile that is seen, if any
-      while (next < t1) {
-        const int j = next, i = next_i;
-        const int p0 = __shfl_sync(FULL, ahead_page[0], i), p1 = __shfl_sync(FULL, ahead_page[1], i);
-        next += WARPS;
-        if (++next_i == 32) {
-          next_i = 0;
-          look(next, ahead_page);
-        }
-        if (!seen(j)) continue;
-        if (lane == 0) load(j, p0, p1);
-        ++filled;
-        return;
+      while (to_load == 0) {
+        next += 32 * WARPS;
+        if (next >= t1) return;
+        to_load = look(next + WARPS * lane, ahead);
       }
+      const int i = __ffs(to_load) - 1;
+      to_load &= to_load - 1;
+      if (lane == i) {
+        const uint32_t dst = ring + in_slot * 2 * HALF, bar = bar0 + 8 * in_slot;
+        bar_expect(bar, 2 * HALF);
+        tma_load_2d(dst, &kmap, 0, ahead.y[0], bar);
+        tma_load_2d(dst + HALF, &vmap, 0, ahead.y[0], bar);
+        if (halves == 2) {
+          tma_load_2d(dst + HALF / 2, &kmap, 0, ahead.y[1], bar);
+          tma_load_2d(dst + HALF + HALF / 2, &vmap, 0, ahead.y[1], bar);
+        }
+      }
+      in_slot = in_slot + 1 == S ? 0 : in_slot + 1;
     };
     for (int i = 0; i < S; ++i) advance();
 
@@ -242,27 +234,33 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
         for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
     }
 
-    int batch = 0;
-    for (int j = t0 + warp; j < t1; j += WARPS, ++batch) {
-      if ((batch & 31) == 0) {
-        look(j, page);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const long long s = (long long)max(page[i], 0) * H + h;
-          ks[i] = page[i] >= 0 ? __ldg(a.c.ks + s) : 0.f;
-          vs[i] = page[i] >= 0 ? __ldg(a.c.vs + s) : 1.f;
+    for (int j0 = t0 + warp; j0 < t1; j0 += 32 * WARPS) {
+    float ks[2] = {0.f, 0.f}, vs[2] = {1.f, 1.f};  // (a scale of 0: no such page)
+    bool on = seen(j0 + WARPS * lane);
+    if (on) {
+      const int x = job.tile(j0 + WARPS * lane) * KV_TILE;
+      for (int i = 0; i < halves; ++i) {
+        const int pg = page_of(x, i);
+        if (pg >= 0) {
+          ks[i] = __ldg(a.c.ks + (long long)pg * H + h);
+          vs[i] = __ldg(a.c.vs + (long long)pg * H + h);
         }
       }
-      const int src = batch & 31;
+      if (halves == 1) {
+        ks[1] = ks[0];
+        vs[1] = vs[0];
+      } else {
+        if (ks[0] == 0.f) vs[0] = vs[1];
+        if (ks[1] == 0.f) vs[1] = vs[0];
+      }
+    }
+    for (uint32_t todo = __ballot_sync(FULL, on); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int x0 = job.tile(j0 + WARPS * src) * KV_TILE;
       const float kh[2] = {__shfl_sync(FULL, ks[0], src), __shfl_sync(FULL, ks[1], src)};
-      float vh[2] = {__shfl_sync(FULL, vs[0], src), __shfl_sync(FULL, vs[1], src)};
-      const bool ok[2] = {__shfl_sync(FULL, page[0], src) >= 0, __shfl_sync(FULL, page[1], src) >= 0};
-      if (!ok[0]) vh[0] = vh[1];
-      if (!ok[1]) vh[1] = vh[0];
-      if (!seen(j)) continue;
-      const int x0 = job.tile(j) * KV_TILE;
-      const uint32_t slot = drained % S, kt = ring + slot * 2 * HALF, vt = kt + HALF;
-      if (!bar_wait(bar0 + 8 * slot, (drained / S) & 1)) bits |= SGD_KV_ERR_WAIT;
+      const float vh[2] = {__shfl_sync(FULL, vs[0], src), __shfl_sync(FULL, vs[1], src)};
+      const uint32_t kt = ring + out_slot * 2 * HALF, vt = kt + HALF;
+      if (!bar_wait(bar0 + 8 * out_slot, parity)) bits |= SGD_KV_ERR_WAIT;
       // ---- s = q . k: rows g, g + 8; tokens 8 nt + 2 c, + 1
       float s[MT][4][4];
 #pragma unroll
@@ -296,7 +294,8 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) {
             const uint32_t w = q4 == 0 ? kw[nt].x : q4 == 1 ? kw[nt].y : q4 == 2 ? kw[nt].z : kw[nt].w;
-            const uint32_t b0 = e4m3x2_to_f16x2(w & 0xffff), b1 = e4m3x2_to_f16x2(w >> 16);
+            uint32_t b0, b1;
+            e4m3x4_to_f16x4(w, b0, b1);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
               if (mt == 0 || mt * 16 < nrows) mma(s[mt][nt], qa[mt], b0, b1);
@@ -304,7 +303,8 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
         }
       }
       // ---- masks, maxima, probabilities
-      const bool edge = x0 + KV_TILE - 1 > p_first || !ok[0] || !ok[1] ||
+      const bool missing = kh[0] == 0.f || kh[1] == 0.f;
+      const bool edge = missing || x0 + KV_TILE - 1 > p_first ||
                         (a.window > 0 && x0 <= p_last - a.window && x0 + KV_TILE > a.sinks);
       uint32_t pa[MT][2][4];
       float scale_o[MT][2];
@@ -321,19 +321,25 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+        const float fk[2][2] = {{f[mt][0] * kh[0], f[mt][0] * kh[1]}, {f[mt][1] * kh[0], f[mt][1] * kh[1]}};
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float z = s[mt][nt][e] * (f[mt][e >> 1] * kh[nt >> 1]);
-            if (edge) {
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] *= fk[e >> 1][nt >> 1];
+        if (edge) {
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
               const int x = x0 + nt * 8 + 2 * c + (e & 1), p = pos[mt][e >> 1];
-              const bool vis = x <= p && ok[nt >> 1] && (a.window == 0 || x > p - a.window || x < a.sinks);
-              z = vis ? z : -CUDART_INF_F;
+              const bool vis = x <= p && kh[nt >> 1] != 0.f && (a.window == 0 || x > p - a.window || x < a.sinks);
+              if (!vis) s[mt][nt][e] = -CUDART_INF_F;
             }
-            s[mt][nt][e] = z;
-            top[e >> 1] = fmaxf(top[e >> 1], z);
-          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[mt][nt][e]);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 1));
@@ -359,12 +365,13 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float p[4][4];
+        const float base[2] = {m[mt][0] == -CUDART_INF_F ? 0.f : m[mt][0],
+                               m[mt][1] == -CUDART_INF_F ? 0.f : m[mt][1]};
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float base = m[mt][e >> 1] == -CUDART_INF_F ? 0.f : m[mt][e >> 1];
-            const float w = ex2_approx(s[mt][nt][e] - base);
+            const float w = ex2_approx(s[mt][nt][e] - base[e >> 1]);
             l[mt][e >> 1] += w;
             p[nt][e] = w * vr[nt >> 1];
           }
@@ -378,14 +385,19 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
       }
       // ---- o += p v: dims 16 j + 4 c .. + 3 of rows g, g + 8.  Slots that no
       // token has reached may hold anything, NaN among it: they count as 0.
-      const bool tail = x0 + KV_TILE > job.n || !ok[0] || !ok[1];
-      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-      if (tail) {
+      if (missing || x0 + KV_TILE > job.n) {
+        __syncwarp();
+        const bool gone = (lane < 16 ? kh[0] : kh[1]) == 0.f || x0 + lane >= job.n;
+        if (gone) {
+          const uint32_t line = D == 128 ? vt + lane * 128 : vt + (lane >> 1) * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = x0 + i * 8 + 2 * c;
-          keep[i] = !ok[i >> 1] ? 0u : (x < job.n ? 0x0000ffffu : 0u) | (x + 1 < job.n ? 0xffff0000u : 0u);
+          for (int ch = 0; ch < D / 16; ++ch) {
+            const int at16 = D == 128 ? ch : (((lane & 1) * 4 + ch) ^ ((lane >> 1) & 7));
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(line + at16 * 16), "r"(0) : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        __syncwarp();
       }
       auto add = [&](auto lo, auto hi) {  // blocks of 16 tokens lo .. hi
 #pragma unroll
@@ -401,10 +413,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
             uint32_t even[2], odd[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (tail) w[2 * kc + i] &= keep[2 * kc + i];
-              const uint32_t x = __byte_perm(w[2 * kc + i], 0, 0x3120);
-              even[i] = e4m3x2_to_f16x2(x & 0xffff);
-              odd[i] = e4m3x2_to_f16x2(x >> 16);
+              e4m3x4_to_f16x4(__byte_perm(w[2 * kc + i], 0, 0x3120), even[i], odd[i]);
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -433,9 +442,11 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
             for (int e = 0; e < 4; ++e) o[mt][n][e] *= k;
         add(i1, i2);
       }
-      ++drained;
+      out_slot = out_slot + 1 == S ? 0 : out_slot + 1;
+      parity ^= out_slot == 0;
       __syncwarp();
       advance();
+    }
     }
 
     // ---- the warps' parts together
@@ -516,29 +527,48 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
       if (tid == 0) s_last = atomicAdd(count, 1) == (unsigned)(g1 - g0);
       __syncthreads();
       if (s_last) {
+        // the parts' weights 2^(m - max) / l first, all loads in flight at once
         __threadfence();
         if (tid == 0) *count = 0;
+        const int parts = g1 - g0 + 1;
+        float *w_m = reinterpret_cast<float *>(smem), *w_l = w_m + parts * M;
+        auto slot = [&](int p) { return part_of<M, D>(a, 2 * (g0 + p) + (p == 0 ? 1 : 0)); };
+        for (int i = tid; i < parts * M; i += THREADS) {
+          const float *from = slot(i / M) + M * D + i % M;
+          const bool on = i % M < nrows;
+          w_m[i] = on ? __ldcg(from) : -CUDART_INF_F;
+          w_l[i] = on ? __ldcg(from + M) : 0.f;
+        }
+        __syncthreads();
+        for (int r = warp; r < nrows; r += WARPS) {
+          float top = -CUDART_INF_F, sum = 0.f;
+          for (int p = lane; p < parts; p += 32) top = fmaxf(top, w_m[p * M + r]);
+#pragma unroll
+          for (int o2 = 16; o2; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o2));
+          const float base = top == -CUDART_INF_F ? 0.f : top;
+          for (int p = lane; p < parts; p += 32) {
+            const float k = ex2_approx(w_m[p * M + r] - base);
+            w_m[p * M + r] = k;
+            if (w_l[p * M + r] != 0.f) sum += w_l[p * M + r] * k;
+          }
+#pragma unroll
+          for (int o2 = 16; o2; o2 >>= 1) sum += __shfl_xor_sync(FULL, sum, o2);
+          if (lane == 0) s_f[r] = sum == 0.f ? 0.f : 1.f / sum;
+        }
+        __syncthreads();
         for (int i = tid; i < nrows * (D / 4); i += THREADS) {
           const int r = i / (D / 4), d = i % (D / 4) * 4;
-          float top = -CUDART_INF_F;
-          for (int p = g0; p <= g1; ++p)
-            top = fmaxf(top, __ldcg(part_of<M, D>(a, 2 * p + (p == g0 ? 1 : 0)) + M * D + r));
-          const float base = top == -CUDART_INF_F ? 0.f : top;
-          float sum = 0.f;
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p = g0; p <= g1; ++p) {
-            const float *from = part_of<M, D>(a, 2 * p + (p == g0 ? 1 : 0));
-            const float k = ex2_approx(__ldcg(from + M * D + r) - base), ll = __ldcg(from + M * D + M + r);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + r * D + d));
-            if (ll != 0.f) {
-              sum += ll * k;
-              x.x += v.x * k;
-              x.y += v.y * k;
-              x.z += v.z * k;
-              x.w += v.w * k;
-            }
+#pragma unroll 8
+          for (int p = 0; p < parts; ++p) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot(p) + r * D + d));
+            const float k = w_m[p * M + r];
+            x.x += v.x * k;
+            x.y += v.y * k;
+            x.z += v.z * k;
+            x.w += v.w * k;
           }
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const float inv = s_f[r];
           const int row = r0 + r;
           T *dst = out + ((long long)(job.q0 + row / a.group) * a.q_heads + h * a.group + row % a.group) * D + d;
           *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
