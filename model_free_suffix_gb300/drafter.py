@@ -31,12 +31,15 @@ def _rational(x: Rational, denom: int = 10 ** 6) -> Tuple[int, int]:
     return f.numerator, f.denominator
 
 
-def _stream_handle(stream) -> ctypes.c_void_p:
+# (the current stream's handle, without the Stream object that
+# torch.cuda.current_stream() makes first)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_handle(stream, index: Optional[int] = None) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _raw_stream(torch.cuda.current_device() if index is None else index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 @dataclass
@@ -109,6 +112,7 @@ class SuffixDrafter:
         cfg.gram_drafts = gram_drafts
         self.cfg = cfg
         self.device = torch.device("cuda", device)
+        self._index = device
         torch.cuda.init()
         with torch.cuda.device(self.device):
             torch.zeros(1, device=self.device)  # make the primary context current
@@ -127,14 +131,14 @@ class SuffixDrafter:
             raise L.SgdError(status, where)
         return status
 
-    def _t(self, t: Optional[torch.Tensor], dtype=torch.int32, name="tensor") -> ctypes.c_void_p:
+    def _t(self, t: Optional[torch.Tensor], dtype=torch.int32, name="tensor") -> Optional[int]:
         if t is None:
-            return ctypes.c_void_p(0)
-        if t.device != self.device:
+            return None
+        if t.get_device() != self._index:  # (-1 for a host tensor)
             raise ValueError("%s must be on %s" % (name, self.device))
-        if t.dtype != dtype or not t.is_contiguous():
+        if t.dtype is not dtype or not t.is_contiguous():
             raise ValueError("%s must be a contiguous %s tensor" % (name, dtype))
-        return ctypes.c_void_p(t.data_ptr())
+        return t.data_ptr()
 
     @staticmethod
     def _host(t: Optional[torch.Tensor], dtype=torch.int32, name="tensor") -> ctypes.c_void_p:
@@ -276,42 +280,55 @@ class SuffixDrafter:
         numbers; draft_probs [rows, V] float32 are the probabilities the drafts
         were drawn from (None: proposed outright, as by this drafter).
         temperature [B] float32 (None: 1; below 1e-5: greedy)."""
-        B = num_valid.shape[0]
-        if logits.dtype not in _DTYPES or logits.dim() != 2:
-            raise ValueError("logits must be a [rows, V] tensor of float32, float16 or bfloat16")
-        if logits.shape[1] != self.V or noise.shape != (B, self.V) or uniform.shape != (B, self.k) \
-                or drafts.shape != (B, self.k):
+        B, (rows, V) = num_valid.shape[0], self._pair(logits, "logits")
+        dtype = _DTYPES.get(logits.dtype)
+        if dtype is None:
+            raise ValueError("logits must be float32, float16 or bfloat16")
+        if V != self.V or self._pair(noise, "noise") != (B, V) or self._pair(uniform, "uniform") != (B, self.k) \
+                or self._pair(drafts, "drafts") != (B, self.k):
             raise ValueError("logits [rows, V], noise [B, V], uniform [B, k] and drafts [B, k] must "
                              "agree with the context's V = %d and k = %d" % (self.V, self.k))
-        if draft_probs is not None and draft_probs.shape != logits.shape:
-            raise ValueError("draft_probs must have the shape of logits")
-        for t, n in ((row_start, "row_start"), (temperature, "temperature"), (active, "active")):
-            if t is not None and t.shape[0] < B:
-                raise ValueError("%s must have an entry per row" % n)
-        out = out or self.new_verdict(B)
-        self._check(self._lib.sgd_verify(
-            self._h, self._rows(logits, logits.dtype, "logits"), _DTYPES[logits.dtype],
-            logits.stride(0) if logits.shape[0] > 1 else self.V, logits.shape[0],
-            self._t(row_start, name="row_start"), self._t(drafts, name="drafts"),
-            self._t(num_valid, name="num_valid"), self._t(active, torch.uint8, "active"), B,
-            self._t(temperature, torch.float32, "temperature"),
-            self._t(uniform, torch.float32, "uniform"), self._rows(noise, torch.float32, "noise"),
-            noise.stride(0) if B > 1 else self.V, self._rows(draft_probs, torch.float32, "draft_probs"),
-            (draft_probs.stride(0) if draft_probs.shape[0] > 1 else self.V)
-            if draft_probs is not None else 0,
-            self._t(out.sampled), self._t(out.num_accepted), self._t(out.logprobs, torch.float32),
-            _stream_handle(stream)), "sgd_verify")
+        q = q_stride = None
+        if draft_probs is not None:
+            if self._pair(draft_probs, "draft_probs") != (rows, V):
+                raise ValueError("draft_probs must have the shape of logits")
+            q, q_stride = self._rows(draft_probs, rows, torch.float32, "draft_probs")
+        if row_start is not None and row_start.shape[0] < B:
+            raise ValueError("row_start must have an entry per row")
+        if temperature is not None and temperature.shape[0] < B:
+            raise ValueError("temperature must have an entry per row")
+        if active is not None and active.shape[0] < B:
+            raise ValueError("active must have an entry per row")
+        if out is None:
+            out = self.new_verdict(B)
+        t = self._t
+        x, x_stride = self._rows(logits, rows, logits.dtype, "logits")
+        n, n_stride = self._rows(noise, B, torch.float32, "noise")
+        st = self._lib.sgd_verify(
+            self._h, x, dtype, x_stride, rows, t(row_start, name="row_start"), t(drafts, name="drafts"),
+            t(num_valid, name="num_valid"), t(active, torch.uint8, "active"), B,
+            t(temperature, torch.float32, "temperature"), t(uniform, torch.float32, "uniform"), n, n_stride,
+            q, q_stride or 0, t(out.sampled), t(out.num_accepted), t(out.logprobs, torch.float32),
+            _stream_handle(stream, self._index))
+        if st < 0:
+            raise L.SgdError(st, "sgd_verify")
         return out
 
-    def _rows(self, t: Optional[torch.Tensor], dtype, name: str):
-        """The address of a tensor whose rows may be apart but are contiguous themselves."""
-        if t is None:
-            return None
-        if t.device != self.device:
+    @staticmethod
+    def _pair(t: torch.Tensor, name: str):
+        if t.dim() != 2:
+            raise ValueError("%s must have two dimensions" % name)
+        return tuple(t.shape)
+
+    def _rows(self, t: torch.Tensor, n: int, dtype, name: str):
+        """Address and row stride of a tensor whose n rows may be apart but are
+        contiguous themselves."""
+        if t.get_device() != self._index:
             raise ValueError("%s must be on %s" % (name, self.device))
-        if t.dtype != dtype or (t.stride(1) != 1 and t.shape[1] > 1):
+        stride, one = t.stride()
+        if t.dtype is not dtype or (one != 1 and t.shape[1] > 1):
             raise ValueError("%s must be a %s tensor with contiguous rows" % (name, dtype))
-        return t.data_ptr()
+        return t.data_ptr(), stride if n > 1 else t.shape[1]
 
     # -- corpus ---------------------------------------------------------------
     def ingest(self, token_ids: torch.Tensor, rows: torch.Tensor, starts: torch.Tensor,

@@ -43,6 +43,7 @@ class KVCache:
                             head_dim, max_batch, max_pages_per_row)
         self.cfg = cfg
         self.device = torch.device("cuda", device)
+        self._index = device
         torch.cuda.init()
         with torch.cuda.device(self.device):
             torch.zeros(1, device=self.device)  # make the primary context current
@@ -63,22 +64,23 @@ class KVCache:
         self.kv_heads, self.q_heads, self.head_dim = kv_heads, cfg.q_heads, head_dim
         self.page_size, self.max_batch, self.max_pages = page_size, max_batch, max_pages_per_row
         self._layers = [L.SgdKvLayer(*(t[i].data_ptr() for t in storage)) for i in range(num_layers)]
+        self._layer_refs = [ctypes.addressof(x) for x in self._layers]
 
     _check = staticmethod(SuffixDrafter._check)
     _t = SuffixDrafter._t
 
     def _new(self, t: torch.Tensor, heads: int, name: str):
         """A packed [N, heads, head_dim] tensor whose last dimension is contiguous."""
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError("%s must be on %s" % (name, self.device))
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim or t.stride(2) != 1:
+        if t.dim() != 3 or t.shape[1:] != (heads, self.head_dim) or t.stride(2) != 1:
             raise ValueError("%s must be [N, %d, %d] with a contiguous last dimension"
                              % (name, heads, self.head_dim))
         return t.data_ptr()
 
     def _rows(self, block_table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor) -> int:
         B = lens.shape[0]
-        if tuple(block_table.shape) != (B, self.max_pages) or starts.shape[0] != B + 1:
+        if block_table.shape != (B, self.max_pages) or starts.shape[0] != B + 1:
             raise ValueError("block_table must be [B, %d], the lengths [B] and the starts [B + 1]"
                              % self.max_pages)
         return B
@@ -89,13 +91,18 @@ class KVCache:
         (float32, float16 or bfloat16; slices of one projection's output are
         taken as they are).  seq_lens [B] counts the new tokens."""
         B = self._rows(block_table, seq_lens, q_start)
-        if k.dtype not in _DTYPES or v.dtype != k.dtype or v.shape != k.shape:
+        dtype = _DTYPES.get(k.dtype)
+        if dtype is None or v.dtype is not k.dtype or v.shape != k.shape:
             raise ValueError("k and v must have one shape, and one type of float32, float16 or bfloat16")
-        self._check(self._lib.sgd_kv_write(
-            self._h, ctypes.byref(self._layers[layer]), self._new(k, self.kv_heads, "k"),
-            self._new(v, self.kv_heads, "v"), _DTYPES[k.dtype], k.stride(0), k.stride(1), v.stride(0),
-            v.stride(1), self._t(block_table, name="block_table"), self._t(seq_lens, name="seq_lens"),
-            self._t(q_start, name="q_start"), B, k.shape[0], _stream_handle(stream)), "sgd_kv_write")
+        t = self._t
+        kt, kh, _ = k.stride()
+        vt, vh, _ = v.stride()
+        st = self._lib.sgd_kv_write(
+            self._h, self._layer_refs[layer], self._new(k, self.kv_heads, "k"), self._new(v, self.kv_heads, "v"),
+            dtype, kt, kh, vt, vh, t(block_table, name="block_table"), t(seq_lens, name="seq_lens"),
+            t(q_start, name="q_start"), B, k.shape[0], _stream_handle(stream, self._index))
+        if st < 0:
+            raise L.SgdError(st, "sgd_kv_write")
 
     def read(self, block_table: torch.Tensor, start: torch.Tensor, out_start: torch.Tensor,
              out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, total: Optional[int] = None,
@@ -111,14 +118,17 @@ class KVCache:
             out = tuple(torch.empty((total, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
                         for _ in range(2))
         k, v = out
-        if k.dtype not in _DTYPES or v.dtype != k.dtype or v.shape != k.shape or not k.is_contiguous() \
+        dtype = _DTYPES.get(k.dtype)
+        if dtype is None or v.dtype is not k.dtype or v.shape != k.shape or not k.is_contiguous() \
                 or not v.is_contiguous():
             raise ValueError("out must be two contiguous tensors of one shape and type")
-        self._check(self._lib.sgd_kv_read(
-            self._h, ctypes.byref(self._layers[layer]), self._t(block_table, name="block_table"),
-            self._t(start, name="start"), self._t(out_start, name="out_start"), B, k.shape[0],
-            self._new(k, self.kv_heads, "out"), self._new(v, self.kv_heads, "out"), _DTYPES[k.dtype],
-            _stream_handle(stream)), "sgd_kv_read")
+        t = self._t
+        st = self._lib.sgd_kv_read(
+            self._h, self._layer_refs[layer], t(block_table, name="block_table"), t(start, name="start"),
+            t(out_start, name="out_start"), B, k.shape[0], self._new(k, self.kv_heads, "out"),
+            self._new(v, self.kv_heads, "out"), dtype, _stream_handle(stream, self._index))
+        if st < 0:
+            raise L.SgdError(st, "sgd_kv_read")
         return k, v
 
     def attend(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -130,18 +140,22 @@ class KVCache:
         positions up to its own, with window > 0 only the last `window` of them
         and the first `sinks`.  max_q: the most new tokens of any row."""
         B = self._rows(block_table, seq_lens, q_start)
-        if q.dtype not in (torch.float16, torch.bfloat16):
+        dtype = _DTYPES.get(q.dtype)
+        if dtype is None or dtype == L.F32:
             raise ValueError("q must be float16 or bfloat16")
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        if out.shape != q.shape:
+        elif out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-        self._check(self._lib.sgd_kv_attend(
-            self._h, ctypes.byref(self._layers[layer]), self._new(q, self.q_heads, "q"), _DTYPES[q.dtype],
-            q.stride(0), q.stride(1), self._t(block_table, name="block_table"),
-            self._t(seq_lens, name="seq_lens"), self._t(q_start, name="q_start"), B, q.shape[0], max_q,
-            scale if scale is not None else self.head_dim ** -0.5, window, sinks,
-            self._t(out, q.dtype, "out"), _stream_handle(stream)), "sgd_kv_attend")
+        t, at = self._t, self._new(q, self.q_heads, "q")
+        qt, qh, _ = q.stride()
+        st = self._lib.sgd_kv_attend(
+            self._h, self._layer_refs[layer], at, dtype, qt, qh, t(block_table, name="block_table"),
+            t(seq_lens, name="seq_lens"), t(q_start, name="q_start"), B, q.shape[0], max_q,
+            scale if scale is not None else self.head_dim ** -0.5, window, sinks, t(out, q.dtype, "out"),
+            _stream_handle(stream, self._index))
+        if st < 0:
+            raise L.SgdError(st, "sgd_kv_attend")
         return out
 
     # -- diagnostics ----------------------------------------------------------
