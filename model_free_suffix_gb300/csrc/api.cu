@@ -398,7 +398,7 @@ int sgd_create(const sgd_config *cfg, int device, sgd_ctx **out) {
   if (e == cudaSuccess) e = cudaMemset(x->d_err, 0, 4);
   if (e == cudaSuccess) e = cudaMemset(x->d_build_err, 0, 4);
   {
-    // no position counted yet, no row ended
+    // no row has ended
     const VerifyLayout l = verify_layout(cfg->max_batch, cfg->k);
     al((void **)&x->d_verify, l.bytes);
     if (e == cudaSuccess) e = cudaMemset(x->d_verify, 0, l.bytes);
@@ -828,11 +828,7 @@ int sgd_verify(sgd_ctx *x, const void *logits, int32_t dtype, int64_t row_stride
   a.accepted = num_accepted;
   a.logprobs = logprobs;
   a.err = x->d_err;
-  a.part = reinterpret_cast<float4 *>(x->d_verify + l.part);
-  a.draw_part = reinterpret_cast<float4 *>(x->d_verify + l.draw_part);
   a.stat = reinterpret_cast<float4 *>(x->d_verify + l.stat);
-  a.count = reinterpret_cast<unsigned *>(x->d_verify + l.count);
-  a.draw_count = reinterpret_cast<unsigned *>(x->d_verify + l.draw_count);
   a.stop = reinterpret_cast<int *>(x->d_verify + l.stop);
   x->launches += 2;
   return check_cuda(launch_verify(a, dtype, (cudaStream_t)stream));

@@ -22,8 +22,10 @@
 namespace sgd {
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int WARPS = 8;
+constexpr int THREADS = 32 * WARPS;
 constexpr int EXP_MIN = -48, EXP_MAX = 48;
+constexpr int PAST = 1 << 30;  // a position that no table reaches
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -46,7 +48,7 @@ struct Eight {
     if (vec) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+        const uint4 v = *(reinterpret_cast<const uint4 *>(p) + i);
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;
         w[4 * i + 2] = v.z;
@@ -85,82 +87,152 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   return r;
 }
 
-// One CTA takes the blocks whose first new token lies among `chunk` packed
-// tokens, for one head, keys or values.  A block's entries stay in registers
-// (PASSES groups of eight per thread) between the maximum and the encoding, so
-// each is read once.
-template <typename T, int PASSES>
+// Some tokens of one row in one page: what a CTA takes, its warps sharing out
+// the heads of keys and values.
+struct Segment {
+  int b;      // row (B: none)
+  int first;  // packed token
+  int count;
+  int page, slot;  // where the first one lives; page -1: nowhere
+};
+
+// The s-th segment of a call whose row b has the packed tokens starts[b] ..
+// starts[b + 1] at positions from pos0(b) on (below 0: a row that must not be
+// touched).  Every CTA counts the rows' segments, which costs about as much as
+// the search for a token's row would and leaves no CTA without work but those
+// past the end.  Up to 32 rows each warp counts for itself, without a barrier.
+template <typename Pos>
+__device__ Segment segment_of(const int32_t *starts, int B, int N, const int32_t *table, int max_pages, int num_pages,
+                              int P, long long s, Pos pos0, uint32_t *bits) {
+  __shared__ int warp_sum[WARPS];
+  __shared__ int found[5];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool alone = B <= 32;
+  int row = B, t0 = 0, t1 = 0, p = 0, j = 0;
+  long long before = 0;
+  if (!alone && tid == 0) found[0] = B;
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
+    const int b = b0 + (alone ? lane : tid);
+    int n = 0;
+    t0 = t1 = p = 0;
+    if (b < B) {
+      t0 = __ldg(starts + b);
+      t1 = __ldg(starts + b + 1);
+      p = pos0(b, t1 - t0);
+      if (t0 < 0 || t1 < t0 || t1 > N || (p < 0 && t1 > t0))
+        *bits |= SGD_KV_ERR_LENGTH;
+      else if (t1 > t0)
+        n = (p % P + (t1 - t0) + P - 1) / P;
+    }
+    int scan = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(FULL, scan, o);
+      if (lane >= o) scan += x;
+    }
+    long long at = before + scan - n;
+    if (alone) {
+      const bool mine = at <= s && s < at + n;
+      const uint32_t who = __ballot_sync(FULL, mine);
+      if (who == 0) return Segment{B, 0, 0, -1, 0};
+      const int src = __ffs(who) - 1;
+      row = src;
+      t0 = __shfl_sync(FULL, t0, src);
+      t1 = __shfl_sync(FULL, t1, src);
+      p = __shfl_sync(FULL, p, src);
+      j = __shfl_sync(FULL, (int)(s - at), src);
+      break;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) at += warp_sum[w];
+      before += warp_sum[w];
+    }
+    if (at <= s && s < at + n) {
+      found[0] = b;
+      found[1] = t0;
+      found[2] = t1;
+      found[3] = p;
+      found[4] = (int)(s - at);
+    }
+    if (before > s) break;
+  }
+  if (!alone) {
+    __syncthreads();
+    row = found[0];
+    t0 = found[1];
+    t1 = found[2];
+    p = found[3];
+    j = found[4];
+  }
+  Segment g{row, 0, 0, -1, 0};
+  if (row == B) return g;
+  const int block = p / P + j, from = j == 0 ? p : block * P;
+  g.slot = from - block * P;
+  g.first = t0 + (from - p);
+  g.count = min(t1 - g.first, P - g.slot);
+  if (block < max_pages) g.page = __ldg(table + (long long)row * max_pages + block);
+  if (g.page < 0 || g.page >= num_pages) {
+    g.page = -1;
+    *bits |= SGD_KV_ERR_PAGE;
+  }
+  return g;
+}
+
+// The largest magnitude among 16 e4m3 bytes, as a byte (NaN codes count as 0).
+__device__ __forceinline__ uint32_t top_bytes(uint32_t top, const uint4 &v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = w[i] & 0x7f7f7f7fu;
+    top = __vmaxu4(top, x & ~__vcmpeq4(x, 0x7f7f7f7fu));
+  }
+  return top;
+}
+
+// A warp takes one head's keys or values of a segment: the largest magnitude
+// first (new entries, and the block's older ones), then the encoding.  The
+// second reading of the new entries finds them in L1.  Bound by latency at the
+// few tokens of a verification step, by the bytes at prompts.
+template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) kv_write_kernel(KvWriteArgs a) {
-  __shared__ float sh[THREADS / 32];
-  const int h = blockIdx.y, tid = threadIdx.x;
-  const bool value = blockIdx.z != 0;
-  const int D = a.c.dim, P = a.c.page;
-  const int per = D / 8;                 // threads of a token
-  const int slot_step = THREADS / per;   // tokens per pass
-  const int sub = tid % per, slot_at = tid / per;
-  const T *src = static_cast<const T *>(value ? a.v : a.k) +
-                 (long long)h * (value ? a.v_head : a.k_head) + sub * 8;
-  const long long src_token = value ? a.v_token : a.k_token;
-  uint8_t *cache = value ? a.c.v : a.c.k;
-  float *scales = value ? a.c.vs : a.c.ks;
-  int i = blockIdx.x * a.chunk;
-  const int end = min(i + a.chunk, a.r.N);
-  int b = row_of_token(a.r.q_start, a.r.B, i);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = a.c.page;
   uint32_t bits = 0;
-  while (b < a.r.B && i < end) {
-    const int q0 = __ldg(a.r.q_start + b), q1 = min(__ldg(a.r.q_start + b + 1), a.r.N);
-    if (i >= q1) {
-      ++b;
-      continue;
-    }
-    const int n = __ldg(a.r.seq_lens + b);
-    const int pos = n - (q1 - q0) + (i - q0);
-    if (q0 < 0 || q0 > i || n < q1 - q0) {
-      bits |= SGD_KV_ERR_LENGTH;
-      i = q1;
-      ++b;
-      continue;
-    }
-    const int slot0 = pos % P;
-    const int stop = min(q1, i + P - slot0);
-    const bool head = i == q0 || slot0 == 0;
-    const int first = i;
-    i = stop;
-    if (!head) continue;  // the CTA of the block's first new token takes it
-    const int block = pos / P;
-    const int page = block < a.r.max_pages ? __ldg(a.r.table + (long long)b * a.r.max_pages + block) : -1;
-    if (page < 0 || page >= a.c.num_pages) {
-      bits |= SGD_KV_ERR_PAGE;
-      continue;
-    }
-    const int cnt = stop - first, used = slot0 + cnt;
-    uint8_t *base = cache + ((long long)page * a.c.heads + h) * P * D + sub * 8;
-    float *scale = scales + (long long)page * a.c.heads + h;
-    const float old = slot0 > 0 ? *scale : 1.f;
-    Eight<T> fresh[PASSES];
-    uint2 was[PASSES];
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int s = p * slot_step + slot_at;
-      if (s < slot0)
-        was[p] = *reinterpret_cast<const uint2 *>(base + s * D);
-      else if (s < used)
-        fresh[p].load(src + (long long)(first + s - slot0) * src_token, a.vec);
-    }
+  const Segment g = segment_of(
+      a.r.q_start, a.r.B, a.r.N, a.r.table, a.r.max_pages, a.c.num_pages, P, blockIdx.x,
+      [&](int b, int ql) { return min(__ldg(a.r.seq_lens + b) - ql, PAST); }, &bits);
+  constexpr int PER = D / 8, STEP = 32 / PER, UNROLL = 4;  // lanes of a token, tokens of a round
+  const int sub = lane % PER, at = lane / PER;
+  for (int hv = blockIdx.y * WARPS + warp; g.page >= 0 && hv < 2 * a.c.heads; hv += gridDim.y * WARPS) {
+    const bool value = hv >= a.c.heads;
+    const int h = value ? hv - a.c.heads : hv;
+    const long long token = value ? a.v_token : a.k_token;
+    const T *src = static_cast<const T *>(value ? a.v : a.k) + (long long)h * (value ? a.v_head : a.k_head) +
+                   (long long)g.first * token + sub * 8;
+    const long long block = (long long)g.page * a.c.heads + h;
+    uint8_t *base = (value ? a.c.v : a.c.k) + block * P * D;
+    float *scale = (value ? a.c.vs : a.c.ks) + block;
+    const float old = g.slot > 0 ? *scale : 1.f;
     float amax = 0.f;
+    for (int t0 = 0; t0 < g.count; t0 += STEP * UNROLL) {
+      Eight<T> x[UNROLL];
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int s = p * slot_step + slot_at;
-      float x[8];
-      if (s < slot0) {
-        decode8(was[p], x);
+      for (int i = 0; i < UNROLL; ++i) {
+        const int t = t0 + i * STEP + at;
+        if (t < g.count) x[i].load(src + t * token, a.vec);
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]) * old);  // (a NaN is dropped)
-      } else if (s < used) {
-        fresh[p].get(x);
+      for (int i = 0; i < UNROLL; ++i) {
+        if (t0 + i * STEP + at >= g.count) continue;
+        float v[8];
+        x[i].get(v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float m = fabsf(x[e]);
+          const float m = fabsf(v[e]);
           if (!(m < CUDART_INF_F))
             bits |= SGD_KV_ERR_NONFINITE;
           else
@@ -168,136 +240,164 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(KvWriteArgs a) {
         }
       }
     }
+    if (g.slot > 0) {
+      uint32_t top = 0;
+      const int n = g.slot * D / 16;
+      for (int i0 = 0; i0 < n; i0 += 32 * 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (i0 + i * 32 + lane < n) v[i] = *reinterpret_cast<const uint4 *>(base + (i0 + i * 32 + lane) * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = top_bytes(top, v[i]);
+      }
+      top = max(max(top & 0xff, top >> 8 & 0xff), max(top >> 16 & 0xff, top >> 24));
+      const uint32_t f = e4m3x2_to_f16x2(top);
+      amax = fmaxf(amax, __low2float(*reinterpret_cast<const __half2 *>(&f)) * old);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-    __syncthreads();  // (the previous block's maxima are read)
-    if ((tid & 31) == 0) sh[tid >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) amax = fmaxf(amax, sh[w]);
     const int e = scale_exp(amax);
     const float s_new = pow2(e), inv = pow2(-e);
-    const bool redo = slot0 > 0 && s_new != old;
-    if (tid == 0) *scale = s_new;
+    if (lane == 0) *scale = s_new;
+    for (int t0 = 0; t0 < g.count; t0 += STEP * UNROLL) {
+      Eight<T> x[UNROLL];
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int s = p * slot_step + slot_at;
-      float x[8];
-      if (s < slot0) {
-        if (!redo) continue;
-        decode8(was[p], x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= old;
-      } else if (s < used) {
-        fresh[p].get(x);
-      } else {
-        continue;
+      for (int i = 0; i < UNROLL; ++i) {
+        const int t = t0 + i * STEP + at;
+        if (t < g.count) x[i].load(src + t * token, a.vec);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] == x[j] ? x[j] : 0.f;
-      *reinterpret_cast<uint2 *>(base + s * D) = encode8(x, inv);
+      for (int i = 0; i < UNROLL; ++i) {
+        const int t = t0 + i * STEP + at;
+        if (t >= g.count) continue;
+        float v[8];
+        x[i].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] : 0.f;
+        *reinterpret_cast<uint2 *>(base + (g.slot + t) * D + sub * 8) = encode8(v, inv);
+      }
+    }
+    if (g.slot > 0 && s_new != old) {
+      for (int i = lane; i < g.slot * D / 8; i += 32) {
+        uint2 *p = reinterpret_cast<uint2 *>(base + i * 8);
+        float v[8];
+        decode8(*p, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] * old : 0.f;
+        *p = encode8(v, inv);
+      }
     }
   }
   if (bits) atomicOr(a.err, bits);
 }
 
-// A thread takes 16 bytes of one token and head at a time and writes 16
-// values; bound by the bytes written.  Tokens of a page and head are
-// contiguous in the cache, heads of a token in the output: a CTA takes 64
-// tokens of one head, so both sides move whole 32-byte sectors.
-constexpr int READ_TOKENS = 64;
-template <typename T>
+// A warp takes one head's keys or values of a segment, 16 bytes a lane; bound
+// by the bytes written.
+template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvReadArgs a) {
-  const int h = blockIdx.y, tid = threadIdx.x, D = a.c.dim, P = a.c.page;
-  const bool value = blockIdx.z != 0;
-  const uint8_t *cache = value ? a.c.v : a.c.k;
-  const float *scales = value ? a.c.vs : a.c.ks;
-  T *out = static_cast<T *>(value ? a.v : a.k);
-  const int i0 = blockIdx.x * READ_TOKENS;
-  int b = row_of_token(a.out_start, a.B, i0);
-  const int per = D / 16, step = THREADS / per, sub = tid % per;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = a.c.page;
   uint32_t bits = 0;
-#pragma unroll 4
-  for (int t = tid / per; t < READ_TOKENS; t += step) {
-    const int i = i0 + t;
-    if (i >= a.N) break;
-    while (b < a.B && i >= __ldg(a.out_start + b + 1)) ++b;
-    float x[16];
+  const Segment g = segment_of(
+      a.out_start, a.B, a.N, a.table, a.max_pages, a.c.num_pages, P, blockIdx.x,
+      [&](int b, int) { return min(__ldg(a.from + b), PAST); }, &bits);
+  // outputs that no row claims
+  const int claimed = min(max(__ldg(a.out_start + a.B), 0), a.N);
+  if (claimed < a.N) {
+    bits |= SGD_KV_ERR_LENGTH;
+    const long long width = (long long)a.c.heads * D;
+    for (long long i = claimed * width + (long long)(blockIdx.y * gridDim.x + blockIdx.x) * THREADS + threadIdx.x;
+         i < a.N * width; i += (long long)gridDim.x * gridDim.y * THREADS)
+      static_cast<T *>(a.k)[i] = static_cast<T *>(a.v)[i] = from_f32<T>(0.f);
+  }
+  constexpr int PER = D / 16, STEP = 32 / PER, UNROLL = 4;
+  const int sub = lane % PER, at = lane / PER;
+  for (int hv = blockIdx.y * WARPS + warp; hv < 2 * a.c.heads; hv += gridDim.y * WARPS) {
+    const bool value = hv >= a.c.heads;
+    const int h = value ? hv - a.c.heads : hv;
+    const long long block = (long long)max(g.page, 0) * a.c.heads + h;
+    const uint8_t *base = (value ? a.c.v : a.c.k) + (block * P + g.slot) * D + sub * 16;
+    const float s = g.page >= 0 ? (value ? a.c.vs : a.c.ks)[block] : 0.f;
+    T *out = static_cast<T *>(value ? a.v : a.k) + ((long long)g.first * a.c.heads + h) * D + sub * 16;
+    for (int t0 = 0; t0 < g.count; t0 += STEP * UNROLL) {
+      uint4 raw[UNROLL];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    if (b < a.B) {
-      const int pos = __ldg(a.from + b) + i - __ldg(a.out_start + b);
-      const int block = pos / P;
-      const int page = pos >= 0 && block < a.max_pages ? __ldg(a.table + (long long)b * a.max_pages + block) : -1;
-      if (page >= 0 && page < a.c.num_pages) {
-        const long long at = (long long)page * a.c.heads + h;
-        const uint4 raw = *reinterpret_cast<const uint4 *>(cache + (at * P + pos % P) * D + sub * 16);
-        const float s = scales[at];
-        float y[8];
-        decode8(make_uint2(raw.x, raw.y), y);
+      for (int i = 0; i < UNROLL; ++i) {
+        const int t = t0 + i * STEP + at;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (t < g.count && g.page >= 0) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(base + t * D));
+      }
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) {
+        const int t = t0 + i * STEP + at;
+        if (t >= g.count) continue;
+        float x[16], y[8];
+        decode8(make_uint2(raw[i].x, raw[i].y), y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = y[e] * s;
-        decode8(make_uint2(raw.z, raw.w), y);
+        decode8(make_uint2(raw[i].z, raw[i].w), y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[8 + e] = y[e] * s;
-      } else {
-        bits |= SGD_KV_ERR_PAGE;  // (zeros are returned for it)
+        T *o = out + (long long)t * a.c.heads * D;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            __stcs(reinterpret_cast<float4 *>(o) + e, make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            __stcs(reinterpret_cast<uint4 *>(o) + e,
+                   make_uint4(pack2<T>(x[8 * e], x[8 * e + 1]), pack2<T>(x[8 * e + 2], x[8 * e + 3]),
+                              pack2<T>(x[8 * e + 4], x[8 * e + 5]), pack2<T>(x[8 * e + 6], x[8 * e + 7])));
+        }
       }
-    } else {
-      bits |= SGD_KV_ERR_LENGTH;
-    }
-    T *o = out + ((long long)i * a.c.heads + h) * D + sub * 16;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        reinterpret_cast<float4 *>(o)[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        reinterpret_cast<uint4 *>(o)[e] =
-            make_uint4(pack2<T>(x[8 * e], x[8 * e + 1]), pack2<T>(x[8 * e + 2], x[8 * e + 3]),
-                       pack2<T>(x[8 * e + 4], x[8 * e + 5]), pack2<T>(x[8 * e + 6], x[8 * e + 7]));
     }
   }
   if (bits) atomicOr(a.err, bits);
+}
+
+// CTAs for B rows of N tokens: a row of n tokens touches at most n / page + 2
+// pages, and 1 if it is one token.
+dim3 segments(int B, int N, const KvView &c) {
+  const long long few = (long long)N, many = (long long)N / c.page + 2LL * B;
+  return dim3((unsigned)(few < many ? few : many), (unsigned)((2 * c.heads + WARPS - 1) / WARPS));
 }
 
 template <typename T>
 cudaError_t write(const KvWriteArgs &a, cudaStream_t st) {
-  const dim3 grid((a.r.N + a.chunk - 1) / a.chunk, a.c.heads, 2);
-  switch (a.c.page * a.c.dim / (8 * THREADS)) {
-    case 1: kv_write_kernel<T, 1><<<grid, THREADS, 0, st>>>(a); break;
-    case 2: kv_write_kernel<T, 2><<<grid, THREADS, 0, st>>>(a); break;
-    case 4: kv_write_kernel<T, 4><<<grid, THREADS, 0, st>>>(a); break;
-    case 8: kv_write_kernel<T, 8><<<grid, THREADS, 0, st>>>(a); break;
-    case 16: kv_write_kernel<T, 16><<<grid, THREADS, 0, st>>>(a); break;
-    default: return cudaErrorInvalidValue;
-  }
+  const dim3 grid = segments(a.r.B, a.r.N, a.c);
+  if (a.c.dim == 128)
+    kv_write_kernel<T, 128><<<grid, THREADS, 0, st>>>(a);
+  else
+    kv_write_kernel<T, 64><<<grid, THREADS, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t read(const KvReadArgs &a, cudaStream_t st) {
+  const dim3 grid = segments(a.B, a.N, a.c);
+  if (a.c.dim == 128)
+    kv_read_kernel<T, 128><<<grid, THREADS, 0, st>>>(a);
+  else
+    kv_read_kernel<T, 64><<<grid, THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_write(KvWriteArgs a, int dtype, cudaStream_t st) {
-  // Few tokens: one per CTA, so that every block has its own; many: up to a
-  // page per CTA, so that few CTAs find that their tokens begin no block.
-  const long long want = 152 * 16;
-  a.chunk = 1;
-  while (a.chunk < a.c.page && (long long)a.r.N * a.c.heads * 2 / (2 * a.chunk) >= want) a.chunk *= 2;
+cudaError_t launch_kv_write(const KvWriteArgs &a, int dtype, cudaStream_t st) {
   if (dtype == SGD_F32) return write<float>(a, st);
   if (dtype == SGD_F16) return write<__half>(a, st);
   return write<__nv_bfloat16>(a, st);
 }
 
-cudaError_t launch_kv_read(KvReadArgs a, int dtype, cudaStream_t st) {
-  const dim3 grid((a.N + READ_TOKENS - 1) / READ_TOKENS, a.c.heads, 2);
-  if (dtype == SGD_F32)
-    kv_read_kernel<float><<<grid, THREADS, 0, st>>>(a);
-  else if (dtype == SGD_F16)
-    kv_read_kernel<__half><<<grid, THREADS, 0, st>>>(a);
-  else
-    kv_read_kernel<__nv_bfloat16><<<grid, THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_kv_read(const KvReadArgs &a, int dtype, cudaStream_t st) {
+  if (dtype == SGD_F32) return read<float>(a, st);
+  if (dtype == SGD_F16) return read<__half>(a, st);
+  return read<__nv_bfloat16>(a, st);
 }
 
 }  // namespace sgd

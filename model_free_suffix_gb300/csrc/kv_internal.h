@@ -30,7 +30,6 @@ struct KvWriteArgs {
   KvRows r;
   const void *k, *v;
   long long k_token, k_head, v_token, v_head;  // strides in elements
-  int chunk;                                   // packed tokens per CTA (a power of two)
   int vec;                                     // 16-byte loads allowed
   uint32_t *err;
 };
@@ -58,8 +57,8 @@ struct KvAttendArgs {
   uint32_t *err;
 };
 
-cudaError_t launch_kv_write(KvWriteArgs a, int dtype, cudaStream_t st);
-cudaError_t launch_kv_read(KvReadArgs a, int dtype, cudaStream_t st);
+cudaError_t launch_kv_write(const KvWriteArgs &a, int dtype, cudaStream_t st);
+cudaError_t launch_kv_read(const KvReadArgs &a, int dtype, cudaStream_t st);
 size_t kv_attend_workspace();
 cudaError_t kv_attend_set_limits();
 cudaError_t launch_kv_attend(KvAttendArgs a, int dtype, cudaStream_t st, int *launches);
@@ -82,17 +81,6 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   uint32_t r;
   asm("{.reg .b16 t; cvt.rn.satfinite.e4m3x2.f32 t, %1, %2; cvt.u32.u16 %0, t;}" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// The row of packed token i, by all threads of a block: starts[0..B] ascends.
-// B if i is past the last row's end.
-__device__ __forceinline__ int row_of_token(const int32_t *starts, int B, int i) {
-  int b = 0;
-  for (int j0 = 0; j0 < B; j0 += blockDim.x) {
-    const int j = j0 + threadIdx.x;
-    b += __syncthreads_count(j < B && __ldg(starts + j + 1) <= i);
-  }
-  return b;
 }
 #endif
 

@@ -220,16 +220,12 @@ struct VerifyArgs {
   float *logprobs;
   uint32_t *err;
   // workspace (verify_layout)
-  float4 *part;         // [positions][splits] {m, Z, argmax}
-  float4 *draw_part;    // [B][draw_splits]
-  float4 *stat;         // [B][k + 1] {m, Z, argmax}
-  unsigned *count;      // [B][k + 1] splits done; 0 between calls
-  unsigned *draw_count; // [B]
-  int *stop;            // [B] first position not accepted; 2^31 - 1 between calls
-  int splits, draw_splits;
+  float4 *stat;  // [B][k + 1] {m, Z, argmax}
+  int *stop;     // [B] first position not accepted; 2^31 - 1 between calls
+  int splits, draw_splits;  // CTAs of a position, of a row's draw
 };
 struct VerifyLayout {
-  size_t part, draw_part, stat, count, draw_count, stop, bytes;
+  size_t stat, stop, bytes;
 };
 VerifyLayout verify_layout(int max_batch, int k);
 // dtype: SGD_F32, SGD_F16 or SGD_BF16

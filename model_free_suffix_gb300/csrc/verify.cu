@@ -15,11 +15,10 @@
 //
 // Two launches.  The first makes (m, Z, argmax) of each position in one pass
 // over its logits, a running maximum and sum per thread; a position is split
-// over several CTAs and the last one to finish joins them in a fixed order, so
-// that the result does not depend on which CTA that is.  The second draws at
-// the one position per row where the drafts end, again split and joined.
-// Statistics are held in 32 bits.  Both are bound by reading the logits (and
-// the noise) once.
+// over the CTAs of a cluster, whose first CTA joins their parts, in order,
+// from its shared memory.  The second draws at the one position per row where
+// the drafts end, split and joined alike.  Statistics are held in 32 bits.
+// Both are bound by reading the logits (and the noise) once.
 #include <math_constants.h>
 
 #include "num_types.cuh"
@@ -30,7 +29,10 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int UNROLL = 4;                 // 16-byte loads in flight per thread
+constexpr int PER_SM = 4;                 // CTAs of an SM
+constexpr int MAX_SPLITS = 8;             // CTAs of a cluster, everywhere allowed
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
 constexpr float GREEDY_BELOW = 1e-5f;
 constexpr float NOISE_MIN = 8.673617379884035e-19f;  // 2^-60: w / noise stays finite
 
@@ -39,28 +41,66 @@ struct Stat {
   int arg;
 };
 
+// A cluster's CTAs give their parts to the first one's shared memory:
+// started() before anything else, then, when a part is ready, reached() (every
+// CTA is running, so its memory may be written), the stores, done(), and in
+// the first CTA all_done().
+__device__ __forceinline__ void started() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void reached() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void done() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void all_done() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void give(void *slot, float4 v) {  // to `slot` in CTA 0
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"((uint32_t)__cvta_generic_to_shared(slot)));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(there), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// exp((l - m) / t) with c = log2(e) / t.  The difference is taken before the
-// scaling, so logits of any size lose nothing; a NaN counts as -inf (the
-// maximum with a number drops it).
-__device__ __forceinline__ float weight(float l, float m, float c) {
-  return ex2(fmaxf((l - m) * c, -1e30f));
+// exp((l - m) / t) as 2^(l c - r), c = log2(e) / t, with the reference r = m c
+// rounded once: the fused multiply-add rounds only its small result, and r
+// cancels in every quotient, so logits of any size lose nothing.  Where r
+// would overflow (maxima near the type's lowest or largest value) the
+// difference is taken first.  A NaN logit or +inf - +inf weighs 0.
+constexpr float HUGE_REF = 1e30f;
+__device__ __forceinline__ float log2_weight(float l, float m, float c) {
+  const float r = m * c;
+  const float x = fabsf(r) < HUGE_REF ? fmaf(l, c, -r) : (l - m) * c;
+  return fmaxf(x, -1e30f);
 }
+__device__ __forceinline__ float weight(float l, float m, float c) { return ex2(log2_weight(l, m, c)); }
 // the same where m may be +inf: then only the +inf logits weigh, 1 each
 __device__ __forceinline__ float weight_any(float l, float m, float c) {
   return m == CUDART_INF_F ? (l == CUDART_INF_F ? 1.f : 0.f) : weight(l, m, c);
+}
+// from one maximum to a larger one: both references are what weight() used
+__device__ __forceinline__ float reweight(float from, float to, float c) {
+  const float x = from * c, y = to * c;
+  return ex2(fmaxf(fabsf(y) < HUGE_REF && fabsf(x) < HUGE_REF ? x - y : (from - to) * c, -1e30f));
 }
 
 __device__ __forceinline__ Stat join(const Stat &a, const Stat &b, float c) {
   Stat r;
   r.m = fmaxf(a.m, b.m);
-  const float sa = a.m == r.m ? 1.f : weight(a.m, r.m, c);
-  const float sb = b.m == r.m ? 1.f : weight(b.m, r.m, c);
+  const float sa = a.m == r.m ? 1.f : reweight(a.m, r.m, c);
+  const float sb = b.m == r.m ? 1.f : reweight(b.m, r.m, c);
   r.z = (a.z == 0.f ? 0.f : a.z * sa) + (b.z == 0.f ? 0.f : b.z * sb);
   r.arg = a.m > b.m ? a.arg : b.m > a.m ? b.arg : min(a.arg, b.arg);
   return r;
@@ -106,6 +146,33 @@ __device__ __forceinline__ Row row_of(const VerifyArgs &a, int b, bool report) {
   return r;
 }
 
+// The largest of N vectors' elements (NaN counts as -inf).
+template <typename T, int N>
+__device__ __forceinline__ float max_of(const uint4 (&raw)[N]) {
+  if constexpr (sizeof(T) == 4) {
+    float mx = -CUDART_INF_F;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float x[4];
+      unpack<float>(raw[j], x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, x[e]);
+    }
+    return mx;
+  } else {  // two at a time
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const uint32_t low = lowest_vec<T>().x;
+    T2 mx = *reinterpret_cast<const T2 *>(&low);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = __hmax2(mx, *reinterpret_cast<const T2 *>(&w[e]));
+    }
+    return fmaxf(to_f32(mx.x), to_f32(mx.y));
+  }
+}
+
 // Splits [lo, hi) of a row of T at `base` into elements before the first
 // 16-byte boundary, whole 16-byte vectors, and what is left.
 template <typename T>
@@ -128,21 +195,42 @@ struct Span {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) verify_stats_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(THREADS, PER_SM) verify_stats_kernel(VerifyArgs a) {
   __shared__ Stat sh[THREADS / 32];
-  __shared__ int last;
+  __shared__ float4 parts[MAX_SPLITS];
+  cudaTriggerProgrammaticLaunchCompletion();  // (the draw's CTAs may take their places and wait)
   const int split = blockIdx.x % a.splits;
   const int pb = blockIdx.x / a.splits;
   const int i = pb / a.B, b = pb % a.B;
   const Row r = row_of(a, b, i == 0 && split == 0 && threadIdx.x == 0);
   if (!r.on || i > r.nv) return;
+  // A position after one that was not accepted decides nothing: its logits are
+  // not read.  Positions come in order, all rows' first ones first, so this is
+  // often known by now; where it is not, the work is done and not used.
+  started();
+  const bool moot = __syncthreads_or(__ldcg(a.stop + b) < i);
   const T *row = static_cast<const T *>(a.logits) + (r.first + i) * a.stride;
   const int chunk = (a.V + a.splits - 1) / a.splits;
-  const int lo = min(a.V, split * chunk), hi = min(a.V, lo + chunk);
+  const int lo = min(a.V, split * chunk), hi = moot ? lo : min(a.V, lo + chunk);
   const Span<T> sp(row, lo, hi);
   constexpr int VN = Span<T>::VN;
   const int tid = threadIdx.x;
+  // what the decision needs, on its way while the logits are read
+  const bool decides = split == 0 && tid == 0 && i < r.nv;
+  int draft = -1;
+  float u = 0.f, l_draft = 0.f;
+  if (decides) {
+    draft = a.drafts[(long long)b * a.k + i];
+    if (draft >= 0 && draft < a.V) {
+      l_draft = to_f32(row[draft]);
+      if (!r.greedy) {
+        u = a.uniform[(long long)b * a.k + i];
+        if (a.q) u *= fmaxf(a.q[(r.first + i) * a.q_stride + draft], 0.f);
+      }
+    }
+  }
   Stat s{-CUDART_INF_F, 0.f, 0x7fffffff};
+  int best = -1;  // the group of vectors that holds the largest logit (-1: an edge element)
   // (edge elements: at most 2 (VN - 1) of them)
   if (tid < 2 * VN) {
     const int e = sp.edge(tid);
@@ -151,45 +239,51 @@ __global__ void __launch_bounds__(THREADS) verify_stats_kernel(VerifyArgs a) {
       if (l > s.m) {
         s.m = l;
         s.arg = e;
-        s.z = 1.f;
+        s.z = weight(l, l, r.c);
       }
     }
   }
+  const float edge_m = s.m;
   const uint4 *vec = reinterpret_cast<const uint4 *>(row + sp.v0);
   for (int v = tid; v < sp.nvec; v += UNROLL * THREADS) {
     uint4 raw[UNROLL];
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j)
       raw[j] = v + j * THREADS < sp.nvec ? __ldcs(vec + v + j * THREADS) : lowest_vec<T>();
-    float x[UNROLL][VN];
-    float mx = -CUDART_INF_F;
-#pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      unpack<T>(raw[j], x[j]);
-#pragma unroll
-      for (int e = 0; e < VN; ++e) mx = fmaxf(mx, x[j][e]);
+    const float mx = max_of<T, UNROLL>(raw);
+    if (mx > s.m) {
+      s.z = s.z == 0.f ? 0.f : s.z * reweight(s.m, mx, r.c);
+      s.m = mx;
+      best = v;
+    } else if (mx == s.m && best < 0) {
+      best = v;  // (an edge element of the same value may be the row's last)
     }
-    if (mx >= s.m) {
-      int at = 0x7fffffff;
-#pragma unroll
-      for (int j = UNROLL - 1; j >= 0; --j)
-#pragma unroll
-        for (int e = VN - 1; e >= 0; --e)
-          if (x[j][e] == mx) at = sp.v0 + (v + j * THREADS) * VN + e;
-      if (mx > s.m) {
-        s.z = s.z == 0.f ? 0.f : s.z * weight(s.m, mx, r.c);
-        s.m = mx;
-        s.arg = at;
-      } else {
-        s.arg = min(s.arg, at);  // (a tail element of the same value may come first)
-      }
-    }
+    const float ref = s.m * r.c;
     float z = 0.f;
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j)
+    for (int j = 0; j < UNROLL; ++j) {
+      float x[VN];
+      unpack<T>(raw[j], x);
 #pragma unroll
-      for (int e = 0; e < VN; ++e) z += weight(x[j][e], s.m, r.c);
+      for (int e = 0; e < VN; ++e) z += ex2(fmaf(x[e], r.c, -ref));
+    }
+    // NaN logits, nothing but -inf so far, or a maximum near the type's limits
+    if (!(z < CUDART_INF_F) || !(fabsf(ref) < HUGE_REF)) {
+      z = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < UNROLL; ++j)
+        for (int e = 0; e < VN && v + j * THREADS < sp.nvec && s.m != -CUDART_INF_F; ++e)
+          z += weight(to_f32(row[sp.v0 + (v + j * THREADS) * VN + e]), s.m, r.c);
+    }
     s.z += z;
+  }
+  if (r.greedy && best >= 0) {  // its lowest index (an earlier group of this thread has none)
+    if (edge_m != s.m) s.arg = 0x7fffffff;
+    for (int j = UNROLL - 1; j >= 0; --j)
+      for (int e = VN - 1; e >= 0; --e) {
+        const int g = best + j * THREADS, at = sp.v0 + g * VN + e;
+        if (g < sp.nvec && to_f32(row[at]) == s.m) s.arg = min(s.arg, at);
+      }
   }
   if (s.m == CUDART_INF_F) {  // +inf logits: they alone weigh; count this thread's
     s.z = 0.f;
@@ -201,46 +295,37 @@ __global__ void __launch_bounds__(THREADS) verify_stats_kernel(VerifyArgs a) {
       for (int e = 0; e < VN; ++e)
         if (to_f32(row[sp.v0 + v * VN + e]) == CUDART_INF_F) s.z += 1.f;
   }
-  s = join_warp(s, r.c);
-  if ((tid & 31) == 0) sh[tid >> 5] = s;
-  __syncthreads();
-  if (tid >= 32) return;
-  s = tid < THREADS / 32 ? sh[tid] : Stat{-CUDART_INF_F, 0.f, 0x7fffffff};
-  s = join_warp(s, r.c);
-  const int pos = b * (a.k + 1) + i;
-  if (a.splits > 1) {
-    if (tid == 0) {
-      float4 *part = a.part + (long long)pb * a.splits;
-      part[split] = make_float4(s.m, s.z, __int_as_float(s.arg), 0.f);
-      __threadfence();
-      last = atomicInc(a.count + pos, (unsigned)a.splits - 1) == (unsigned)a.splits - 1;
-    }
-    __syncwarp();
-    if (!last) return;
-    __threadfence();
-    const float4 *part = a.part + (long long)pb * a.splits;
-    s = Stat{-CUDART_INF_F, 0.f, 0x7fffffff};
-    for (int j = tid; j < a.splits; j += 32) {
-      const float4 p = __ldcg(part + j);
-      s = join(s, Stat{p.x, p.y, __float_as_int(p.z)}, r.c);
-    }
+  if (!moot) {
+    s = join_warp(s, r.c);
+    if ((tid & 31) == 0) sh[tid >> 5] = s;
+    __syncthreads();
+  }
+  reached();
+  if (tid < 32 && !moot) {
+    s = tid < THREADS / 32 ? sh[tid] : Stat{-CUDART_INF_F, 0.f, 0x7fffffff};
     s = join_warp(s, r.c);
   }
+  if (tid == 0) give(parts + split, make_float4(s.m, s.z, __int_as_float(s.arg), moot ? 1.f : 0.f));
+  done();
+  if (split != 0) return;
+  all_done();
+  if (tid >= 32) return;
+  s = Stat{-CUDART_INF_F, 0.f, 0x7fffffff};
+  bool missing = false;
+  if (tid < a.splits) {
+    const float4 p = parts[tid];
+    s = Stat{p.x, p.y, __float_as_int(p.z)};
+    missing = p.w != 0.f;
+  }
+  if (__any_sync(FULL, missing)) return;
+  s = join_warp(s, r.c);
   if (tid != 0) return;
-  a.stat[pos] = make_float4(s.m, s.z, __int_as_float(s.arg), 0.f);
+  a.stat[b * (a.k + 1) + i] = make_float4(s.m, s.z, __int_as_float(s.arg), 0.f);
   if (i == r.nv) return;
   // draft i: accepted, or the row ends here at the latest
-  const int x = a.drafts[(long long)b * a.k + i];
   bool ok = false;
-  if (x >= 0 && x < a.V && s.z > 0.f) {
-    if (r.greedy) {
-      ok = x == s.arg;
-    } else {
-      float u = a.uniform[(long long)b * a.k + i];
-      if (a.q) u *= fmaxf(a.q[(r.first + i) * a.q_stride + x], 0.f);
-      ok = u < weight_any(to_f32(row[x]), s.m, r.c) / s.z;
-    }
-  }
+  if (draft >= 0 && draft < a.V && s.z > 0.f)
+    ok = r.greedy ? draft == s.arg : u < weight_any(l_draft, s.m, r.c) / s.z;
   if (!ok) atomicMin(a.stop + b, i);
 }
 
@@ -257,14 +342,9 @@ __device__ __forceinline__ Best better_warp(Best s) {
     s = better(s, Best{__shfl_xor_sync(FULL, s.w, o), __shfl_xor_sync(FULL, s.arg, o)});
   return s;
 }
-// The product with the noise is compared before the quotient is made: the
-// division is reached a few times per thread only.
-__device__ __forceinline__ void take(Best &s, float w, float noise, int j) {
-  const float n = fmaxf(noise, NOISE_MIN);
-  if (w >= s.w * n && w > 0.f) {
-    const float q = w / n;
-    if (q > s.w || (q == s.w && j < s.arg)) s = Best{q, j};
-  }
+// A weight over its noise.
+__device__ __forceinline__ float ratio(float w, float noise) {
+  return __fdividef(w, fmaxf(noise, NOISE_MIN));
 }
 
 // Row b's outputs: the accepted drafts and `token` (-1: none), the log
@@ -280,9 +360,9 @@ __device__ void emit(const VerifyArgs &a, const Row &r, int b, int acc, int toke
     if (a.logprobs) {
       float lp = 0.f;
       if (x >= 0) {
-        const float4 st = a.stat[b * (a.k + 1) + i];
+        const float4 st = __ldcg(a.stat + b * (a.k + 1) + i);
         const float l = to_f32(first[i * a.stride + x]);
-        lp = (l == st.x ? 0.f : (l - st.x) * (1.f / r.t)) - logf(st.y);
+        lp = ((l == st.x && fabsf(l) == CUDART_INF_F ? 0.f : log2_weight(l, st.x, r.c)) - log2f(st.y)) * LN2;
       }
       a.logprobs[(long long)b * (a.k + 1) + i] = lp;
     }
@@ -291,9 +371,9 @@ __device__ void emit(const VerifyArgs &a, const Row &r, int b, int acc, int toke
 }
 
 template <typename T, bool Q>
-__global__ void __launch_bounds__(THREADS) verify_draw_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(THREADS, Q ? 3 : 4) verify_draw_kernel(VerifyArgs a) {
   __shared__ Best sh[2][THREADS / 32];
-  __shared__ int last;
+  __shared__ float4 parts[MAX_SPLITS];
   const int split = blockIdx.x % a.draw_splits, b = blockIdx.x / a.draw_splits;
   const int tid = threadIdx.x;
   const Row r = row_of(a, b, false);
@@ -307,9 +387,11 @@ __global__ void __launch_bounds__(THREADS) verify_draw_kernel(VerifyArgs a) {
     }
     return;
   }
-  if (r.greedy && split != 0) return;
+  if (!r.greedy) started();
+  else if (split != 0) return;
+  cudaGridDependencySynchronize();
   const int acc = min(__ldcg(a.stop + b), r.nv);
-  const float4 st = a.stat[b * (a.k + 1) + acc];
+  const float4 st = __ldcg(a.stat + b * (a.k + 1) + acc);
   const float m = st.x, z = st.y;
   int token = -1;
   if (r.greedy) {
@@ -327,34 +409,77 @@ __global__ void __launch_bounds__(THREADS) verify_draw_kernel(VerifyArgs a) {
     const Span<T> sp(row, lo, hi);
     constexpr int VN = Span<T>::VN;
     Best s{0.f, 0x7fffffff}, f{0.f, 0x7fffffff};  // of the residual; of p, should that be empty
-    const float inv_z = 1.f / z;
-    auto one = [&](int j, float l, float nz, float qj) {
-      const float e = weight_any(l, m, r.c);
+    const float inv_z = 1.f / z, ref = m * r.c;
+    const bool plain = fabsf(ref) < HUGE_REF;  // (m is finite, so only a NaN logit needs more)
+    // weight over noise: of the residual, and of p
+    auto pair = [&](int j, float l, float nz, float qj, float &of_s, float &of_f) {
+      const float e = plain ? ex2(fmaf(l, r.c, -ref)) : weight_any(l, m, r.c);
       if (Q && q) {
-        take(s, fmaxf(e * inv_z - fmaxf(qj, 0.f), 0.f), nz, j);
-        take(f, e, nz, j);
+        of_s = ratio(fmaxf(__fmaf_rn(e, inv_z, -fmaxf(qj, 0.f)), 0.f), nz);
+        of_f = ratio(e, nz);
       } else {
-        take(s, j == x ? 0.f : e, nz, j);
+        of_s = j == x ? 0.f : ratio(e, nz);
+        of_f = 0.f;
       }
     };
     if (tid < 2 * VN) {
       const int e = sp.edge(tid);
-      if (e >= 0) one(e, to_f32(row[e]), noise[e], Q && q ? q[e] : 0.f);
+      if (e >= 0) {
+        float u, w;
+        pair(e, to_f32(row[e]), noise[e], Q && q ? q[e] : 0.f, u, w);
+        if (u > 0.f) s = Best{u, e};
+        if (w > 0.f) f = Best{w, e};
+      }
     }
     const uint4 *vec = reinterpret_cast<const uint4 *>(row + sp.v0);
     const bool nz16 = (((uintptr_t)(noise + sp.v0)) & 15) == 0;
     const bool q16 = Q && q && (((uintptr_t)(q + sp.v0)) & 15) == 0;
-    for (int v = tid; v < sp.nvec; v += THREADS) {
+    int at_s = -1, at_f = -1;  // the vectors that hold the best
+    auto load = [&](int v, uint4 &raw, float (&nz)[VN], float (&qv)[VN]) {
+      raw = __ldcs(vec + v);
+      load_f32<VN>(noise + sp.v0 + v * VN, nz16, nz);
+      if (Q && q) load_f32<VN>(q + sp.v0 + v * VN, q16, qv);
+    };
+    auto take = [&](int v, const uint4 &raw, const float (&nz)[VN], const float (&qv)[VN]) {
       const int j0 = sp.v0 + v * VN;
-      const uint4 raw = __ldcs(vec + v);
-      float nz[VN], qv[VN];
-      load_f32<VN>(noise + j0, nz16, nz);
-      if (Q && q) load_f32<VN>(q + j0, q16, qv);
-      float l[VN];
+      float l[VN], top_s = 0.f, top_f = 0.f;
       unpack<T>(raw, l);
 #pragma unroll
-      for (int e = 0; e < VN; ++e) one(j0 + e, l[e], nz[e], Q && q ? qv[e] : 0.f);
+      for (int e = 0; e < VN; ++e) {
+        float u, w;
+        pair(j0 + e, l[e], nz[e], Q && q ? qv[e] : 0.f, u, w);
+        top_s = fmaxf(top_s, u);
+        if (Q) top_f = fmaxf(top_f, w);
+      }
+      if (top_s > s.w || (top_s == s.w && s.arg != 0x7fffffff && j0 < s.arg)) {
+        s = Best{top_s, j0};
+        at_s = v;
+      }
+      if (Q && (top_f > f.w || (top_f == f.w && f.arg != 0x7fffffff && j0 < f.arg))) {
+        f = Best{top_f, j0};
+        at_f = v;
+      }
+    };
+    for (int v = tid; v < sp.nvec; v += 2 * THREADS) {
+      uint4 raw[2];
+      float nz[2][VN], qv[2][VN];
+      const bool more = v + THREADS < sp.nvec;
+      load(v, raw[0], nz[0], qv[0]);
+      if (more) load(v + THREADS, raw[1], nz[1], qv[1]);
+      take(v, raw[0], nz[0], qv[0]);
+      if (more) take(v + THREADS, raw[1], nz[1], qv[1]);
     }
+    // the best's own index: the lowest of its vector that has its value
+    auto index = [&](int v, bool residual, Best &best) {
+      for (int e = VN - 1; e >= 0; --e) {
+        const int j = sp.v0 + v * VN + e;
+        float u, w;
+        pair(j, to_f32(row[j]), noise[j], Q && q ? q[j] : 0.f, u, w);
+        if ((residual ? u : w) == best.w) best.arg = j;
+      }
+    };
+    if (at_s >= 0) index(at_s, true, s);
+    if (Q && at_f >= 0) index(at_f, false, f);
     s = better_warp(s);
     if (Q) f = better_warp(f);
     if ((tid & 31) == 0) {
@@ -362,32 +487,19 @@ __global__ void __launch_bounds__(THREADS) verify_draw_kernel(VerifyArgs a) {
       if (Q) sh[1][tid >> 5] = f;
     }
     __syncthreads();
+    reached();
+    if (tid < 32) {
+      s = better_warp(tid < THREADS / 32 ? sh[0][tid] : Best{0.f, 0x7fffffff});
+      if (Q) f = better_warp(tid < THREADS / 32 ? sh[1][tid] : Best{0.f, 0x7fffffff});
+    }
+    if (tid == 0) give(parts + split, make_float4(s.w, __int_as_float(s.arg), f.w, __int_as_float(f.arg)));
+    done();
+    if (split != 0) return;
+    all_done();
     if (tid >= 32) return;
-    s = tid < THREADS / 32 ? sh[0][tid] : Best{0.f, 0x7fffffff};
-    s = better_warp(s);
-    if (Q) {
-      f = tid < THREADS / 32 ? sh[1][tid] : Best{0.f, 0x7fffffff};
-      f = better_warp(f);
-    }
-    if (a.draw_splits > 1) {
-      float4 *part = a.draw_part + (long long)b * a.draw_splits;
-      if (tid == 0) {
-        part[split] = make_float4(s.w, __int_as_float(s.arg), f.w, __int_as_float(f.arg));
-        __threadfence();
-        last = atomicInc(a.draw_count + b, (unsigned)a.draw_splits - 1) == (unsigned)a.draw_splits - 1;
-      }
-      __syncwarp();
-      if (!last) return;
-      __threadfence();
-      s = f = Best{0.f, 0x7fffffff};
-      for (int j = tid; j < a.draw_splits; j += 32) {
-        const float4 p = __ldcg(part + j);
-        s = better(s, Best{p.x, __float_as_int(p.y)});
-        f = better(f, Best{p.z, __float_as_int(p.w)});
-      }
-      s = better_warp(s);
-      f = better_warp(f);
-    }
+    const float4 p = tid < a.draw_splits ? parts[tid] : make_float4(0.f, __int_as_float(0x7fffffff), 0.f, __int_as_float(0x7fffffff));
+    s = better_warp(Best{p.x, __float_as_int(p.y)});
+    f = better_warp(Best{p.z, __float_as_int(p.w)});
     if (s.w > 0.f) {
       token = s.arg;
     } else if (Q && q && f.w > 0.f) {
@@ -403,51 +515,56 @@ __global__ void __launch_bounds__(THREADS) verify_draw_kernel(VerifyArgs a) {
   }
 }
 
+template <typename K>
+cudaError_t launch_clusters(K *kernel, const VerifyArgs &a, long long rows, int splits, bool early, cudaStream_t st) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(rows * splits));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <typename T>
 cudaError_t launch(const VerifyArgs &a, cudaStream_t st) {
-  const unsigned stats = (unsigned)((long long)a.B * (a.k + 1) * a.splits);
-  verify_stats_kernel<T><<<stats, THREADS, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_clusters(verify_stats_kernel<T>, a, (long long)a.B * (a.k + 1), a.splits, false, st);
   if (e != cudaSuccess) return e;
-  const unsigned draws = (unsigned)(a.B * a.draw_splits);
-  if (a.q)
-    verify_draw_kernel<T, true><<<draws, THREADS, 0, st>>>(a);
-  else
-    verify_draw_kernel<T, false><<<draws, THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_clusters(a.q ? verify_draw_kernel<T, true> : verify_draw_kernel<T, false>, a, a.B, a.draw_splits,
+                         true, st);
+}
+
+// A power of two: CTAs enough to fill the GPU where there are few rows, and
+// pieces of at least 2048 elements, a 16-byte load per thread.
+int splits_of(long long ctas, long long rows, int V) {
+  int s = 1;
+  while (s < MAX_SPLITS && rows * s < ctas && V > 2048 * s) s *= 2;
+  return s;
 }
 
 }  // namespace
 
-// CTAs that a launch is split into where there are fewer rows than that.
-constexpr long long VERIFY_CTAS = 152 * 64;
-constexpr int VERIFY_MAX_SPLITS = 64;
-
-int verify_splits(long long rows, int V) {
-  long long s = (VERIFY_CTAS + rows - 1) / rows;
-  s = s < VERIFY_MAX_SPLITS ? s : VERIFY_MAX_SPLITS;
-  const long long most = (V + 2047) / 2048;  // 2048 elements: one 16-byte load per thread
-  s = s < most ? s : most;
-  return s < 1 ? 1 : (int)s;
-}
-
 VerifyLayout verify_layout(int max_batch, int k) {
   VerifyLayout l;
-  const size_t pos = (size_t)max_batch * (k + 1);
-  l.part = 0;
-  l.draw_part = l.part + (VERIFY_CTAS + pos) * 16;
-  l.stat = l.draw_part + (VERIFY_CTAS + (size_t)max_batch) * 16;
-  l.count = l.stat + pos * 16;
-  l.draw_count = l.count + pos * 4;
-  l.stop = l.draw_count + (size_t)max_batch * 4;
+  l.stat = 0;
+  l.stop = (size_t)max_batch * (k + 1) * 16;
   l.bytes = l.stop + (size_t)max_batch * 4;
   return l;
 }
 
 cudaError_t launch_verify(const VerifyArgs &args, int dtype, cudaStream_t st) {
   VerifyArgs a = args;
-  a.splits = verify_splits((long long)a.B * (a.k + 1), a.V);
-  a.draw_splits = verify_splits(a.B, a.V);
+  // The statistics go in small pieces also where there are many positions: the
+  // sooner one is decided, the fewer after it are begun.
+  a.splits = splits_of(152 * 64, (long long)a.B * (a.k + 1), a.V);
+  a.draw_splits = splits_of(152 * 16, a.B, a.V);
   if (dtype == SGD_F32) return launch<float>(a, st);
   if (dtype == SGD_F16) return launch<__half>(a, st);
   return launch<__nv_bfloat16>(a, st);
