@@ -67,6 +67,33 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = to_f32(t[i]);
   }
+  // The largest magnitude so far (NaN once there is one): two values at a time
+  // where they have 16 bits.
+  using Top = typename std::conditional<sizeof(T) == 4, float, uint32_t>::type;
+  __device__ __forceinline__ void top(Top &m) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(__uint_as_float(w[i]))));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __half>::value)
+          asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+        else
+          asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+      }
+    }
+  }
+  __device__ __forceinline__ static float top_value(Top m) {
+    if constexpr (sizeof(T) == 4) {
+      return m;
+    } else {
+      T t[2];
+      memcpy(t, &m, 4);
+      const float a = to_f32(t[0]), b = to_f32(t[1]);
+      return a != a ? a : fmaxf(b, a == a && b == b ? a : b);
+    }
+  }
 };
 
 __device__ __forceinline__ void decode8(uint2 r, float (&x)[8]) {
@@ -182,23 +209,26 @@ __device__ Segment segment_of(const int32_t *starts, int B, int N, const int32_t
   return g;
 }
 
-// The largest magnitude among 16 e4m3 bytes, as a byte (NaN codes count as 0).
-__device__ __forceinline__ uint32_t top_bytes(uint32_t top, const uint4 &v) {
+// The larger magnitudes of 16 e4m3 bytes and what is there (NaN codes drop out).
+__device__ __forceinline__ __half2 top_of(__half2 top, const uint4 &v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t x = w[i] & 0x7f7f7f7fu;
-    top = __vmaxu4(top, x & ~__vcmpeq4(x, 0x7f7f7f7fu));
+    uint32_t x, y;
+    e4m3x4_to_f16x4(w[i], x, y);
+    top = __hmax2(top, __habs2(*reinterpret_cast<const __half2 *>(&x)));
+    top = __hmax2(top, __habs2(*reinterpret_cast<const __half2 *>(&y)));
   }
   return top;
 }
 
-// A warp takes one head's keys or values of a segment: the largest magnitude
-// first (new entries, and the block's older ones), then the encoding.  The
-// second reading of the new entries finds them in L1.  Bound by latency at the
-// few tokens of a verification step, by the bytes at prompts.
+// A team of warps (one, or as many as keep a page's new entries in registers)
+// takes one head's keys or values of a segment: the largest magnitude first, of
+// the new entries and the block's older ones, then the encoding.  Bound by
+// latency at the few tokens of a verification step, by the bytes at prompts.
 template <typename T, int D>
-__global__ void __launch_bounds__(THREADS) kv_write_kernel(KvWriteArgs a) {
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 3 : 4) kv_write_kernel(KvWriteArgs a) {
+  __shared__ float team_max[2][WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int P = a.c.page;
   uint32_t bits = 0;
@@ -206,96 +236,114 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(KvWriteArgs a) {
       a.r.q_start, a.r.B, a.r.N, a.r.table, a.r.max_pages, a.c.num_pages, P, blockIdx.x,
       [&](int b, int ql) { return min(__ldg(a.r.seq_lens + b) - ql, PAST); }, &bits);
   constexpr int PER = D / 8, STEP = 32 / PER, UNROLL = 4;  // lanes of a token, tokens of a round
+  constexpr int ROUND = STEP * UNROLL;
   const int sub = lane % PER, at = lane / PER;
-  for (int hv = blockIdx.y * WARPS + warp; g.page >= 0 && hv < 2 * a.c.heads; hv += gridDim.y * WARPS) {
+  const int teams = WARPS / a.team, mate = warp % a.team;
+  int turn = 0;
+  for (int hv0 = blockIdx.y * teams; g.count > 0 && hv0 < 2 * a.c.heads; hv0 += gridDim.y * teams, turn ^= 1) {
+    const int hv = hv0 + warp / a.team;
+    const bool idle = hv >= 2 * a.c.heads;  // (its warps only keep the others' barriers)
     const bool value = hv >= a.c.heads;
-    const int h = value ? hv - a.c.heads : hv;
+    const int h = idle ? 0 : value ? hv - a.c.heads : hv;
+    const int count = idle ? 0 : g.count;
     const long long token = value ? a.v_token : a.k_token;
     const T *src = static_cast<const T *>(value ? a.v : a.k) + (long long)h * (value ? a.v_head : a.k_head) +
                    (long long)g.first * token + sub * 8;
+    Eight<T> x[UNROLL];
+    auto fetch = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i)
+        if (t0 + i * STEP + at < count) x[i].load(src + (t0 + i * STEP + at) * token, a.vec);
+    };
+    fetch(mate * ROUND);  // (on its way before the page is known)
+    if (g.page < 0) break;
     const long long block = (long long)g.page * a.c.heads + h;
     uint8_t *base = (value ? a.c.v : a.c.k) + block * P * D;
     float *scale = (value ? a.c.vs : a.c.ks) + block;
     const float old = g.slot > 0 ? *scale : 1.f;
-    float amax = 0.f;
-    for (int t0 = 0; t0 < g.count; t0 += STEP * UNROLL) {
-      Eight<T> x[UNROLL];
+    __half2 top = __float2half2_rn(0.f);
+    const int n_old = idle ? 0 : g.slot * D / 16;
+    for (int i0 = mate * 32 * 4; i0 < n_old; i0 += a.team * 32 * 4) {
+      uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < UNROLL; ++i) {
-        const int t = t0 + i * STEP + at;
-        if (t < g.count) x[i].load(src + t * token, a.vec);
+      for (int i = 0; i < 4; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (i0 + i * 32 + lane < n_old) v[i] = *reinterpret_cast<const uint4 *>(base + (i0 + i * 32 + lane) * 16);
       }
 #pragma unroll
-      for (int i = 0; i < UNROLL; ++i) {
-        if (t0 + i * STEP + at >= g.count) continue;
-        float v[8];
-        x[i].get(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float m = fabsf(v[e]);
-          if (!(m < CUDART_INF_F))
-            bits |= SGD_KV_ERR_NONFINITE;
-          else
-            amax = fmaxf(amax, m);
-        }
-      }
+      for (int i = 0; i < 4; ++i) top = top_of(top, v[i]);
     }
-    if (g.slot > 0) {
-      uint32_t top = 0;
-      const int n = g.slot * D / 16;
-      for (int i0 = 0; i0 < n; i0 += 32 * 8) {
-        uint4 v[8];
+    float amax = fmaxf(__low2float(top), __high2float(top)) * old;
+    typename Eight<T>::Top all = 0;
+    for (int t0 = mate * ROUND; t0 < count; t0 += a.team * ROUND) {
+      if (t0 != mate * ROUND) fetch(t0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (i0 + i * 32 + lane < n) v[i] = *reinterpret_cast<const uint4 *>(base + (i0 + i * 32 + lane) * 16);
+      for (int i = 0; i < UNROLL; ++i)
+        if (t0 + i * STEP + at < count) x[i].top(all);
+    }
+    const float new_max = Eight<T>::top_value(all);
+    const bool finite = new_max < CUDART_INF_F;
+    if (finite) {
+      amax = fmaxf(amax, new_max);
+    } else {  // without what is not
+      bits |= SGD_KV_ERR_NONFINITE;
+      for (int t = mate * ROUND + at; t < count; t += t % ROUND + STEP < ROUND ? STEP : (a.team - 1) * ROUND + STEP)
+        for (int e = 0; e < 8; ++e) {
+          const float m = fabsf(to_f32(src[t * token + e]));
+          if (m < CUDART_INF_F) amax = fmaxf(amax, m);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = top_bytes(top, v[i]);
-      }
-      top = max(max(top & 0xff, top >> 8 & 0xff), max(top >> 16 & 0xff, top >> 24));
-      const uint32_t f = e4m3x2_to_f16x2(top);
-      amax = fmaxf(amax, __low2float(*reinterpret_cast<const __half2 *>(&f)) * old);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
+    if (a.team > 1) {
+      if (lane == 0) team_max[turn][warp] = amax;
+      __syncthreads();
+      for (int w = warp - mate; w < warp - mate + a.team; ++w) amax = fmaxf(amax, team_max[turn][w]);
+    }
     const int e = scale_exp(amax);
     const float s_new = pow2(e), inv = pow2(-e);
-    if (lane == 0) *scale = s_new;
-    for (int t0 = 0; t0 < g.count; t0 += STEP * UNROLL) {
-      Eight<T> x[UNROLL];
+    if (lane == 0 && mate == 0 && !idle) *scale = s_new;
+    for (int t0 = mate * ROUND; t0 < count; t0 += a.team * ROUND) {
+      if (count > a.team * ROUND) fetch(t0);
 #pragma unroll
       for (int i = 0; i < UNROLL; ++i) {
         const int t = t0 + i * STEP + at;
-        if (t < g.count) x[i].load(src + t * token, a.vec);
-      }
-#pragma unroll
-      for (int i = 0; i < UNROLL; ++i) {
-        const int t = t0 + i * STEP + at;
-        if (t >= g.count) continue;
+        if (t >= count) continue;
         float v[8];
         x[i].get(v);
+        if (!finite) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] : 0.f;
+          for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] : 0.f;
+        }
         *reinterpret_cast<uint2 *>(base + (g.slot + t) * D + sub * 8) = encode8(v, inv);
       }
     }
-    if (g.slot > 0 && s_new != old) {
-      for (int i = lane; i < g.slot * D / 8; i += 32) {
-        uint2 *p = reinterpret_cast<uint2 *>(base + i * 8);
-        float v[8];
-        decode8(*p, v);
+    if (g.slot > 0 && !idle && s_new != old) {
+      const int n = g.slot * D / 8;
+      for (int i0 = mate * 32 * 4; i0 < n; i0 += a.team * 32 * 4) {
+        uint2 w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] * old : 0.f;
-        *p = encode8(v, inv);
+        for (int i = 0; i < 4; ++i)
+          if (i0 + i * 32 + lane < n) w[i] = *reinterpret_cast<const uint2 *>(base + (i0 + i * 32 + lane) * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i0 + i * 32 + lane >= n) continue;
+          float v[8];
+          decode8(w[i], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] * old : 0.f;
+          *reinterpret_cast<uint2 *>(base + (i0 + i * 32 + lane) * 8) = encode8(v, inv);
+        }
       }
     }
   }
   if (bits) atomicOr(a.err, bits);
 }
 
-// A warp takes one head's keys or values of a segment, 16 bytes a lane; bound
-// by the bytes written.
+// A warp takes one head's keys or values of a segment, 16 bytes a lane, four
+// loads in flight; bound by the bytes written.
+template <int D>
+constexpr int READ_ROUND = 4 * 32 * 16 / D;  // tokens of a warp's round
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvReadArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -309,11 +357,11 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvReadArgs a) {
   if (claimed < a.N) {
     bits |= SGD_KV_ERR_LENGTH;
     const long long width = (long long)a.c.heads * D;
-    for (long long i = claimed * width + (long long)(blockIdx.y * gridDim.x + blockIdx.x) * THREADS + threadIdx.x;
-         i < a.N * width; i += (long long)gridDim.x * gridDim.y * THREADS)
+    for (long long i = claimed * width + ((long long)(blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * THREADS + threadIdx.x;
+         i < a.N * width; i += (long long)gridDim.x * gridDim.y * gridDim.z * THREADS)
       static_cast<T *>(a.k)[i] = static_cast<T *>(a.v)[i] = from_f32<T>(0.f);
   }
-  constexpr int PER = D / 16, STEP = 32 / PER, UNROLL = 4;
+  constexpr int PER = D / 16, STEP = 32 / PER, UNROLL = READ_ROUND<D> / STEP;  // 4
   const int sub = lane % PER, at = lane / PER;
   for (int hv = blockIdx.y * WARPS + warp; hv < 2 * a.c.heads; hv += gridDim.y * WARPS) {
     const bool value = hv >= a.c.heads;
@@ -322,7 +370,7 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvReadArgs a) {
     const uint8_t *base = (value ? a.c.v : a.c.k) + (block * P + g.slot) * D + sub * 16;
     const float s = g.page >= 0 ? (value ? a.c.vs : a.c.ks)[block] : 0.f;
     T *out = static_cast<T *>(value ? a.v : a.k) + ((long long)g.first * a.c.heads + h) * D + sub * 16;
-    for (int t0 = 0; t0 < g.count; t0 += STEP * UNROLL) {
+    for (int t0 = blockIdx.z * READ_ROUND<D>; t0 < g.count; t0 += gridDim.z * READ_ROUND<D>) {
       uint4 raw[UNROLL];
 #pragma unroll
       for (int i = 0; i < UNROLL; ++i) {
@@ -361,14 +409,22 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvReadArgs a) {
 
 // CTAs for B rows of N tokens: a row of n tokens touches at most n / page + 2
 // pages, and 1 if it is one token.
-dim3 segments(int B, int N, const KvView &c) {
+unsigned segments(int B, int N, const KvView &c) {
   const long long few = (long long)N, many = (long long)N / c.page + 2LL * B;
-  return dim3((unsigned)(few < many ? few : many), (unsigned)((2 * c.heads + WARPS - 1) / WARPS));
+  return (unsigned)(few < many ? few : many);
 }
 
 template <typename T>
-cudaError_t write(const KvWriteArgs &a, cudaStream_t st) {
-  const dim3 grid = segments(a.r.B, a.r.N, a.c);
+cudaError_t write(KvWriteArgs a, cudaStream_t st) {
+  // Rows of a page's tokens or more on average: a page in a team's registers.
+  // Measured at 8 rows of 8192 (8 heads, dim 128, pages of 64): teams of one
+  // 50 us, of four 43; a step of 1..17 tokens takes teams of one.
+  a.team = 1;
+  if (a.r.N / a.r.B >= a.c.page)
+    while (a.team < WARPS && a.team * 1024 < a.c.page * a.c.dim) a.team *= 2;
+  const unsigned x = segments(a.r.B, a.r.N, a.c);
+  const unsigned teams = WARPS / a.team;
+  const dim3 grid(x, (2 * a.c.heads + teams - 1) / teams);
   if (a.c.dim == 128)
     kv_write_kernel<T, 128><<<grid, THREADS, 0, st>>>(a);
   else
@@ -376,14 +432,19 @@ cudaError_t write(const KvWriteArgs &a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <typename T, int D>
+cudaError_t read(const KvReadArgs &a, cudaStream_t st) {
+  const unsigned x = segments(a.B, a.N, a.c), y = (2 * a.c.heads + WARPS - 1) / WARPS;
+  // Each CTA finds its segment first: a segment's tokens are split over CTAs
+  // only where the GPU would not be full otherwise.
+  const unsigned rounds = x * y < 152 * 4 ? (a.c.page + READ_ROUND<D> - 1) / READ_ROUND<D> : 1;
+  kv_read_kernel<T, D><<<dim3(x, y, rounds), THREADS, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t read(const KvReadArgs &a, cudaStream_t st) {
-  const dim3 grid = segments(a.B, a.N, a.c);
-  if (a.c.dim == 128)
-    kv_read_kernel<T, 128><<<grid, THREADS, 0, st>>>(a);
-  else
-    kv_read_kernel<T, 64><<<grid, THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return a.c.dim == 128 ? read<T, 128>(a, st) : read<T, 64>(a, st);
 }
 
 }  // namespace

@@ -31,6 +31,7 @@ struct KvWriteArgs {
   const void *k, *v;
   long long k_token, k_head, v_token, v_head;  // strides in elements
   int vec;                                     // 16-byte loads allowed
+  int team;                                    // warps of a block (chosen at the launch)
   uint32_t *err;
 };
 

@@ -245,11 +245,17 @@ __global__ void __launch_bounds__(THREADS, PER_SM) verify_stats_kernel(VerifyArg
   }
   const float edge_m = s.m;
   const uint4 *vec = reinterpret_cast<const uint4 *>(row + sp.v0);
-  for (int v = tid; v < sp.nvec; v += UNROLL * THREADS) {
-    uint4 raw[UNROLL];
+  uint4 raw[UNROLL], ahead[UNROLL];  // the next group is on its way while one is worked on
+  auto fetch = [&](int v) {
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j)
-      raw[j] = v + j * THREADS < sp.nvec ? __ldcs(vec + v + j * THREADS) : lowest_vec<T>();
+      ahead[j] = v + j * THREADS < sp.nvec ? __ldcs(vec + v + j * THREADS) : lowest_vec<T>();
+  };
+  fetch(tid);
+  for (int v = tid; v < sp.nvec; v += UNROLL * THREADS) {
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) raw[j] = ahead[j];
+    if (v + UNROLL * THREADS < sp.nvec) fetch(v + UNROLL * THREADS);
     const float mx = max_of<T, UNROLL>(raw);
     if (mx > s.m) {
       s.z = s.z == 0.f ? 0.f : s.z * reweight(s.m, mx, r.c);
@@ -541,11 +547,14 @@ cudaError_t launch(const VerifyArgs &a, cudaStream_t st) {
                          true, st);
 }
 
-// A power of two: CTAs enough to fill the GPU where there are few rows, and
-// pieces of at least 2048 elements, a 16-byte load per thread.
-int splits_of(long long ctas, long long rows, int V) {
+// CTAs of a row of logits: a power of two, until there are three CTAs per SM,
+// in pieces of at least 2048 elements (a 16-byte load per thread).  Measured
+// at V = 151936, B = 256, k = 16: 1 piece 142 us, 2 150, 4 182, 8 269 (each CTA
+// costs its start and its joining); at V = 128256, B = 48, k = 5, 32-bit logits:
+// 1 piece 48 us, 2 41, 8 44; at V = 32000, B = 4, k = 8: 1 piece 11.5 us, 8 10.5.
+int splits_of(long long rows, int V) {
   int s = 1;
-  while (s < MAX_SPLITS && rows * s < ctas && V > 2048 * s) s *= 2;
+  while (s < MAX_SPLITS && rows * s < 152 * 3 && V > 2048 * s) s *= 2;
   return s;
 }
 
@@ -561,10 +570,8 @@ VerifyLayout verify_layout(int max_batch, int k) {
 
 cudaError_t launch_verify(const VerifyArgs &args, int dtype, cudaStream_t st) {
   VerifyArgs a = args;
-  // The statistics go in small pieces also where there are many positions: the
-  // sooner one is decided, the fewer after it are begun.
-  a.splits = splits_of(152 * 64, (long long)a.B * (a.k + 1), a.V);
-  a.draw_splits = splits_of(152 * 16, a.B, a.V);
+  a.splits = splits_of((long long)a.B * (a.k + 1), a.V);
+  a.draw_splits = splits_of(a.B, a.V);
   if (dtype == SGD_F32) return launch<float>(a, st);
   if (dtype == SGD_F16) return launch<__half>(a, st);
   return launch<__nv_bfloat16>(a, st);
