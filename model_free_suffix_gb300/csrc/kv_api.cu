@@ -165,6 +165,7 @@ int sgd_kv_attend(sgd_kv *x, const sgd_kv_layer *layer, const void *q, int32_t d
   a.q = q;
   a.q_token = q_token_stride;
   a.q_head = q_head_stride;
+  a.q_vec = aligned(q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
   a.out = out;
   a.q_heads = x->cfg.q_heads;
   a.group = x->cfg.q_heads / x->cfg.kv_heads;

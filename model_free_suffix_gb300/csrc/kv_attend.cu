@@ -6,7 +6,8 @@
 //
 // One pass over keys and values with a running maximum m and sum l per row: a
 // tile's products s give m' = max(m, max s), and l and o are scaled by
-// 2^(m - m') before the tile's 2^(s - m') are added (s in units of log 2).
+// 2^(m - m') before the tile's 2^(s - m') are added (kv_attend.cuh has the
+// scales of the blocks, and when this scaling is due).
 // Rows of the query heads that share a head of keys and values go together, so
 // that each byte of the cache is read once for all of them.
 #include <math_constants.h>
@@ -14,6 +15,7 @@
 #include <type_traits>
 
 #include "async_copy.cuh"
+#include "kv_attend.cuh"
 #include "kv_internal.h"
 #include "kv_sched.cuh"
 #include "num_types.cuh"
@@ -22,11 +24,9 @@
 namespace sgd {
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
-constexpr int MAX_CTAS = 152 * 3;
-constexpr float LAZY = 8.f;  // o and l are scaled once the maximum has grown by 2^8
+constexpr int KV_TILE = 32;  // tokens
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -47,15 +47,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// 2^e for e in [-126, 127]
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-
-// Where the parts of split units and their counters lie in the workspace.
-template <int M, int D>
-__device__ __forceinline__ float *part_of(const KvAttendArgs &a, int slot) {
-  return reinterpret_cast<float *>(a.work + MAX_CTAS * 8) + (long long)slot * (M * (D + 2));
-}
-
 // Few rows (M = 16 MT <= 32 a unit), bound by reading the cache.  Each warp
 // streams its own 32-token tiles through a ring of TMA loads, S deep, and keeps
 // m, l and o of all the unit's rows in registers; warps meet only where a unit
@@ -63,10 +54,8 @@ __device__ __forceinline__ float *part_of(const KvAttendArgs &a, int slot) {
 // feed the matrix instructions, so the products carry no rounding of the
 // cache's; q goes to f16 after each row is scaled to [1, 2) by a power of two
 // (bf16 has fewer bits than f16: only elements 2^-24 times the row's largest
-// lose any), and the probabilities to f16 (relative 2^-12 each, in values up to
-// 2^8; the sum l is taken before that rounding).  The scales of a block of
-// keys multiply its products; o is held in units of a recent block's value
-// scale, and probabilities of blocks with another one are scaled by the ratio.
+// lose any), and the probabilities to f16 (relative 2^-12 each; the sum l is
+// taken before that rounding).
 //
 // The order of the elements of a product's long axis is free as long as both
 // sides use the same: a lane takes 2 (D = 128) or 1 (D = 64) whole 16-byte
@@ -88,7 +77,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   uint32_t bits = 0;
-  const KvShare share = kv_share<THREADS>(a, M, WARPS, &bits);
+  const KvShare share = kv_share<THREADS, M, KV_TILE>(a, WARPS, &bits);
   if (share.begin >= share.end) {
     if (bits && tid == 0) atomicOr(a.err, bits);
     return;
@@ -105,26 +94,10 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 
   const int P = a.c.page, H = a.c.heads;
   const int halves = P < KV_TILE ? 2 : 1;  // pages of a tile
-  long long at = share.begin, b_begin = share.b_begin;
-  int b = share.b;
-  KvJob job = kv_job(a, b, M, &bits);
-  while (at < share.end) {
-    while (at >= b_begin + kv_work(job, H)) {
-      b_begin += kv_work(job, H);
-      ++b;
-      job = kv_job(a, b, M, &bits);
-    }
-    // the unit and the range of its tiles that this share holds
-    const int u = (int)((at - b_begin) / job.tiles);
-    const long long u_begin = b_begin + (long long)u * job.tiles, u_end = u_begin + job.tiles;
-    const int t0 = (int)(at - u_begin);
-    const int t1 = (int)(min(u_end, share.end) - u_begin);
-    at = u_begin + t1;
-    const int h = u % H, rt = u / H;
-    const int r0 = rt * M, nrows = min(M, job.ql * a.group - r0);
-    const int p_first = job.n - job.ql + r0 / a.group;
-    const int p_last = job.n - job.ql + (r0 + nrows - 1) / a.group;
-    const int32_t *table = a.r.table + (long long)b * a.r.max_pages;
+  KvWalk<M, KV_TILE> w(a, share, &bits);
+  while (w.next(&bits)) {
+    const KvJob &job = w.job;
+    const int h = w.h, nrows = w.nrows, t0 = w.t0, t1 = w.t1, p_first = w.p_first, p_last = w.p_last;
 
     // ---- this warp's tiles, t0 + warp, + WARPS, ..., 32 at a time: lane i holds
     // what the i-th of them needs.  Those that no row of the unit sees are
@@ -133,29 +106,16 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
       int y[2];   // lines of the tile's page(s) in the maps
       bool on;    // some row sees it
     };
-    auto page_of = [&](int x, int i) {  // of the tile at position x, its i-th page
-      const int block = x / P + i;
-      if (block >= a.r.max_pages || block * P >= job.n) return -1;
-      const int pg = __ldg(table + block);
-      if (pg >= 0 && pg < a.c.num_pages) return pg;
-      bits |= SGD_KV_ERR_PAGE;
-      return -1;
-    };
-    auto seen = [&](int j) {
-      if (j >= t1) return false;
-      const int x = job.tile(j) * KV_TILE;
-      return x <= p_last && (a.window == 0 || x + KV_TILE - 1 > p_first - a.window || x < a.sinks);
-    };
     constexpr int PACK = 128 / D;  // tokens of a 128-byte line
-    auto look = [&](int j, Ahead &w) {
-      w.on = seen(j);
-      w.y[0] = w.y[1] = 0;
-      if (w.on) {
+    auto look = [&](int j, Ahead &t) {
+      t.on = w.seen(j);
+      t.y[0] = t.y[1] = 0;
+      if (t.on) {
         const int x = job.tile(j) * KV_TILE;
-        w.y[0] = ((max(page_of(x, 0), 0) * H + h) * P + (x & (P - 1))) / PACK;
-        if (halves == 2) w.y[1] = (max(page_of(x, 1), 0) * H + h) * P / PACK;
+        t.y[0] = ((max(w.page(x, 0, &bits), 0) * H + h) * P + (x & (P - 1))) / PACK;
+        if (halves == 2) t.y[1] = (max(w.page(x, 1, &bits), 0) * H + h) * P / PACK;
       }
-      return __ballot_sync(FULL, w.on);
+      return __ballot_sync(FULL, t.on);
     };
     Ahead ahead;
     int next = t0 + warp;  // the first tile of the batch being loaded
@@ -185,9 +145,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
     // ---- the unit's queries, as the matrix instructions take them
     for (int r = warp; r < M; r += WARPS) {
       const bool on = r < nrows;
-      const int row = r0 + r;
-      const T *q = static_cast<const T *>(a.q) + (long long)(job.q0 + row / a.group) * a.q_token +
-                   (long long)(h * a.group + row % a.group) * a.q_head;
+      const T *q = static_cast<const T *>(a.q) + w.token(r) * a.q_token + w.q_head(r) * a.q_head;
       float x[4] = {0.f, 0.f, 0.f, 0.f};
       const bool mine = lane * 4 < D;
       if (on && mine) {
@@ -207,9 +165,9 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
       if (mine) {
         constexpr int DPT = D / 4;  // dims of a lane
         const int d = lane * 4, qc = d / DPT, s = d % DPT / 4;
-        const uint32_t w = q_at + (((r / 16) * KS + s) * 32 + (r % 8) * 4 + qc) * 16 + (r % 16) / 8 * 4;
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(w), "r"(pack2<__half>(x[0] * inv, x[1] * inv)) : "memory");
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(w + 8), "r"(pack2<__half>(x[2] * inv, x[3] * inv)) : "memory");
+        const uint32_t to = q_at + (((r / 16) * KS + s) * 32 + (r % 8) * 4 + qc) * 16 + (r % 16) / 8 * 4;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(pack2<__half>(x[0] * inv, x[1] * inv)) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 8), "r"(pack2<__half>(x[2] * inv, x[3] * inv)) : "memory");
       }
     }
     __syncthreads();
@@ -217,7 +175,6 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
     float o[MT][2 * NJ][4];
     float m[MT][2], l[MT][2], f[MT][2];
     int pos[MT][2];
-    float unit = 0.f;  // o is in units of this value scale
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -226,7 +183,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
         m[mt][x] = -CUDART_INF_F;
         l[mt][x] = 0.f;
         f[mt][x] = s_f[r];
-        pos[mt][x] = r < nrows ? job.n - job.ql + (r0 + r) / a.group : -1;
+        pos[mt][x] = r < nrows ? job.n - job.ql + (w.r0 + r) / a.group : -1;
       }
 #pragma unroll
       for (int n = 0; n < 2 * NJ; ++n)
@@ -235,30 +192,32 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
     }
 
     for (int j0 = t0 + warp; j0 < t1; j0 += 32 * WARPS) {
-    float ks[2] = {0.f, 0.f}, vs[2] = {1.f, 1.f};  // (a scale of 0: no such page)
-    bool on = seen(j0 + WARPS * lane);
+    float ks[2] = {0.f, 0.f};           // (a scale of 0: no such page)
+    float lv[2] = {0.f, 0.f}, iv[2] = {1.f, 1.f};  // log2 V, 1 / V
+    bool on = w.seen(j0 + WARPS * lane);
     if (on) {
       const int x = job.tile(j0 + WARPS * lane) * KV_TILE;
       for (int i = 0; i < halves; ++i) {
-        const int pg = page_of(x, i);
+        const int pg = w.page(x, i, &bits);
         if (pg >= 0) {
           ks[i] = __ldg(a.c.ks + (long long)pg * H + h);
-          vs[i] = __ldg(a.c.vs + (long long)pg * H + h);
+          const float vs = __ldg(a.c.vs + (long long)pg * H + h);
+          lv[i] = log2_scale(vs);
+          iv[i] = 1.f / vs;
         }
       }
       if (halves == 1) {
         ks[1] = ks[0];
-        vs[1] = vs[0];
-      } else {
-        if (ks[0] == 0.f) vs[0] = vs[1];
-        if (ks[1] == 0.f) vs[1] = vs[0];
+        lv[1] = lv[0];
+        iv[1] = iv[0];
       }
     }
     for (uint32_t todo = __ballot_sync(FULL, on); todo; todo &= todo - 1) {
       const int src = __ffs(todo) - 1;
       const int x0 = job.tile(j0 + WARPS * src) * KV_TILE;
       const float kh[2] = {__shfl_sync(FULL, ks[0], src), __shfl_sync(FULL, ks[1], src)};
-      const float vh[2] = {__shfl_sync(FULL, vs[0], src), __shfl_sync(FULL, vs[1], src)};
+      const float lh[2] = {__shfl_sync(FULL, lv[0], src), __shfl_sync(FULL, lv[1], src)};
+      const float ih[2] = {__shfl_sync(FULL, iv[0], src), __shfl_sync(FULL, iv[1], src)};
       const uint32_t kt = ring + out_slot * 2 * HALF, vt = kt + HALF;
       if (!bar_wait(bar0 + 8 * out_slot, parity)) bits |= SGD_KV_ERR_WAIT;
       // ---- s = q . k: rows g, g + 8; tokens 8 nt + 2 c, + 1
@@ -304,20 +263,10 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
       }
       // ---- masks, maxima, probabilities
       const bool missing = kh[0] == 0.f || kh[1] == 0.f;
-      const bool edge = missing || x0 + KV_TILE - 1 > p_first ||
-                        (a.window > 0 && x0 <= p_last - a.window && x0 + KV_TILE > a.sinks);
+      const bool edge = missing || w.edge(x0);
       uint32_t pa[MT][2][4];
       float scale_o[MT][2];
-      // the value scale of o's units follows the blocks' where they differ by
-      // more than 2^4: probabilities keep f16's bits
-      const bool two = vh[1] > 16.f * vh[0] || vh[1] < 0.0625f * vh[0];
-      float ratio = 1.f;
-      if (vh[0] > 16.f * unit || vh[0] < 0.0625f * unit) {
-        ratio = unit / vh[0];
-        unit = vh[0];
-      }
-      const float vr[2] = {vh[0] / unit, two ? 1.f : vh[1] / unit};
-      bool rescale = ratio != 1.f;
+      bool rescale = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
@@ -325,7 +274,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] *= fk[e >> 1][nt >> 1];
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] = fmaf(s[mt][nt][e], fk[e >> 1][nt >> 1], lh[nt >> 1]);
         if (edge) {
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt)
@@ -344,7 +293,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
         for (int x = 0; x < 2; ++x) {
           top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 1));
           top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 2));
-          scale_o[mt][x] = ratio;
+          scale_o[mt][x] = 1.f;
           if (top[x] > m[mt][x] + LAZY || (m[mt][x] == -CUDART_INF_F && top[x] > m[mt][x])) {
             const float k = m[mt][x] == -CUDART_INF_F ? 0.f : ex2_approx(m[mt][x] - top[x]);
             l[mt][x] *= k;
@@ -365,15 +314,15 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float p[4][4];
-        const float base[2] = {m[mt][0] == -CUDART_INF_F ? 0.f : m[mt][0],
-                               m[mt][1] == -CUDART_INF_F ? 0.f : m[mt][1]};
+        const float base[2] = {(m[mt][0] == -CUDART_INF_F ? 0.f : m[mt][0]) - LIFT,
+                               (m[mt][1] == -CUDART_INF_F ? 0.f : m[mt][1]) - LIFT};
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float w = ex2_approx(s[mt][nt][e] - base[e >> 1]);
-            l[mt][e >> 1] += w;
-            p[nt][e] = w * vr[nt >> 1];
+            const float y = ex2_approx(s[mt][nt][e] - base[e >> 1]);
+            l[mt][e >> 1] = fmaf(y, ih[nt >> 1], l[mt][e >> 1]);
+            p[nt][e] = y;
           }
 #pragma unroll
         for (int kc = 0; kc < 2; ++kc) {
@@ -399,48 +348,26 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
         }
         __syncwarp();
       }
-      auto add = [&](auto lo, auto hi) {  // blocks of 16 tokens lo .. hi
 #pragma unroll
-        for (int jd = 0; jd < NJ; ++jd) {
-          const int t = (lane >> 3) * 8 + (lane & 7);
-          uint32_t w[4];
-          if (D == 128)
-            ldmatrix_x4_trans(w, vt + t * 128 + ((jd ^ (t & 7)) << 4));
-          else
-            ldmatrix_x4_trans(w, vt + (t >> 1) * 128 + ((((t & 1) * 4 + jd) ^ ((t >> 1) & 7)) << 4));
+      for (int jd = 0; jd < NJ; ++jd) {
+        const int t = (lane >> 3) * 8 + (lane & 7);
+        uint32_t x[4];
+        if (D == 128)
+          ldmatrix_x4_trans(x, vt + t * 128 + ((jd ^ (t & 7)) << 4));
+        else
+          ldmatrix_x4_trans(x, vt + (t >> 1) * 128 + ((((t & 1) * 4 + jd) ^ ((t >> 1) & 7)) << 4));
 #pragma unroll
-          for (int kc = decltype(lo)::value; kc < decltype(hi)::value; ++kc) {
-            uint32_t even[2], odd[2];
+        for (int kc = 0; kc < 2; ++kc) {
+          uint32_t even[2], odd[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              e4m3x4_to_f16x4(__byte_perm(w[2 * kc + i], 0, 0x3120), even[i], odd[i]);
-            }
+          for (int i = 0; i < 2; ++i) e4m3x4_to_f16x4(__byte_perm(x[2 * kc + i], 0, 0x3120), even[i], odd[i]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              if (mt != 0 && mt * 16 >= nrows) continue;
-              mma(o[mt][2 * jd], pa[mt][kc], even[0], even[1]);
-              mma(o[mt][2 * jd + 1], pa[mt][kc], odd[0], odd[1]);
-            }
+          for (int mt = 0; mt < MT; ++mt) {
+            if (mt != 0 && mt * 16 >= nrows) continue;
+            mma(o[mt][2 * jd], pa[mt][kc], even[0], even[1]);
+            mma(o[mt][2 * jd + 1], pa[mt][kc], odd[0], odd[1]);
           }
         }
-      };
-      using std::integral_constant;
-      const integral_constant<int, 0> i0;
-      const integral_constant<int, 1> i1;
-      const integral_constant<int, 2> i2;
-      if (!two) {
-        add(i0, i2);
-      } else {  // (pages of 16 tokens whose value scales are far apart)
-        add(i0, i1);
-        const float k = unit / vh[1];
-        unit = vh[1];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int n = 0; n < 2 * NJ; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][n][e] *= k;
-        add(i1, i2);
       }
       out_slot = out_slot + 1 == S ? 0 : out_slot + 1;
       parity ^= out_slot == 0;
@@ -474,30 +401,29 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 #pragma unroll
           for (int jd = 0; jd < NJ; ++jd)
             *reinterpret_cast<float4 *>(so + r * D + jd * 16 + 4 * c) =
-                make_float4(o[mt][2 * jd][2 * x] * unit, o[mt][2 * jd + 1][2 * x] * unit,
-                            o[mt][2 * jd][2 * x + 1] * unit, o[mt][2 * jd + 1][2 * x + 1] * unit);
+                make_float4(o[mt][2 * jd][2 * x], o[mt][2 * jd + 1][2 * x],
+                            o[mt][2 * jd][2 * x + 1], o[mt][2 * jd + 1][2 * x + 1]);
         }
       }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == job.tiles;
+    const bool whole = w.whole(), starts = t0 == 0;
     T *out = static_cast<T *>(a.out);
-    const bool starts = t0 == 0;
     float *part = part_of<M, D>(a, 2 * blockIdx.x + (starts ? 1 : 0));
     const float *all = reinterpret_cast<const float *>(smem);
     for (int i = tid; i < nrows * (D / 4); i += THREADS) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float top = -CUDART_INF_F;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_m[w][r]);
+      for (int i2 = 0; i2 < WARPS; ++i2) top = fmaxf(top, s_m[i2][r]);
       const float base = top == -CUDART_INF_F ? 0.f : top;
       float sum = 0.f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float k = ex2_approx(s_m[w][r] - base);
-        const float4 v = *reinterpret_cast<const float4 *>(all + (w * M + r) * D + d);
-        if (s_l[w][r] != 0.f) {
-          sum += s_l[w][r] * k;
+      for (int i2 = 0; i2 < WARPS; ++i2) {
+        const float k = ex2_approx(s_m[i2][r] - base);
+        const float4 v = *reinterpret_cast<const float4 *>(all + (i2 * M + r) * D + d);
+        if (s_l[i2][r] != 0.f) {
+          sum += s_l[i2][r] * k;
           x.x += v.x * k;
           x.y += v.y * k;
           x.z += v.z * k;
@@ -506,8 +432,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
       }
       if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int row = r0 + r;
-        T *dst = out + ((long long)(job.q0 + row / a.group) * a.q_heads + h * a.group + row % a.group) * D + d;
+        T *dst = out + ((long long)w.token(r) * a.q_heads + w.q_head(r)) * D + d;
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
       } else {
         *reinterpret_cast<float4 *>(part + r * D + d) = x;
@@ -519,8 +444,8 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
     }
     if (!whole) {
       // ---- the unit's parts together, by the CTA that is last
-      const int g0 = kv_cta_of(share.total, share.ctas, u_begin);
-      const int g1 = kv_cta_of(share.total, share.ctas, u_end - 1);
+      const int g0 = kv_cta_of(share.total, share.ctas, w.u_begin);
+      const int g1 = kv_cta_of(share.total, share.ctas, w.u_end - 1);
       unsigned *count = reinterpret_cast<unsigned *>(a.work) + g0;
       __threadfence();
       __syncthreads();
@@ -569,8 +494,7 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
             x.w += v.w * k;
           }
           const float inv = s_f[r];
-          const int row = r0 + r;
-          T *dst = out + ((long long)(job.q0 + row / a.group) * a.q_heads + h * a.group + row % a.group) * D + d;
+          T *dst = out + ((long long)w.token(r) * a.q_heads + w.q_head(r)) * D + d;
           *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
         }
       }
@@ -584,12 +508,14 @@ __global__ void __launch_bounds__(THREADS) attend_few_kernel(KvAttendArgs a, con
 
 // ---- host --------------------------------------------------------------------
 
+}  // namespace
+
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                  CUtensorMapFloatOOBfill);
 
-EncodeTiled encode_tiled() {
+static EncodeTiled encode_tiled() {
   static const EncodeTiled fn = [] {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -604,9 +530,7 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Keys or values as lines of 128 bytes (one token, or two of 64 bytes), in
-// boxes of `tokens`, with the 128-byte swizzle.
-bool make_map(CUtensorMap *map, const KvView &c, void *base, int tokens) {
+bool kv_make_map(CUtensorMap *map, const KvView &c, void *base, int tokens) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t lines = (cuuint64_t)c.num_pages * c.heads * c.page * c.dim / 128;
@@ -617,6 +541,8 @@ bool make_map(CUtensorMap *map, const KvView &c, void *base, int tokens) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
 template <int D, int MT, int S>
 constexpr int few_smem() {
   return 1024 + WARPS * S * 2 * KV_TILE * D + MT * D / 16 * 512;
@@ -626,7 +552,7 @@ template <typename T, int D, int MT, int S, int PER_SM>
 cudaError_t launch_few(const KvAttendArgs &a, cudaStream_t st) {
   CUtensorMap k, v;
   const int tokens = a.c.page < KV_TILE ? a.c.page : KV_TILE;
-  if (!make_map(&k, a.c, a.c.k, tokens) || !make_map(&v, a.c, a.c.v, tokens)) return cudaErrorInvalidValue;
+  if (!kv_make_map(&k, a.c, a.c.k, tokens) || !kv_make_map(&v, a.c, a.c.v, tokens)) return cudaErrorInvalidValue;
   attend_few_kernel<T, D, MT, S><<<a.sms * PER_SM, THREADS, few_smem<D, MT, S>(), st>>>(a, k, v);
   return cudaGetLastError();
 }
@@ -648,7 +574,9 @@ cudaError_t limits() {
 
 template <typename T>
 cudaError_t attend(const KvAttendArgs &a, cudaStream_t st) {
-  const bool one = (long long)a.max_q * a.group <= 16;
+  const long long rows = (long long)a.max_q * a.group;
+  if (kv_many_rows(a)) return launch_attend_many(a, std::is_same<T, __half>::value ? SGD_F16 : SGD_BF16, st);
+  const bool one = rows <= 16;
   if (a.c.dim == 128) return one ? launch_few<T, 128, 1, 2, 3>(a, st) : launch_few<T, 128, 2, 3, 2>(a, st);
   return one ? launch_few<T, 64, 1, 4, 3>(a, st) : launch_few<T, 64, 2, 6, 2>(a, st);
 }
@@ -656,12 +584,14 @@ cudaError_t attend(const KvAttendArgs &a, cudaStream_t st) {
 }  // namespace
 
 size_t kv_attend_workspace() {
-  return (size_t)MAX_CTAS * 8 + (size_t)MAX_CTAS * 2 * 32 * (128 + 2) * 4;
+  // (the larger of 456 CTAs' parts of up to 32 rows and 152 CTAs' of 128)
+  return (size_t)MAX_CTAS * 8 + (size_t)(MAX_CTAS / 3) * 2 * 128 * (128 + 2) * 4;
 }
 
 cudaError_t kv_attend_set_limits() {
   cudaError_t e = limits<__half>();
   if (e == cudaSuccess) e = limits<__nv_bfloat16>();
+  if (e == cudaSuccess) e = attend_many_limits();
   return e;
 }
 

@@ -48,6 +48,7 @@ struct KvAttendArgs {
   KvRows r;
   const void *q;
   long long q_token, q_head;
+  int q_vec;  // 16-byte loads allowed
   void *out;  // [N, q_heads, dim]
   int q_heads, group;  // group = q_heads / heads
   int max_q;

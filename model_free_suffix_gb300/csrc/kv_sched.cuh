@@ -14,8 +14,6 @@
 
 namespace sgd {
 
-constexpr int KV_TILE = 32;  // tokens
-
 // What one batch row asks for.
 struct KvJob {
   int q0, ql, n;       // first packed token, new tokens, cached tokens
@@ -27,7 +25,9 @@ struct KvJob {
   __device__ __forceinline__ int tile(int j) const { return j < sink_tiles ? j : lo_tile + j - sink_tiles; }
 };
 
-__device__ __forceinline__ KvJob kv_job(const KvAttendArgs &a, int b, int M, uint32_t *bits) {
+// M: rows of a unit; TILE: tokens of a tile.
+template <int M, int TILE>
+__device__ __forceinline__ KvJob kv_job(const KvAttendArgs &a, int b, uint32_t *bits) {
   KvJob r;
   const int q0 = __ldg(a.r.q_start + b), q1 = __ldg(a.r.q_start + b + 1);
   r.n = __ldg(a.r.seq_lens + b);
@@ -48,9 +48,9 @@ __device__ __forceinline__ KvJob kv_job(const KvAttendArgs &a, int b, int M, uin
   const int first = r.n - r.ql;  // position of the first new token
   int lo = 0;
   if (a.window > 0) lo = max(0, first - a.window + 1);
-  r.lo_tile = lo / KV_TILE;
-  r.sink_tiles = min((int)(((long long)min(a.sinks, r.n) + KV_TILE - 1) / KV_TILE), r.lo_tile);
-  r.tiles = r.sink_tiles + (r.n + KV_TILE - 1) / KV_TILE - r.lo_tile;
+  r.lo_tile = lo / TILE;
+  r.sink_tiles = min((int)(((long long)min(a.sinks, r.n) + TILE - 1) / TILE), r.lo_tile);
+  r.tiles = r.sink_tiles + (r.n + TILE - 1) / TILE - r.lo_tile;
   return r;
 }
 
@@ -61,8 +61,7 @@ __device__ __forceinline__ long long kv_work(const KvJob &j, int heads) {
 // A CTA's share [begin, end) of the work, and the batch row where it begins.
 struct KvShare {
   long long begin, end, total;
-  long long per;        // shares are [g * total / ctas, (g + 1) * total / ctas)
-  int ctas;
+  int ctas;             // shares are [g * total / ctas, (g + 1) * total / ctas)
   int b;                // batch row of `begin`
   long long b_begin;    // the work before row b
 };
@@ -78,8 +77,8 @@ __device__ __forceinline__ int kv_cta_of(long long total, int ctas, long long at
 }
 
 // By all threads of the block.  `least`: tiles that make a share worth a CTA.
-template <int THREADS>
-__device__ KvShare kv_share(const KvAttendArgs &a, int M, int least, uint32_t *bits) {
+template <int THREADS, int M, int TILE>
+__device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
   __shared__ long long s_warp[THREADS / 32];
   __shared__ long long s_before;
   __shared__ int s_b;
@@ -87,7 +86,7 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int M, int least, uint32_t *b
   const int per = (a.r.B + THREADS - 1) / THREADS;
   const int b0 = min(a.r.B, tid * per), b1 = min(a.r.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += kv_work(kv_job(a, b, M, bits), a.c.heads);
+  for (int b = b0; b < b1; ++b) mine += kv_work(kv_job<M, TILE>(a, b, bits), a.c.heads);
   long long scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -116,7 +115,7 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int M, int least, uint32_t *b
   s.end = kv_cut(total, s.ctas, g + 1);
   if (before <= s.begin && s.begin < before + mine) {
     for (int b = b0; b < b1; ++b) {
-      const long long w = kv_work(kv_job(a, b, M, bits), a.c.heads);
+      const long long w = kv_work(kv_job<M, TILE>(a, b, bits), a.c.heads);
       if (s.begin < before + w) {
         s_b = b;
         s_before = before;
@@ -130,5 +129,67 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int M, int least, uint32_t *b
   s.b_begin = s_before;
   return s;
 }
+
+// A share's segments: the units it holds or cuts, each with its range of tiles.
+template <int M, int TILE>
+struct KvWalk {
+  const KvAttendArgs &a;
+  const KvShare &share;
+  long long at, b_begin;
+  int b;
+  KvJob job;
+  // of the current segment
+  long long u_begin, u_end;  // its unit's place in all the work
+  int h, r0, nrows;          // head, first row of the unit, rows
+  int t0, t1;                // tiles of the list
+  int p_first, p_last;       // positions of the first and the last row's token
+
+  __device__ KvWalk(const KvAttendArgs &a_, const KvShare &s, uint32_t *bits)
+      : a(a_), share(s), at(s.begin), b_begin(s.b_begin), b(s.b), job(kv_job<M, TILE>(a_, s.b, bits)) {}
+
+  __device__ bool next(uint32_t *bits) {
+    if (at >= share.end) return false;
+    while (at >= b_begin + kv_work(job, a.c.heads)) {
+      b_begin += kv_work(job, a.c.heads);
+      ++b;
+      job = kv_job<M, TILE>(a, b, bits);
+    }
+    const int u = (int)((at - b_begin) / job.tiles);
+    u_begin = b_begin + (long long)u * job.tiles;
+    u_end = u_begin + job.tiles;
+    t0 = (int)(at - u_begin);
+    t1 = (int)(min(u_end, share.end) - u_begin);
+    at = u_begin + t1;
+    h = u % a.c.heads;
+    r0 = u / a.c.heads * M;
+    nrows = min(M, job.ql * a.group - r0);
+    p_first = job.n - job.ql + r0 / a.group;
+    p_last = job.n - job.ql + (r0 + nrows - 1) / a.group;
+    return true;
+  }
+  __device__ bool whole() const { return t0 == 0 && t1 == job.tiles; }
+  // whether some row of the unit sees some token of tile j of the list
+  __device__ bool seen(int j) const {
+    if (j >= t1) return false;
+    const int x = job.tile(j) * TILE;
+    return x <= p_last && (a.window == 0 || x + TILE - 1 > p_first - a.window || x < a.sinks);
+  }
+  // whether some row does not see some token of the tile at x
+  __device__ bool edge(int x) const {
+    return x + TILE - 1 > p_first || (a.window > 0 && x <= p_last - a.window && x + TILE > a.sinks);
+  }
+  // the page of the tile at x, its i-th; -1: none (reported where it should be there)
+  __device__ int page(int x, int i, uint32_t *bits) const {
+    const int block = x / a.c.page + i;
+    if (block >= a.r.max_pages || block * a.c.page >= job.n) return -1;
+    const int pg = __ldg(a.r.table + (long long)b * a.r.max_pages + block);
+    if (pg >= 0 && pg < a.c.num_pages) return pg;
+    *bits |= SGD_KV_ERR_PAGE;
+    return -1;
+  }
+  // token and query head of row r of the unit
+  __device__ int token(int r) const { return job.q0 + (r0 + r) / a.group; }
+  __device__ int q_head(int r) const { return h * a.group + (r0 + r) % a.group; }
+};
 
 }  // namespace sgd

@@ -259,6 +259,75 @@ def test_attend_window_and_sinks(KV, P, D, window, sinks):
     p.kv.close()
 
 
+MANY = [1, 2, 17, 63, 64, 65, 127, 128, 129, 191, 193, 300, 511, 640, 1000, 1500]
+
+
+@pytest.mark.parametrize("P,H,D,G", [(64, 4, 128, 4), (128, 3, 64, 6), (64, 3, 64, 16), (128, 4, 128, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3), (64, 70), (1, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attend_many_rows(KV, P, H, D, G, window, sinks, dtype):
+    """Batches whose rows open 0..33 positions: units of up to 128 rows, several
+    units a row, rows of every length around the tiles, cuts within a unit."""
+    rng = np.random.default_rng(P + G + window)
+    counts = [int(min(n, c)) for n, c in zip(MANY, rng.integers(0, 34, len(MANY)))]
+    counts[-1], counts[4], counts[7] = 33, 20, 33
+    p = Pair(KV, MANY, P=P, H=H, D=D, G=G, seed=P + window)
+    p.write(MANY, MANY, spread=1.0)
+    out = p.check_attend(MANY, counts, dtype, window=window, sinks=sinks)
+    assert p.kv.get_error() == 0 and bool(out.isfinite().all())
+    p.kv.close()
+
+
+def test_attend_many_rows_of_unequal_blocks(KV):
+    """Blocks of very unequal key and value scales, queries of unequal size, a
+    negative scale and a scale of zero, a query that is not finite."""
+    lens = [130 + 37 * i for i in range(20)]
+    counts = [1 + i % 9 for i in range(20)]
+    p = Pair(KV, lens, P=64, H=2, D=128, G=4, seed=5)
+    N = sum(lens)
+    g = p.g
+    size = torch.exp2(torch.randint(-12, 13, (N // 16 + 1, 1, 1), generator=g).float()).repeat_interleave(16, 0)[:N]
+    p.write(lens, lens, tensors=(torch.randn(N, 2, 128, generator=g), torch.randn(N, 2, 128, generator=g) * size))
+    q = torch.randn(sum(counts), 8, 128, generator=g) * torch.exp2(torch.randn(sum(counts), 8, 1, generator=g) * 2)
+    q = q.to(torch.bfloat16)
+    p.check_attend(lens, counts, q=q)
+    p.check_attend(lens, counts, q=q, scale=-0.2)
+    p.check_attend(lens, counts, q=q, scale=0.0)
+    p.check_attend(lens, counts, q=(q.float() * 1e-30).to(torch.bfloat16))
+    clean = p.check_attend(lens, counts, q=q)
+    bad = q.clone()
+    bad[7, 3, 100] = float("inf")
+    bad[20, 0, 0] = float("nan")
+    out = p.kv.attend(bad.cuda(), p.dev_table, torch.tensor(lens, dtype=torch.int32).cuda(), _starts(counts), 9)
+    assert bool(out[7, 3].isnan().all()) and bool(out[20, 0].isnan().all())
+    out[7, 3], out[20, 0] = clean[7, 3], clean[20, 0]
+    assert torch.equal(out, clean)
+    p.kv.close()
+
+
+def test_attend_many_rows_bad_pages_and_lengths(KV):
+    from model_free_suffix_gb300 import _lib as L
+    lens, counts = [200 + 10 * i for i in range(20)], [9] * 20
+    p = Pair(KV, lens, P=64, H=2, D=64, G=4, seed=6)
+    p.write(lens, lens, spread=1.0)
+    q = torch.randn(180, 8, 64, generator=p.g).to(torch.bfloat16)
+    clean = p.check_attend(lens, counts, q=q)
+    table, n = p.dev_table.clone(), torch.tensor(lens, dtype=torch.int32).cuda()
+    table[3] = 10 ** 6
+    n[5], n[6] = 8, 64 * table.shape[1] + 1
+    out = p.kv.attend(q.cuda(), table, n, _starts(counts), 9)
+    assert p.kv.get_error(clear=True) == L.KV_ERR_LENGTH | L.KV_ERR_PAGE
+    # (units of other rows may be cut elsewhere: two results within the bound of the same value)
+    for b in range(20):
+        now, before = out[9 * b:9 * b + 9].double(), clean[9 * b:9 * b + 9].double()
+        if b in (3, 5, 6):
+            assert not now.any()
+        else:
+            v = p.ref.rows("v", p.table[b], 0, lens[b]).abs().amax(0).cuda().repeat_interleave(4, 0)
+            assert bool(((now - before).abs() <= 2.0 ** -7 * before.abs() + 2.0 ** -9 * v + 2e-7).all())
+    p.kv.close()
+
+
 @pytest.mark.parametrize("n,c", [(5000, 1), (5000, 9), (20000, 1), (3001, 3001)])
 def test_attend_long_rows(KV, n, c):
     """One long row (split over many CTAs and joined), and a whole prompt at once."""
