@@ -37,6 +37,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // Waits for a phase to complete; false after a bound (each try suspends for a
 // while by itself), so that no launch can hang.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
   for (int i = 0; i < (1 << 18); ++i)
     if (bar_try(bar, parity)) return true;
   return false;

@@ -40,7 +40,8 @@ int view(const sgd_kv *x, const sgd_kv_layer *l, KvView *v) {
   if (!l || !l->k || !l->v || !l->k_scale || !l->v_scale) return SGD_EINVAL;
   if (!aligned(l->k, 16) || !aligned(l->v, 16) || !aligned(l->k_scale, 4) || !aligned(l->v_scale, 4)) return SGD_EINVAL;
   *v = KvView{static_cast<uint8_t *>(l->k), static_cast<uint8_t *>(l->v), l->k_scale, l->v_scale,
-              x->cfg.num_pages, x->cfg.kv_heads, x->cfg.page_size, x->cfg.head_dim};
+              x->cfg.num_pages, x->cfg.kv_heads, x->cfg.page_size, x->cfg.head_dim, 0};
+  while (1 << v->page_bits < v->page) ++v->page_bits;
   return SGD_OK;
 }
 

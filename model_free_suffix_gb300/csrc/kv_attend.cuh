@@ -1,4 +1,4 @@
-// kv_attend.cuh -- what the two attention kernels share.
+// kv_attend.cuh -- the attention's references, and where parts of units lie.
 #pragma once
 
 #include <cuda.h>
@@ -10,7 +10,7 @@
 namespace sgd {
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int MAX_CTAS = 152 * 3;
+constexpr int MAX_CTAS = 152 * 3;  // what the workspace is laid out for
 
 // Token j adds 2^z_j, z its scaled product in units of log 2, to l and
 // 2^(z_j + log2 V_j) q_j to o, V_j the scale of its block of values and q_j what
@@ -27,11 +27,9 @@ constexpr int MAX_CTAS = 152 * 3;
 constexpr float LAZY = 4.f;
 constexpr float LIFT = 11.99f;
 
-// log2 of a block's scale (a power of two when sgd_kv_write made it)
-__device__ __forceinline__ float log2_scale(float s) {
-  const uint32_t u = __float_as_uint(s);
-  return (u & 0x7fffff) ? log2f(s) : (float)((int)(u >> 23) - 127);
-}
+// log2 of a block's scale (a power of two when sgd_kv_write made it), and its inverse
+__device__ __forceinline__ float log2_scale(float s) { return __log2f(s); }
+__device__ __forceinline__ float inverse_scale(float s) { return __fdividef(1.f, s); }
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -42,14 +40,5 @@ template <int M, int D>
 __device__ __forceinline__ float *part_of(const KvAttendArgs &a, int slot) {
   return reinterpret_cast<float *>(a.work + MAX_CTAS * 8) + (long long)slot * (M * (D + 2));
 }
-
-// Keys or values as lines of 128 bytes (one token, or two of 64 bytes), in
-// boxes of `tokens`, with the 128-byte swizzle.
-bool kv_make_map(CUtensorMap *map, const KvView &c, void *base, int tokens);
-
-// Whether a call goes to the kernel for many rows.
-bool kv_many_rows(const KvAttendArgs &a);
-cudaError_t launch_attend_many(const KvAttendArgs &a, int dtype, cudaStream_t st);
-cudaError_t attend_many_limits();
 
 }  // namespace sgd

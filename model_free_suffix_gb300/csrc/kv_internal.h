@@ -15,6 +15,7 @@ struct KvView {
   uint8_t *k, *v;
   float *ks, *vs;
   int num_pages, heads, page, dim;
+  int page_bits;  // log2 of page
 };
 
 // Which tokens a call means: row b's tokens are packed q_start[b] ..

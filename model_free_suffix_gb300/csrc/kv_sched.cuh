@@ -86,6 +86,7 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
   const int per = (a.r.B + THREADS - 1) / THREADS;
   const int b0 = min(a.r.B, tid * per), b1 = min(a.r.B, b0 + per);
   long long mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += kv_work(kv_job<M, TILE>(a, b, bits), a.c.heads);
   long long scan = mine;
 #pragma unroll
@@ -114,6 +115,7 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
   s.begin = kv_cut(total, s.ctas, g);
   s.end = kv_cut(total, s.ctas, g + 1);
   if (before <= s.begin && s.begin < before + mine) {
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const long long w = kv_work(kv_job<M, TILE>(a, b, bits), a.c.heads);
       if (s.begin < before + w) {
@@ -144,24 +146,29 @@ struct KvWalk {
   int t0, t1;                // tiles of the list
   int p_first, p_last;       // positions of the first and the last row's token
 
-  __device__ KvWalk(const KvAttendArgs &a_, const KvShare &s, uint32_t *bits)
-      : a(a_), share(s), at(s.begin), b_begin(s.b_begin), b(s.b), job(kv_job<M, TILE>(a_, s.b, bits)) {}
+  __device__ KvWalk(const KvAttendArgs &a_, const KvShare &s)
+      : a(a_), share(s), at(s.begin), b_begin(s.b_begin), b(s.b) {
+    job.units = -1;
+  }
 
-  __device__ bool next(uint32_t *bits) {
+  __device__ __forceinline__ bool next(uint32_t *bits) {
     if (at >= share.end) return false;
+    if (job.units < 0) job = kv_job<M, TILE>(a, b, bits);
+#pragma unroll 1
     while (at >= b_begin + kv_work(job, a.c.heads)) {
       b_begin += kv_work(job, a.c.heads);
       ++b;
       job = kv_job<M, TILE>(a, b, bits);
     }
-    const int u = (int)((at - b_begin) / job.tiles);
+    const long long into = at - b_begin;
+    const int u = into < 0x7fffffff ? (int)((unsigned)into / (unsigned)job.tiles) : (int)(into / job.tiles);
     u_begin = b_begin + (long long)u * job.tiles;
     u_end = u_begin + job.tiles;
     t0 = (int)(at - u_begin);
     t1 = (int)(min(u_end, share.end) - u_begin);
     at = u_begin + t1;
-    h = u % a.c.heads;
-    r0 = u / a.c.heads * M;
+    h = u / job.units;  // (a head's units follow one another: the later ones find its tiles in L2)
+    r0 = u % job.units * M;
     nrows = min(M, job.ql * a.group - r0);
     p_first = job.n - job.ql + r0 / a.group;
     p_last = job.n - job.ql + (r0 + nrows - 1) / a.group;
@@ -180,8 +187,8 @@ struct KvWalk {
   }
   // the page of the tile at x, its i-th; -1: none (reported where it should be there)
   __device__ int page(int x, int i, uint32_t *bits) const {
-    const int block = x / a.c.page + i;
-    if (block >= a.r.max_pages || block * a.c.page >= job.n) return -1;
+    const int block = (x >> a.c.page_bits) + i;
+    if (block >= a.r.max_pages || block << a.c.page_bits >= job.n) return -1;
     const int pg = __ldg(a.r.table + (long long)b * a.r.max_pages + block);
     if (pg >= 0 && pg < a.c.num_pages) return pg;
     *bits |= SGD_KV_ERR_PAGE;
