@@ -2,8 +2,9 @@
 //
 // A unit is up to M rows (new token, query head of the group) of one batch row
 // and one head of keys and values; its work is the list of key tiles that the
-// batch row's new tokens see.  All tiles of all units, one after the other, are
-// cut into equal shares, one per CTA, wherever the cut falls: rows of very
+// batch row's new tokens see, each weighted by what the unit's rows make it cost.
+// All tiles of all units, one after the other, are cut into equal shares, one
+// per CTA, wherever the cut falls (within a tile: before it): rows of very
 // unequal length keep every SM busy to the end.  A unit that a cut goes through
 // is joined from its parts by the CTA that finishes last, in the order of the
 // parts, so that the result does not depend on which CTA that is.
@@ -19,15 +20,17 @@ struct KvJob {
   int q0, ql, n;       // first packed token, new tokens, cached tokens
   int sink_tiles;      // tiles of first tokens before the others
   int lo_tile, tiles;  // the others start at lo_tile; all tiles
-  int units;           // of one head
+  int units;           // of one head: all but the last have M rows
+  int cost, cost_last; // of a tile of the units before the last; of the last
 
   // the token tile of the j-th tile of the list
   __device__ __forceinline__ int tile(int j) const { return j < sink_tiles ? j : lo_tile + j - sink_tiles; }
 };
 
-// M: rows of a unit; TILE: tokens of a tile.
-template <int M, int TILE>
+// The kernel's M: rows of a unit; TILE: tokens of a tile; cost(rows): of a tile.
+template <class K>
 __device__ __forceinline__ KvJob kv_job(const KvAttendArgs &a, int b, uint32_t *bits) {
+  constexpr int TILE = K::TILE;
   KvJob r;
   const int q0 = __ldg(a.r.q_start + b), q1 = __ldg(a.r.q_start + b + 1);
   r.n = __ldg(a.r.seq_lens + b);
@@ -37,7 +40,9 @@ __device__ __forceinline__ KvJob kv_job(const KvAttendArgs &a, int b, uint32_t *
     *bits |= SGD_KV_ERR_LENGTH;
     r.ql = 0;
   }
-  r.units = (int)(((long long)r.ql * a.group + M - 1) / M);
+  r.units = (int)(((long long)r.ql * a.group + K::M - 1) / K::M);
+  r.cost = K::cost(K::M);
+  r.cost_last = K::cost(r.ql * a.group - (r.units - 1) * K::M);
   r.sink_tiles = r.lo_tile = 0;
   if (r.ql > 0 && (r.n < r.ql || (long long)r.n > (long long)a.r.max_pages * a.c.page)) {
     *bits |= SGD_KV_ERR_LENGTH;  // sees nothing: one tile, which no token sees
@@ -54,9 +59,10 @@ __device__ __forceinline__ KvJob kv_job(const KvAttendArgs &a, int b, uint32_t *
   return r;
 }
 
-__device__ __forceinline__ long long kv_work(const KvJob &j, int heads) {
-  return (long long)j.units * heads * j.tiles;
+__device__ __forceinline__ long long kv_head_work(const KvJob &j) {
+  return j.units ? ((long long)(j.units - 1) * j.cost + j.cost_last) * j.tiles : 0;
 }
+__device__ __forceinline__ long long kv_work(const KvJob &j, int heads) { return kv_head_work(j) * heads; }
 
 // A CTA's share [begin, end) of the work, and the batch row where it begins.
 struct KvShare {
@@ -76,8 +82,8 @@ __device__ __forceinline__ int kv_cta_of(long long total, int ctas, long long at
   return g;
 }
 
-// By all threads of the block.  `least`: tiles that make a share worth a CTA.
-template <int THREADS, int M, int TILE>
+// By all threads of the block.  `least`: work that makes a share worth a CTA.
+template <class K, int THREADS>
 __device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
   __shared__ long long s_warp[THREADS / 32];
   __shared__ long long s_before;
@@ -87,7 +93,7 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
   const int b0 = min(a.r.B, tid * per), b1 = min(a.r.B, b0 + per);
   long long mine = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += kv_work(kv_job<M, TILE>(a, b, bits), a.c.heads);
+  for (int b = b0; b < b1; ++b) mine += kv_work(kv_job<K>(a, b, bits), a.c.heads);
   long long scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -117,7 +123,7 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
   if (before <= s.begin && s.begin < before + mine) {
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const long long w = kv_work(kv_job<M, TILE>(a, b, bits), a.c.heads);
+      const long long w = kv_work(kv_job<K>(a, b, bits), a.c.heads);
       if (s.begin < before + w) {
         s_b = b;
         s_before = before;
@@ -133,8 +139,9 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
 }
 
 // A share's segments: the units it holds or cuts, each with its range of tiles.
-template <int M, int TILE>
+template <class K>
 struct KvWalk {
+  static constexpr int M = K::M, TILE = K::TILE;
   const KvAttendArgs &a;
   const KvShare &share;
   long long at, b_begin;
@@ -153,28 +160,35 @@ struct KvWalk {
 
   __device__ __forceinline__ bool next(uint32_t *bits) {
     if (at >= share.end) return false;
-    if (job.units < 0) job = kv_job<M, TILE>(a, b, bits);
+    if (job.units < 0) job = kv_job<K>(a, b, bits);
 #pragma unroll 1
     while (at >= b_begin + kv_work(job, a.c.heads)) {
       b_begin += kv_work(job, a.c.heads);
       ++b;
-      job = kv_job<M, TILE>(a, b, bits);
+      job = kv_job<K>(a, b, bits);
     }
-    const long long into = at - b_begin;
-    const int u = into < 0x7fffffff ? (int)((unsigned)into / (unsigned)job.tiles) : (int)(into / job.tiles);
-    u_begin = b_begin + (long long)u * job.tiles;
-    u_end = u_begin + job.tiles;
-    t0 = (int)(at - u_begin);
-    t1 = (int)(min(u_end, share.end) - u_begin);
-    at = u_begin + t1;
-    h = u / job.units;  // (a head's units follow one another: the later ones find its tiles in L2)
-    r0 = u % job.units * M;
+    const long long into = at - b_begin, head = kv_head_work(job), unit = (long long)job.cost * job.tiles;
+    h = (int)quotient(into, head);
+    const long long in_head = into - h * head;
+    const int u = min((int)quotient(in_head, unit), job.units - 1);
+    const int cost = u == job.units - 1 ? job.cost_last : job.cost;
+    u_begin = at - in_head + u * unit;
+    u_end = u_begin + (long long)cost * job.tiles;
+    t0 = (int)quotient(at - u_begin, cost);
+    at = min(u_end, share.end);
+    t1 = (int)quotient(at - u_begin, cost);
+    r0 = u * M;  // (a head's units follow one another: the later ones find its tiles in L2)
     nrows = min(M, job.ql * a.group - r0);
     p_first = job.n - job.ql + r0 / a.group;
     p_last = job.n - job.ql + (r0 + nrows - 1) / a.group;
     return true;
   }
-  __device__ bool whole() const { return t0 == 0 && t1 == job.tiles; }
+  // whether the share holds the whole unit, or its begin
+  __device__ bool whole() const { return u_begin >= share.begin && u_end <= share.end; }
+  __device__ bool starts() const { return u_begin >= share.begin; }
+  __device__ static long long quotient(long long x, long long y) {
+    return (x | y) >> 31 ? x / y : (long long)((unsigned)x / (unsigned)y);
+  }
   // whether some row of the unit sees some token of tile j of the list
   __device__ bool seen(int j) const {
     if (j >= t1) return false;

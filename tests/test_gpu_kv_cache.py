@@ -498,3 +498,14 @@ def test_offsets_past_32_bits(KV):
     want, mass = want[:, :, 0], mass[:, :, 0]
     assert bool(((out - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * mass + 1e-7).all())
     kv.close()
+
+
+@pytest.mark.parametrize("D,P,counts", [(128, 64, [8]), (64, 128, [1]), (64, 16, [20]), (128, 32, [1, 12])])
+def test_attend_one_long_row(KV, D, P, counts):
+    """A unit cut into as many parts as there are CTAs."""
+    lens = [100_003, 5][:len(counts)]
+    p = Pair(KV, lens, P=P, H=1, D=D, G=4, seed=9)
+    p.write(lens, lens, spread=1.0)
+    p.check_attend(lens, [min(c, n) for c, n in zip(counts, lens)])
+    assert p.kv.get_error() == 0
+    p.kv.close()
