@@ -563,7 +563,7 @@ int sgd_kv_destroy(sgd_kv *kv);
  *               between tokens and heads, the last dimension contiguous (parts
  *               of one projection's output are taken as they are).
  *   block_table DEVICE int32 [B, max_pages_per_row], seq_lens DEVICE int32 [B],
- *   q_start     DEVICE int32 [B + 1], ascending from 0 to N.
+ *   q_start     DEVICE int32 [B + 1], ascending from 0 to at most N.
  * A block's scale is the smallest power of two that brings its largest
  * magnitude, over the entries before the first new token and the new ones, to
  * at most 448; entries already there are encoded again where that changes it.
@@ -587,10 +587,14 @@ int sgd_kv_read(sgd_kv *kv, const sgd_kv_layer *layer, const int32_t *block_tabl
  * which stay visible).
  *   q    DEVICE dtype (SGD_F16 or SGD_BF16) [N, q_heads, head_dim], strides in
  *        elements, the last dimension contiguous.
- *   max_q  the most new tokens of any row (rows with more are cut to it).
+ *   max_q  the most new tokens of any row; only chooses how the work is laid
+ *          out (rows with more are still right).
  *   scale  of the products before the softmax.
  *   out  DEVICE dtype [N, q_heads, head_dim], contiguous, 16-byte aligned; 0 for
- *        a token that sees nothing. */
+ *        a token that sees nothing.
+ * Tokens from q_start[B] on belong to no row: q is not read and out not written
+ * there, so a call may have room for more tokens than its rows have (also in
+ * sgd_kv_write, where k and v are not read). */
 int sgd_kv_attend(sgd_kv *kv, const sgd_kv_layer *layer, const void *q, int32_t dtype,
                   int64_t q_token_stride, int64_t q_head_stride, const int32_t *block_table,
                   const int32_t *seq_lens, const int32_t *q_start, int32_t B, int32_t N,

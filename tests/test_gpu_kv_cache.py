@@ -509,3 +509,27 @@ def test_attend_one_long_row(KV, D, P, counts):
     p.check_attend(lens, [min(c, n) for c, n in zip(counts, lens)])
     assert p.kv.get_error() == 0
     p.kv.close()
+
+
+@pytest.mark.parametrize("counts,room", [([1, 1, 1], 4), ([3, 0, 9], 300)])
+def test_room_for_more_tokens(KV, counts, room):
+    """Tokens past q_start[B] are neither read nor written."""
+    lens = [40, 7, 90]
+    p = Pair(KV, lens, P=32, H=2, D=64, G=2)
+    p.write(lens, lens, spread=1.0)
+    N = sum(counts)
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    q = torch.full((N + room, 4, 64), float("nan"), dtype=torch.bfloat16)
+    q[:N] = torch.randn(N, 4, 64, generator=p.g)
+    out = torch.full((N + room, 4, 64), 7.0, dtype=torch.bfloat16).cuda()
+    p.kv.attend(q.cuda(), p.dev_table, n, _starts(counts), max(counts), out=out)
+    assert bool((out[N:] == 7).all())
+    assert torch.equal(out[:N], p.check_attend(lens, counts, q=q[:N]))
+    kv = torch.full((N + room, 2, 2, 64), float("nan"), dtype=torch.bfloat16)
+    kv[:N] = torch.randn(N, 2, 2, 64, generator=p.g)
+    dev = kv.cuda()
+    p.kv.write(dev[:, 0], dev[:, 1], p.dev_table, n, _starts(counts))
+    p.ref.write({"k": kv[:N, 0], "v": kv[:N, 1]}, p.table, lens, counts)
+    p.check(lens)
+    assert p.kv.get_error() == 0
+    p.kv.close()
