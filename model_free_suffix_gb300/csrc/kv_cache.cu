@@ -226,10 +226,13 @@ __device__ __forceinline__ __half2 top_of(__half2 top, const uint4 &v) {
 // takes one head's keys or values of a segment: the largest magnitude first, of
 // the new entries and the block's older ones, then the encoding.  Bound by
 // latency at the few tokens of a verification step (256 rows of 1 to 17 tokens,
-// 8 heads of 128: 32 us, 3.0 TB/s; 5 tokens of one row: 7 us), by the bytes and
-// the conversions at prompts (8 rows of 8192: 92 us, 4.1 TB/s).  A page and head
-// is one team's, since the scale needs every entry before any is encoded, and
-// the new ones are read once: a lane keeps its entries in registers.
+// 8 heads of 128, 31 MB with the entries already there: 12 us, 2.5 TB/s; 4 tokens
+// of one row: 4 us), by the bytes and the conversions at prompts (8 rows, 30620
+// tokens, 188 MB: 46 us, 4.1 TB/s).  A page and head is one team's, since the
+// scale needs every entry before any is encoded, and the new ones are read once:
+// a lane keeps its entries in registers.  (Eight loads of old entries in flight
+// instead of four, or wider ones, cost more registers than they gain: 36 us for
+// that step and its read back against 32.)
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 3 : 4) kv_write_kernel(KvWriteArgs a) {
   __shared__ float team_max[2][WARPS];
@@ -421,15 +424,18 @@ unsigned segments(int B, int N, const KvView &c) {
 
 template <typename T>
 cudaError_t write(KvWriteArgs a, cudaStream_t st) {
-  // Rows of a page's tokens or more on average: as many warps as keep a page in
-  // their registers, else one.  Measured, teams against single warps (8 heads of
-  // 128): one row of 512 tokens, pages of 128: 8.3 us, 27.8; of 2048, pages of 64:
-  // 9.5, 16.1; of 8192, pages of 128: 24.6, 37.3; 8 rows of 8192, pages of 64: 92,
-  // 92.  Fewer tokens than a page leave most of a team idle.
+  // Rows of a page's tokens or more on average, and fewer warps than the GPU holds:
+  // as many warps a page and head as keep it in their registers.  Measured, teams
+  // against single warps (8 heads of 128): one row of 512 tokens, pages of 128: 4.7
+  // us, 17.1; of 2048, pages of 64: 4.5, 9.1; of 8192, pages of 128: 12.3, 24.5; at
+  // 8 rows of up to 8192 there are warps enough without: 52, 46.  Fewer tokens than
+  // a page leave most of a team idle: a step of 1 to 17 tokens with its read back
+  // takes 32 us with single warps, 40 with teams of two.
+  const unsigned x = segments(a.r.B, a.r.N, a.c);
   a.team = 1;
   if (a.r.N / a.r.B >= a.c.page)
-    while (a.team < WARPS && a.team * 1024 < a.c.page * a.c.dim) a.team *= 2;
-  const unsigned x = segments(a.r.B, a.r.N, a.c);
+    while (a.team < WARPS && a.team * 1024 < a.c.page * a.c.dim && (long long)x * 2 * a.c.heads * a.team < 152 * 32)
+      a.team *= 2;
   const unsigned teams = WARPS / a.team;
   const dim3 grid(x, (2 * a.c.heads + teams - 1) / teams);
   if (a.c.dim == 128)
