@@ -1,6 +1,6 @@
 """A whole speculative decoding loop: drafts, verification pass, next step.
 
-    python examples/speculate.py [--batch 8] [--steps 60] [--temperature 0]
+    PYTHONPATH=. python examples/speculate.py [--batch 8] [--steps 60] [--temperature 0]
 
 The target is a small random transformer (plain torch products around the cache
 and its attention); what matters is how the calls fit together.  Per step
