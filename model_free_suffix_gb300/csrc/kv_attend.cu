@@ -12,11 +12,11 @@
 // that each byte of the cache is read once for all of them.
 //
 // Bound by reading the cache: at 256 batch rows of one token over 1024 to 4096
-// cached ones, 8 heads of 128, 1.35 GB: 234 us, 5.8 TB/s, with 8 query heads a
-// head of keys; 236 us with 4 new tokens and 4 query heads (16 rows).  At a dim
-// of 64 and pages of 16, 1.08 GB: 220 us, 4.9 TB/s (a tile is half the bytes for
+// cached ones, 8 heads of 128, 1.35 GB: 230 us, 5.9 TB/s, with 8 query heads a
+// head of keys; 232 us with 4 new tokens and 4 query heads (16 rows).  At a dim
+// of 64 and pages of 16, 1.08 GB: 207 us, 5.2 TB/s (a tile is half the bytes for
 // the same softmax, and comes from two pages).  A window of 2048 over up to 16k
-// tokens, 128 batch rows: 80 us, 3.4 TB/s.  One row of 2000 tokens: 18 us, of
+// tokens, 128 batch rows: 76 us, 3.6 TB/s.  One row of 2000 tokens: 17 us, of
 // which the work is 1; the rest is a chain of loads, and joining the parts.
 // The work is cut into equal shares wherever a cut falls since whole units leave
 // the last ones running alone; 3 CTAs an SM of 4 warps with rings of their own
@@ -224,16 +224,21 @@ __global__ void __launch_bounds__(THREADS, PER_SM)
           }
         }
       }
-      // ---- masks, maxima, probabilities
+      // ---- scales and masks: s becomes the exponent of the probability
       const bool missing = kh[0] == 0.f || kh[1] == 0.f;
-      {
-        const float fk[2][2] = {{f[0] * kh[0], f[0] * kh[1]}, {f[1] * kh[0], f[1] * kh[1]}};
+      float limit[2];  // beyond it the row's maximum has moved
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bool fresh = m[x] == -CUDART_INF_F;
+        const float base = LIFT - (fresh ? 0.f : m[x]);
+        limit[x] = fresh ? -CUDART_INF_F : LIFT + LAZY;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], fk[e >> 1][nt >> 1], lh[nt >> 1]);
+          for (int e = 0; e < 2; ++e)
+            s[nt][2 * x + e] = fmaf(s[nt][2 * x + e], f[x] * kh[nt >> 1], lh[nt >> 1] + base);
       }
-      if (missing || w.edge(x0)) {
+      if (__builtin_expect(missing || w.edge(x0), 0)) {
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
@@ -243,46 +248,51 @@ __global__ void __launch_bounds__(THREADS, PER_SM)
             if (!vis) s[nt][e] = -CUDART_INF_F;
           }
       }
-      float top[2] = {-CUDART_INF_F, -CUDART_INF_F}, scale_o[2] = {1.f, 1.f};
-      bool rescale = false;
+      // ---- maxima
+      float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[nt][e]);
+      if (__builtin_expect(__any_sync(FULL, top[0] > limit[0] || top[1] > limit[1]), 0)) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 1));
-        top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 2));
-        if (top[x] > m[x] + LAZY || (m[x] == -CUDART_INF_F && top[x] > m[x])) {
-          scale_o[x] = m[x] == -CUDART_INF_F ? 0.f : ex2_approx(m[x] - top[x]);
-          l[x] *= scale_o[x];
-          m[x] = top[x];
-          rescale = true;
-        }
-      }
-      if (__any_sync(FULL, rescale)) {
+        for (int x = 0; x < 2; ++x) {
+          top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 1));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(FULL, top[x], 2));
+          if (top[x] > limit[x]) {
+            const bool fresh = m[x] == -CUDART_INF_F;
+            const float by = LIFT - top[x];  // what the exponents change by
+            const float k = fresh ? 0.f : ex2_approx(by);
+            m[x] = (fresh ? 0.f : m[x]) - by;
+            l[x] *= k;
 #pragma unroll
-        for (int n = 0; n < 2 * NJ; ++n)
+            for (int nt = 0; nt < 4; ++nt) {
+              s[nt][2 * x] += by;
+              s[nt][2 * x + 1] += by;
+            }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] *= scale_o[e >> 1];
-      }
-      uint32_t pa[2][4];
-      {
-        const float base[2] = {(m[0] == -CUDART_INF_F ? 0.f : m[0]) - LIFT, (m[1] == -CUDART_INF_F ? 0.f : m[1]) - LIFT};
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[nt][e] = ex2_approx(s[nt][e] - base[e >> 1]);
-            l[e >> 1] = fmaf(s[nt][e], ih[nt >> 1], l[e >> 1]);
+            for (int n = 0; n < 2 * NJ; ++n) {
+              o[n][2 * x] *= k;
+              o[n][2 * x + 1] *= k;
+            }
           }
-          pa[nt >> 1][(nt & 1) * 2] = pack2<__half>(s[nt][0], s[nt][1]);
-          pa[nt >> 1][(nt & 1) * 2 + 1] = pack2<__half>(s[nt][2], s[nt][3]);
         }
+      }
+      // ---- probabilities
+      uint32_t pa[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[nt][e] = ex2_approx(s[nt][e]);
+          l[e >> 1] = fmaf(s[nt][e], ih[nt >> 1], l[e >> 1]);
+        }
+        pa[nt >> 1][(nt & 1) * 2] = pack2<__half>(s[nt][0], s[nt][1]);
+        pa[nt >> 1][(nt & 1) * 2 + 1] = pack2<__half>(s[nt][2], s[nt][3]);
       }
       // ---- o += p v: dims 16 j + 4 c .. + 3 of rows g, g + 8.  Slots that no
       // token has reached may hold anything, NaN among it: they count as 0.
-      if (missing || x0 + KV_TILE > job.n) {
+      if (__builtin_expect(missing || x0 + KV_TILE > job.n, 0)) {
         __syncwarp();
         const bool gone = (lane < 16 ? kh[0] : kh[1]) == 0.f || x0 + lane >= job.n;
         if (gone) {
@@ -471,9 +481,9 @@ cudaError_t launch_kv_attend(KvAttendArgs a, int dtype, cudaStream_t st, int *la
   *launches = 1;
   // Up to 16 rows a batch row and head, a tile a warp (this file); beyond, a tile
   // a CTA.  Measured, this against the other, at up to 16 rows: one row of 2000
-  // tokens 18 us, 18; 4 tokens and 4 query heads 236, 241; one token and 8 query
-  // heads 234, 238, and with dim 64 and pages of 16 220, 275; a window of 2048 80,
-  // 93.  At 32 rows two warps to a tile took 411 against 291.  (max_q only chooses:
+  // tokens 17 us, 17; 4 tokens and 4 query heads 232, 232; one token and 8 query
+  // heads 230, 228, but with dim 64 and pages of 16 207, 273; a window of 2048 76,
+  // 92.  At 32 rows two warps to a tile took 411 against 280.  (max_q only chooses:
   // each takes any number of rows.)
   if ((long long)a.max_q * a.group > M) return launch_attend_many(a, dtype, st);
   return dtype == SGD_F16 ? attend<__half>(a, st) : attend<__nv_bfloat16>(a, st);

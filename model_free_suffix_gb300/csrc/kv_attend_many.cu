@@ -10,19 +10,22 @@
 // Two barriers a tile: one that also tells whether any row's maximum has moved
 // (else there is nothing to exchange), one before the probabilities are read.
 //
-// What bounds it: neither the memory nor one unit alone.  At 256 batch rows of 8
-// new tokens, 8 heads of 128, 4 query heads each, 1.36 GB of keys and values: 291
-// us, 4.7 TB/s; ncu shows the instruction slots 41% busy, the mma.sync units 35%,
-// and the warps waiting for one another's results and for the tiles in equal
-// parts.  With 17 new tokens, 3 units that read the same tiles: 450 us.
+// What bounds it: neither the memory nor one unit alone.  At 256 batch rows of up
+// to 8 new tokens, 8 heads of 128, 4 query heads each, 1.36 GB of keys and values:
+// 280 us, 4.9 TB/s.  With up to 17 new tokens, 3 units that read the same tiles:
+// 438 us; ncu shows the instruction slots 46% busy and the mma.sync units 42%, with
+// 16 warps an SM that wait for results of their own and, a sixth of the time, at
+// the barriers.
 // Measured against it, in us at 8 new tokens, 17, and 33 over 8k to 32k tokens
-// (291, 450, 682 here):
+// (280, 438, 667 here):
 //   two warps to a tile, 16 rows each, every warp converting all of it   411 611 837
 //   32 rows a warp (245 registers, 8 warps an SM)                        430 670 785
 //   units of 64 rows, 3 CTAs an SM (the code outgrows the instruction
 //     cache; 740 for the second before cold code was moved out of the way) 309 637 722
 //   units of 48 rows, 3 CTAs an SM                                       337 505 724
 //   units of 32, values with no place more than keys                     323 480 725
+//   one barrier a tile, its products beside the sums of the tile before  314 481 719
+//   exponents relative to the maximum taken after the barrier            291 448 682
 //   tcgen05 with the tiles converted into shared memory                  573 745 836
 #include <math_constants.h>
 
@@ -207,15 +210,20 @@ __device__ __forceinline__ void segment(const KvAttendArgs &a, const KvWalk<KvMa
           }
         }
       }
-      // ---- scales and masks
+      // ---- scales and masks: s becomes the exponent of the probability
+      float limit[MT][2];  // beyond it the row's maximum has moved
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float f[2] = {sh.f[mt * 16 + g] * kh, sh.f[mt * 16 + 8 + g] * kh};
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int x = 0; x < 2; ++x) {
+          const bool fresh = m[mt][x] == -CUDART_INF_F;
+          const float f = sh.f[mt * 16 + x * 8 + g] * kh, plus = lh + (LIFT - (fresh ? 0.f : m[mt][x]));
+          limit[mt][x] = fresh ? -CUDART_INF_F : LIFT + LAZY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] = fmaf(s[mt][nt][e], f[e >> 1], lh);
-      }
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[mt][nt][2 * x + e] = fmaf(s[mt][nt][2 * x + e], f, plus);
+        }
       const bool missing = kh == 0.f;
       if (__builtin_expect(missing || w.edge(x0), 0)) {
 #pragma unroll
@@ -257,7 +265,7 @@ __device__ __forceinline__ void segment(const KvAttendArgs &a, const KvWalk<KvMa
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[mt][x] = fmaxf(fmaxf(s[mt][0][2 * x], s[mt][0][2 * x + 1]), fmaxf(s[mt][1][2 * x], s[mt][1][2 * x + 1]));
-          moves = moves || top[mt][x] > m[mt][x] + LAZY;
+          moves = moves || top[mt][x] > limit[mt][x];
         }
       if (__builtin_expect(__syncthreads_or(moves), 0)) {
 #pragma unroll
@@ -276,10 +284,17 @@ __device__ __forceinline__ void segment(const KvAttendArgs &a, const KvWalk<KvMa
           for (int x = 0; x < 2; ++x) {
             const int r = mt * 16 + x * 8 + g;
             const float v = fmaxf(fmaxf(sh.of_warp[0][r], sh.of_warp[1][r]), fmaxf(sh.of_warp[2][r], sh.of_warp[3][r]));
-            if (v > m[mt][x] + LAZY) {
-              const float k = m[mt][x] == -CUDART_INF_F ? 0.f : ex2_approx(m[mt][x] - v);
+            if (v > limit[mt][x]) {
+              const bool fresh = m[mt][x] == -CUDART_INF_F;
+              const float by = LIFT - v;  // what the exponents change by
+              const float k = fresh ? 0.f : ex2_approx(by);
+              m[mt][x] = (fresh ? 0.f : m[mt][x]) - by;
               l[mt][x] *= k;
-              m[mt][x] = v;
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                s[mt][nt][2 * x] += by;
+                s[mt][nt][2 * x + 1] += by;
+              }
 #pragma unroll
               for (int n = 0; n < 2 * NJ; ++n) {
                 o[mt][n][2 * x] *= k;
@@ -295,11 +310,10 @@ __device__ __forceinline__ void segment(const KvAttendArgs &a, const KvWalk<KvMa
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float base = (m[mt][x] == -CUDART_INF_F ? 0.f : m[mt][x]) - LIFT;
           const uint32_t line = p_at + (mt * 16 + x * 8 + g) * 128 + 4 * c;
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
-            const float p0 = ex2_approx(s[mt][nt][2 * x] - base), p1 = ex2_approx(s[mt][nt][2 * x + 1] - base);
+            const float p0 = ex2_approx(s[mt][nt][2 * x]), p1 = ex2_approx(s[mt][nt][2 * x + 1]);
             l[mt][x] = fmaf(p0 + p1, ih, l[mt][x]);
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(line + (((2 * warp + nt) ^ g) << 4)), "r"(pack2<__half>(p0, p1))
                          : "memory");
