@@ -14,13 +14,15 @@
 // Bound by reading the cache: at 256 batch rows of one token over 1024 to 4096
 // cached ones, 8 heads of 128, 1.35 GB: 230 us, 5.9 TB/s, with 8 query heads a
 // head of keys; 232 us with 4 new tokens and 4 query heads (16 rows).  At a dim
-// of 64 and pages of 16, 1.08 GB: 207 us, 5.2 TB/s (a tile is half the bytes for
+// of 64 and pages of 16, 1.08 GB: 203 us, 5.3 TB/s (a tile is half the bytes for
 // the same softmax, and comes from two pages).  A window of 2048 over up to 16k
-// tokens, 128 batch rows: 76 us, 3.6 TB/s.  One row of 2000 tokens: 17 us, of
+// tokens, 128 batch rows: 72 us, 3.8 TB/s.  One row of 2000 tokens: 17 us, of
 // which the work is 1; the rest is a chain of loads, and joining the parts.
 // The work is cut into equal shares wherever a cut falls since whole units leave
-// the last ones running alone; 3 CTAs an SM of 4 warps with rings of their own
-// since the warps then never wait for one another (64 KB of loads in flight).
+// the last ones running alone; 4 warps a CTA have rings of their own since they
+// then never wait for one another, 3 CTAs an SM (64 KB of loads in flight each),
+// at a dim of 64, where registers allow it, 4: 203 and 72 us against 207 and 76
+// (with tiles of 64 tokens there instead, 200 and 84: fewer, larger pieces to share).
 #include <math_constants.h>
 
 #include <type_traits>
@@ -38,7 +40,8 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int KV_TILE = 32;  // tokens
-constexpr int PER_SM = 3;    // CTAs
+template <int D>
+constexpr int PER_SM = D == 128 ? 3 : 4;  // CTAs
 constexpr int M = 16;        // rows of a unit
 
 struct KvFew {
@@ -62,7 +65,7 @@ struct KvFew {
 // chunks of a key, so all shared-memory reads are 16 bytes wide and, with the
 // 128-byte swizzle of the TMA load, without bank conflicts.
 template <typename T, int D, int S>
-__global__ void __launch_bounds__(THREADS, PER_SM)
+__global__ void __launch_bounds__(THREADS, PER_SM<D>)
     attend_kernel(KvAttendArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   constexpr int HALF = KV_TILE * D;          // bytes of a tile's keys (or values)
   constexpr int NJ = D / 16;                 // 16-dim groups of the output
@@ -449,7 +452,7 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t st) {
   CUtensorMap k, v;
   const int tokens = a.c.page < KV_TILE ? a.c.page : KV_TILE;
   if (!kv_make_map(&k, a.c, a.c.k, tokens) || !kv_make_map(&v, a.c, a.c.v, tokens)) return cudaErrorInvalidValue;
-  attend_kernel<T, D, S><<<a.sms * PER_SM, THREADS, smem_bytes<D, S>(), st>>>(a, k, v);
+  attend_kernel<T, D, S><<<(a.sms < MAX_CTAS / PER_SM<D> ? a.sms : MAX_CTAS / PER_SM<D>) * PER_SM<D>, THREADS, smem_bytes<D, S>(), st>>>(a, k, v);
   return cudaGetLastError();
 }
 
@@ -460,7 +463,7 @@ cudaError_t limit() {
 
 template <typename T>
 cudaError_t attend(const KvAttendArgs &a, cudaStream_t st) {
-  return a.c.dim == 128 ? launch<T, 128, 2>(a, st) : launch<T, 64, 4>(a, st);
+  return a.c.dim == 128 ? launch<T, 128, 2>(a, st) : launch<T, 64, 3>(a, st);
 }
 
 }  // namespace
@@ -469,20 +472,19 @@ size_t kv_attend_workspace() { return (size_t)MAX_CTAS * 8 + (size_t)MAX_CTAS * 
 
 cudaError_t kv_attend_set_limits() {
   cudaError_t e = limit<__half, 128, 2>();
-  if (e == cudaSuccess) e = limit<__half, 64, 4>();
+  if (e == cudaSuccess) e = limit<__half, 64, 3>();
   if (e == cudaSuccess) e = limit<__nv_bfloat16, 128, 2>();
-  if (e == cudaSuccess) e = limit<__nv_bfloat16, 64, 4>();
+  if (e == cudaSuccess) e = limit<__nv_bfloat16, 64, 3>();
   if (e == cudaSuccess) e = attend_many_limits();
   return e;
 }
 
 cudaError_t launch_kv_attend(KvAttendArgs a, int dtype, cudaStream_t st, int *launches) {
-  if (a.sms > MAX_CTAS / PER_SM) a.sms = MAX_CTAS / PER_SM;
   *launches = 1;
   // Up to 16 rows a batch row and head, a tile a warp (this file); beyond, a tile
   // a CTA.  Measured, this against the other, at up to 16 rows: one row of 2000
   // tokens 17 us, 17; 4 tokens and 4 query heads 232, 232; one token and 8 query
-  // heads 230, 228, but with dim 64 and pages of 16 207, 273; a window of 2048 76,
+  // heads 230, 228, but with dim 64 and pages of 16 203, 273; a window of 2048 72,
   // 92.  At 32 rows two warps to a tile took 411 against 280.  (max_q only chooses:
   // each takes any number of rows.)
   if ((long long)a.max_q * a.group > M) return launch_attend_many(a, dtype, st);
