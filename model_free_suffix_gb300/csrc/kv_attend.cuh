@@ -76,6 +76,8 @@ __device__ __forceinline__ void kv_queries(const KvAttendArgs &a, const Walk &w,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool mine = lane * 4 < D;
   constexpr int BATCH = 4;  // rows of a warp with their loads in flight
+  constexpr int DPT = D / 4;  // dims of a lane
+  const int qc = lane * 4 / DPT, s = lane * 4 % DPT / 4;
 #pragma unroll 1
   for (int r0 = warp; r0 < R && r0 < (w.nrows + 15) / 16 * 16; r0 += WARPS * BATCH) {
     uint2 raw[BATCH];
@@ -96,28 +98,33 @@ __device__ __forceinline__ void kv_queries(const KvAttendArgs &a, const Walk &w,
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const int r = r0 + i * WARPS;
-      T in[4];
-      *reinterpret_cast<uint2 *>(in) = raw[i];
-      float x[4], top = 0.f;
-      bool bad = false;
+      const uint32_t to = q_at + (((r / 16) * (D / 16) + s) * 32 + (r % 8) * 4 + qc) * 16 + (r % 16) / 8 * 4;
+      uint32_t pair[2] = {0, 0};
+      if (r < w.nrows) {
+        T in[4];
+        *reinterpret_cast<uint2 *>(in) = raw[i];
+        float x[4], top = 0.f;
+        bool bad = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = to_f32(in[e]);
-        top = fmaxf(top, fabsf(x[e]));
-        bad = bad || !(fabsf(x[e]) < CUDART_INF_F);
+        for (int e = 0; e < 4; ++e) {
+          x[e] = to_f32(in[e]);
+          top = fmaxf(top, fabsf(x[e]));
+          bad = bad || !(fabsf(x[e]) < CUDART_INF_F);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+        const bool poison = __any_sync(FULL, bad);  // (a bad element makes its row NaN)
+        const int e2 = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+        const float inv = poison ? CUDART_NAN_F : pow2(-min(e2, 126));
+        if (lane == 0) s_f[r] = a.scale * LOG2E * pow2(min(e2, 126));
+        pair[0] = pack2<__half>(x[0] * inv, x[1] * inv);
+        pair[1] = pack2<__half>(x[2] * inv, x[3] * inv);
+      } else if (lane == 0) {
+        s_f[r] = 0.f;
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-      const bool poison = __any_sync(FULL, bad);  // (a bad element makes its row NaN)
-      const int e2 = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-      const float inv = poison ? CUDART_NAN_F : pow2(-min(e2, 126));
-      if (lane == 0) s_f[r] = a.scale * LOG2E * pow2(min(e2, 126));
       if (mine) {
-        constexpr int DPT = D / 4;  // dims of a lane
-        const int d = lane * 4, qc = d / DPT, s = d % DPT / 4;
-        const uint32_t to = q_at + (((r / 16) * (D / 16) + s) * 32 + (r % 8) * 4 + qc) * 16 + (r % 16) / 8 * 4;
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(pack2<__half>(x[0] * inv, x[1] * inv)) : "memory");
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 8), "r"(pack2<__half>(x[2] * inv, x[3] * inv)) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(pair[0]) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 8), "r"(pair[1]) : "memory");
       }
     }
   }
@@ -135,8 +142,7 @@ __device__ __forceinline__ void kv_join(const KvAttendArgs &a, const KvShare &sh
                                         int *s_last) {
   constexpr int M = K::M, R = JOIN_ROWS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g0 = kv_cta_of(share.total, share.ctas, w.u_begin);
-  const int g1 = kv_cta_of(share.total, share.ctas, w.u_end - 1);
+  const int g0 = share.cta_of(w.u_begin), g1 = share.cta_of(w.u_end - 1);
   unsigned *count = reinterpret_cast<unsigned *>(a.work) + g0;
   __threadfence();
   __syncthreads();

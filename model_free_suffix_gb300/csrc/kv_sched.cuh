@@ -64,23 +64,29 @@ __device__ __forceinline__ long long kv_head_work(const KvJob &j) {
 }
 __device__ __forceinline__ long long kv_work(const KvJob &j, int heads) { return kv_head_work(j) * heads; }
 
-// A CTA's share [begin, end) of the work, and the batch row where it begins.
+// (A 64-bit division takes about a hundred instructions, and at one token of one
+// row the scheduling is most of what a warp executes.)
+static __device__ __noinline__ long long wide_quotient(long long x, long long y) { return x / y; }
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return (x | y) >> 31 ? wide_quotient(x, y) : (long long)((unsigned)x / (unsigned)y);
+}
+
+// A CTA's share [begin, end) of the work, and the batch row where it begins.  The
+// first `more` shares are of each + 1, the others of each.
 struct KvShare {
-  long long begin, end, total;
-  int ctas;             // shares are [g * total / ctas, (g + 1) * total / ctas)
+  long long begin, end;
+  long long each;
+  int ctas, more;
   int b;                // batch row of `begin`
   long long b_begin;    // the work before row b
+
+  __device__ __forceinline__ long long cut(int g) const { return each * g + min(g, more); }
+  // the CTA whose share holds `at`
+  __device__ __forceinline__ int cta_of(long long at) const {
+    const long long large = (each + 1) * more;
+    return at < large ? (int)quotient(at, each + 1) : more + (int)quotient(at - large, each);
+  }
 };
-
-__device__ __forceinline__ long long kv_cut(long long total, int ctas, int g) { return total * g / ctas; }
-
-// The CTA whose share holds `at`.
-__device__ __forceinline__ int kv_cta_of(long long total, int ctas, long long at) {
-  int g = (int)(at * ctas / total);
-  while (g + 1 < ctas && kv_cut(total, ctas, g + 1) <= at) ++g;
-  while (g > 0 && kv_cut(total, ctas, g) > at) --g;
-  return g;
-}
 
 // By all threads of the block.  `least`: work that makes a share worth a CTA.
 template <class K, int THREADS>
@@ -109,17 +115,19 @@ __device__ KvShare kv_share(const KvAttendArgs &a, int least, uint32_t *bits) {
     total += s_warp[w];
   }
   KvShare s;
-  s.total = total;
-  const long long most = (total + least - 1) / least;
+  const long long most = quotient(total + least - 1, least);
   s.ctas = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
   const int g = blockIdx.x;
   if (g >= s.ctas) {
-    s.begin = s.end = 0;
+    s.begin = s.end = s.each = s.b_begin = 0;
+    s.more = 0;
     s.b = a.r.B;
     return s;
   }
-  s.begin = kv_cut(total, s.ctas, g);
-  s.end = kv_cut(total, s.ctas, g + 1);
+  s.each = quotient(total, s.ctas);
+  s.more = (int)(total - s.each * s.ctas);
+  s.begin = s.cut(g);
+  s.end = s.cut(g + 1);
   if (before <= s.begin && s.begin < before + mine) {
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
@@ -186,9 +194,6 @@ struct KvWalk {
   // whether the share holds the whole unit, or its begin
   __device__ bool whole() const { return u_begin >= share.begin && u_end <= share.end; }
   __device__ bool starts() const { return u_begin >= share.begin; }
-  __device__ static long long quotient(long long x, long long y) {
-    return (x | y) >> 31 ? x / y : (long long)((unsigned)x / (unsigned)y);
-  }
   // whether some row of the unit sees some token of tile j of the list
   __device__ bool seen(int j) const {
     if (j >= t1) return false;
