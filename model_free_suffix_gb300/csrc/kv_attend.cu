@@ -12,17 +12,18 @@
 // that each byte of the cache is read once for all of them.
 //
 // Bound by reading the cache: at 256 batch rows of one token over 1024 to 4096
-// cached ones, 8 heads of 128, 1.35 GB: 230 us, 5.9 TB/s, with 8 query heads a
+// cached ones, 8 heads of 128, 1.35 GB: 228 us, 5.9 TB/s, with 8 query heads a
 // head of keys; 232 us with 4 new tokens and 4 query heads (16 rows).  At a dim
-// of 64 and pages of 16, 1.08 GB: 203 us, 5.3 TB/s (a tile is half the bytes for
+// of 64 and pages of 16, 1.08 GB: 197 us, 5.5 TB/s (a tile is half the bytes for
 // the same softmax, and comes from two pages).  A window of 2048 over up to 16k
-// tokens, 128 batch rows: 72 us, 3.8 TB/s.  One row of 2000 tokens: 17 us, of
+// tokens, 128 batch rows: 69 us, 3.9 TB/s.  One row of 2000 tokens: 17 us, of
 // which the work is 1; the rest is a chain of loads, and joining the parts.
 // The work is cut into equal shares wherever a cut falls since whole units leave
 // the last ones running alone; 4 warps a CTA have rings of their own since they
 // then never wait for one another, 3 CTAs an SM (64 KB of loads in flight each),
-// at a dim of 64, where registers allow it, 4: 203 and 72 us against 207 and 76
-// (with tiles of 64 tokens there instead, 200 and 84: fewer, larger pieces to share).
+// at a dim of 64, where registers allow it, 4 (before a later gain: 203 and 72 us
+// against 207 and 76; with tiles of 64 tokens there instead, 200 and 84: fewer,
+// larger pieces to share).
 #include <math_constants.h>
 
 #include <type_traits>
@@ -482,11 +483,12 @@ cudaError_t kv_attend_set_limits() {
 cudaError_t launch_kv_attend(KvAttendArgs a, int dtype, cudaStream_t st, int *launches) {
   *launches = 1;
   // Up to 16 rows a batch row and head, a tile a warp (this file); beyond, a tile
-  // a CTA.  Measured, this against the other, at up to 16 rows: one row of 2000
-  // tokens 17 us, 17; 4 tokens and 4 query heads 232, 232; one token and 8 query
-  // heads 230, 228, but with dim 64 and pages of 16 203, 273; a window of 2048 72,
-  // 92.  At 32 rows two warps to a tile took 411 against 280.  (max_q only chooses:
-  // each takes any number of rows.)
+  // a CTA.  Measured, this against the other, at up to 16 rows: at a dim of 64 with
+  // pages of 16 197 us, 271, with a window of 2048 69, 90; at 128, a window of 2048
+  // over pages of 16 186, 207; without a window 1 to 3% apart either way (one row
+  // of 2000 tokens 17, 17, 256 rows of one token and 8 query heads 228, 224), a
+  // window of 256 over pages of 64 67, 60.  At 32 rows two warps to a tile took 411
+  // against 279.  (max_q only chooses: each takes any number of rows.)
   if ((long long)a.max_q * a.group > M) return launch_attend_many(a, dtype, st);
   return dtype == SGD_F16 ? attend<__half>(a, st) : attend<__nv_bfloat16>(a, st);
 }

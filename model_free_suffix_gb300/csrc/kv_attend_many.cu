@@ -12,12 +12,12 @@
 //
 // What bounds it: neither the memory nor one unit alone.  At 256 batch rows of up
 // to 8 new tokens, 8 heads of 128, 4 query heads each, 1.36 GB of keys and values:
-// 280 us, 4.9 TB/s.  With up to 17 new tokens, 3 units that read the same tiles:
-// 438 us; ncu shows the instruction slots 46% busy and the mma.sync units 42%, with
+// 279 us, 4.9 TB/s.  With up to 17 new tokens, 3 units that read the same tiles:
+// 430 us; ncu shows the instruction slots 46% busy and the mma.sync units 42%, with
 // 16 warps an SM that wait for results of their own and, a sixth of the time, at
 // the barriers.
 // Measured against it, in us at 8 new tokens, 17, and 33 over 8k to 32k tokens
-// (280, 438, 667 here):
+// (279, 430, 669 here; 280, 438, 667 before shares were cut without divisions):
 //   two warps to a tile, 16 rows each, every warp converting all of it   411 611 837
 //   32 rows a warp (245 registers, 8 warps an SM)                        430 670 785
 //   units of 64 rows, 3 CTAs an SM (the code outgrows the instruction
