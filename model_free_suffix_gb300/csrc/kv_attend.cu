@@ -453,7 +453,8 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t st) {
   CUtensorMap k, v;
   const int tokens = a.c.page < KV_TILE ? a.c.page : KV_TILE;
   if (!kv_make_map(&k, a.c, a.c.k, tokens) || !kv_make_map(&v, a.c, a.c.v, tokens)) return cudaErrorInvalidValue;
-  attend_kernel<T, D, S><<<(a.sms < MAX_CTAS / PER_SM<D> ? a.sms : MAX_CTAS / PER_SM<D>) * PER_SM<D>, THREADS, smem_bytes<D, S>(), st>>>(a, k, v);
+  const int sms = a.sms < MAX_CTAS / PER_SM<D> ? a.sms : MAX_CTAS / PER_SM<D>;
+  attend_kernel<T, D, S><<<sms * PER_SM<D>, THREADS, smem_bytes<D, S>(), st>>>(a, k, v);
   return cudaGetLastError();
 }
 

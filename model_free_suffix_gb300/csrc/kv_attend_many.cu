@@ -55,7 +55,7 @@ struct Layout {  // of the dynamic shared memory, from a multiple of 1024
   static constexpr int HALF = KvMany::TILE * D;  // bytes of a tile's keys (or values)
   static constexpr int STAGES = 2 * 128 / D;
   static constexpr int V = STAGES * HALF;                     // values: read later, so one place more
-  static constexpr int P = V + (STAGES + 1) * HALF;              // probabilities, [row][token] f16
+  static constexpr int P = V + (STAGES + 1) * HALF;           // probabilities, [row][token] f16
   static constexpr int Q = P + KvMany::M * KvMany::TILE * 2;  // queries
   static constexpr int BYTES = 1024 + Q + KvMany::M * D * 2;
   static_assert(Q + KvMany::M * D * 2 >= kv_join_floats() * 4, "the parts' weights fit");
@@ -72,7 +72,7 @@ struct Ring {
   uint32_t tiles, bars, &bits;
   int slot, in_slot;      // to read, to load: places of keys
   int v_slot, in_v_slot;  // of values
-  uint32_t phases;    // of the places, a bit each
+  uint32_t phases;        // of the places, a bit each
   int next;           // tile of the list of lane 0
   uint32_t to_load;   // of the 32, those still to load
   int y[4];           // the lane's: lines of the tile's pages in the maps
@@ -85,7 +85,8 @@ struct Ring {
       const int x = w.job.tile(next + lane_id()) * KvMany::TILE;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < pages || i == 0) y[i] = ((max(w.page(x, i, &bits), 0) * a.c.heads + w.h) * P + (i == 0 ? x & (P - 1) : 0)) / PACK;
+        if (i < pages || i == 0)
+          y[i] = ((max(w.page(x, i, &bits), 0) * a.c.heads + w.h) * P + (i == 0 ? x & (P - 1) : 0)) / PACK;
     }
     to_load = __ballot_sync(FULL, on);
   }
@@ -450,7 +451,8 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t st) {
   CUtensorMap k, v;
   const int tokens = a.c.page < KvMany::TILE ? a.c.page : KvMany::TILE;
   if (!kv_make_map(&k, a.c, a.c.k, tokens) || !kv_make_map(&v, a.c, a.c.v, tokens)) return cudaErrorInvalidValue;
-  attend_many_kernel<T, D><<<(a.sms < MAX_CTAS / PER_SM ? a.sms : MAX_CTAS / PER_SM) * PER_SM, THREADS, Layout<D>::BYTES, st>>>(a, k, v);
+  const int sms = a.sms < MAX_CTAS / PER_SM ? a.sms : MAX_CTAS / PER_SM;
+  attend_many_kernel<T, D><<<sms * PER_SM, THREADS, Layout<D>::BYTES, st>>>(a, k, v);
   return cudaGetLastError();
 }
 
