@@ -78,15 +78,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// exp((l - m) / t) as 2^(l c - r), c = log2(e) / t, with the reference r = m c
-// rounded once: the fused multiply-add rounds only its small result, and r
-// cancels in every quotient, so logits of any size lose nothing.  Where r
-// would overflow (maxima near the type's lowest or largest value) the
-// difference is taken first.  A NaN logit or +inf - +inf weighs 0.
-constexpr float HUGE_REF = 1e30f;
+// exp((l - m) / t) as 2^x, c = log2(e) / t.  With the reference r = m c rounded
+// once, x = l c - r is one multiply-add that rounds only its small result, and
+// the error of r (half a unit of its last place) is the same factor in every
+// weight and in Z, and cancels.  That factor has to stay near 1: from |r| = 2^20
+// on, where it would pass 2^(2^-4) and, ever larger, leave the type's range, the
+// difference is taken first, x = (l - m) c.  A NaN logit or +inf - +inf weighs 0.
+constexpr float LARGE_REF = 1048576.f;  // 2^20
+__device__ __forceinline__ bool small_ref(float r) { return fabsf(r) < LARGE_REF; }
 __device__ __forceinline__ float log2_weight(float l, float m, float c) {
   const float r = m * c;
-  const float x = fabsf(r) < HUGE_REF ? fmaf(l, c, -r) : (l - m) * c;
+  const float x = small_ref(r) ? fmaf(l, c, -r) : (l - m) * c;
   return fmaxf(x, -1e30f);
 }
 __device__ __forceinline__ float weight(float l, float m, float c) { return ex2(log2_weight(l, m, c)); }
@@ -94,18 +96,21 @@ __device__ __forceinline__ float weight(float l, float m, float c) { return ex2(
 __device__ __forceinline__ float weight_any(float l, float m, float c) {
   return m == CUDART_INF_F ? (l == CUDART_INF_F ? 1.f : 0.f) : weight(l, m, c);
 }
-// from one maximum to a larger one: both references are what weight() used
+// From one maximum to a larger one: the difference of what weight() took away,
+// each maximum's product with c rounded where it is small, else exact.
 __device__ __forceinline__ float reweight(float from, float to, float c) {
   const float x = from * c, y = to * c;
-  return ex2(fmaxf(fabsf(y) < HUGE_REF && fabsf(x) < HUGE_REF ? x - y : (from - to) * c, -1e30f));
+  float d = x - y;
+  if (__builtin_expect(!(small_ref(x) && small_ref(y)), 0))
+    d = small_ref(x) ? fmaf(-to, c, x) : small_ref(y) ? fmaf(from, c, -y) : (from - to) * c;
+  return ex2(fmaxf(d, -1e30f));
 }
 
 __device__ __forceinline__ Stat join(const Stat &a, const Stat &b, float c) {
   Stat r;
   r.m = fmaxf(a.m, b.m);
-  const float sa = a.m == r.m ? 1.f : reweight(a.m, r.m, c);
-  const float sb = b.m == r.m ? 1.f : reweight(b.m, r.m, c);
-  r.z = (a.z == 0.f ? 0.f : a.z * sa) + (b.z == 0.f ? 0.f : b.z * sb);
+  const float k = a.m == b.m ? 1.f : reweight(fminf(a.m, b.m), r.m, c);
+  r.z = a.m == r.m ? fmaf(b.z, k, a.z) : fmaf(a.z, k, b.z);
   r.arg = a.m > b.m ? a.arg : b.m > a.m ? b.arg : min(a.arg, b.arg);
   return r;
 }
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) verify_stats_kernel(VerifyArg
     if (v + UNROLL * THREADS < sp.nvec) fetch(v + UNROLL * THREADS);
     const float mx = max_of<T, UNROLL>(raw);
     if (mx > s.m) {
-      s.z = s.z == 0.f ? 0.f : s.z * reweight(s.m, mx, r.c);
+      s.z *= reweight(s.m, mx, r.c);  // (0 and finite, or a finite product)
       s.m = mx;
       best = v;
     } else if (mx == s.m && best < 0) {
@@ -270,15 +275,24 @@ __global__ void __launch_bounds__(THREADS, PER_SM) verify_stats_kernel(VerifyArg
     }
     const float ref = s.m * r.c;
     float z = 0.f;
+    if (__builtin_expect(small_ref(ref), 1)) {
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      float x[VN];
-      unpack<T>(raw[j], x);
+      for (int j = 0; j < UNROLL; ++j) {
+        float x[VN];
+        unpack<T>(raw[j], x);
 #pragma unroll
-      for (int e = 0; e < VN; ++e) z += ex2(fmaf(x[e], r.c, -ref));
+        for (int e = 0; e < VN; ++e) z += ex2(fmaf(x[e], r.c, -ref));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) {
+        float x[VN];
+        unpack<T>(raw[j], x);
+#pragma unroll
+        for (int e = 0; e < VN; ++e) z += ex2((x[e] - s.m) * r.c);
+      }
     }
-    // NaN logits, nothing but -inf so far, or a maximum near the type's limits
-    if (!(z < CUDART_INF_F) || !(fabsf(ref) < HUGE_REF)) {
+    if (!(z < CUDART_INF_F)) {  // NaN logits, an infinite maximum, or nothing but -inf so far
       z = 0.f;
 #pragma unroll 1
       for (int j = 0; j < UNROLL; ++j)
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) verify_stats_kernel(VerifyArg
   if (i == r.nv) return;
   // draft i: accepted, or the row ends here at the latest
   bool ok = false;
-  if (draft >= 0 && draft < a.V && s.z > 0.f)
+  if (draft >= 0 && draft < a.V && s.m != -CUDART_INF_F)
     ok = r.greedy ? draft == s.arg : u < weight_any(l_draft, s.m, r.c) / s.z;
   if (!ok) atomicMin(a.stop + b, i);
 }
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, Q ? 3 : 4) verify_draw_kernel(VerifyA
   int token = -1;
   if (r.greedy) {
     __syncthreads();
-    if (z > 0.f) token = __float_as_int(st.z);
+    if (m != -CUDART_INF_F) token = __float_as_int(st.z);
   } else {
     const long long at = r.first + acc;
     const T *row = static_cast<const T *>(a.logits) + at * a.stride;
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, Q ? 3 : 4) verify_draw_kernel(VerifyA
     constexpr int VN = Span<T>::VN;
     Best s{0.f, 0x7fffffff}, f{0.f, 0x7fffffff};  // of the residual; of p, should that be empty
     const float inv_z = 1.f / z, ref = m * r.c;
-    const bool plain = fabsf(ref) < HUGE_REF;  // (m is finite, so only a NaN logit needs more)
+    const bool plain = small_ref(ref);  // (m is finite, so only a NaN logit needs more)
     // weight over noise: of the residual, and of p
     auto pair = [&](int j, float l, float nz, float qj, float &of_s, float &of_f) {
       const float e = plain ? ex2(fmaf(l, r.c, -ref)) : weight_any(l, m, r.c);
