@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM<D>)
   uint32_t bits = 0;
   const KvShare share = kv_share<KvFew, THREADS>(a, WARPS, &bits);
   if (share.begin >= share.end) {
-    if (bits && tid == 0) atomicOr(a.err, bits);
+    if (bits) atomicOr(a.err, bits);  // (each thread looked at rows of its own)
     return;
   }
   const uint32_t q_at = smem_addr(smem) + WARPS * S * 2 * HALF;

@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM)
   uint32_t bits = 0;
   const KvShare share = kv_share<KvMany, THREADS>(a, 2 * KvMany::cost(KvMany::M), &bits);
   if (share.begin >= share.end) {
-    if (bits && threadIdx.x == 0) atomicOr(a.err, bits);
+    if (bits) atomicOr(a.err, bits);  // (each thread looked at rows of its own)
     return;
   }
   unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
