@@ -359,7 +359,12 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvReadArgs a) {
   uint32_t bits = 0;
   const Segment g = segment_of(
       a.out_start, a.B, a.N, a.table, a.max_pages, a.c.num_pages, P, blockIdx.x,
-      [&](int b, int) { return min(__ldg(a.from + b), PAST); }, &bits);
+      [&](int b, int count) {
+        const int from = __ldg(a.from + b);
+        if (from < 0 && count > 0) bits |= SGD_KV_ERR_LENGTH;  // reads as what lies past the table: 0
+        return from < 0 ? PAST : min(from, PAST);
+      },
+      &bits);
   // outputs that no row claims
   const int claimed = min(max(__ldg(a.out_start + a.B), 0), a.N);
   if (claimed < a.N) {

@@ -25,3 +25,21 @@ def test_attend_reports_starts_when_no_row_has_work(KV, starts, max_q):
     p.kv.attend(q, p.dev_table, _i32([40, 40]), _i32([0, 0, 0]), max_q, out=out)
     assert p.kv.get_error() == 0
     p.kv.close()
+
+
+@pytest.mark.parametrize("B", [2, 40])         # (up to 32 rows are searched by one warp)
+def test_read_before_the_first_position_gives_zeros(KV, B):
+    from model_free_suffix_gb300 import _lib as L
+    lens = [40] * B
+    p = Pair(KV, lens, P=16, H=2, D=64)
+    p.write(lens, lens)
+    out = tuple(torch.full((3 * B, 2, 64), 7.0, dtype=torch.float32).cuda() for _ in range(2))
+    first = [4] * B
+    first[1] = -1
+    p.kv.read(p.dev_table, _i32(first), _i32([3 * b for b in range(B + 1)]), out=out)
+    assert p.kv.get_error(clear=True) & L.KV_ERR_LENGTH
+    for name, got in zip("kv", out):
+        for b in range(B):
+            want = torch.zeros(3, 2, 64).double() if b == 1 else p.ref.rows(name, p.table[b], 4, 7)
+            assert torch.equal(got[3 * b:3 * b + 3].cpu().double(), want)
+    p.kv.close()
