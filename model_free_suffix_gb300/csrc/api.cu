@@ -22,6 +22,7 @@
 #include "delta_sig.cuh"
 #include "row_index.cuh"
 #include "sgd_internal.h"
+#include "verify.h"
 
 using namespace sgd;
 

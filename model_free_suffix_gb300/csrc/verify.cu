@@ -27,6 +27,7 @@
 
 #include "num_types.cuh"
 #include "sgd_internal.h"
+#include "verify.h"
 
 namespace sgd {
 namespace {
