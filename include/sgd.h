@@ -330,8 +330,9 @@ int sgd_step_host(sgd_ctx *ctx, int32_t *token_ids, int32_t *num_tokens, const i
  *   num_accepted DEVICE int32 [B]: accepted drafts (without the token).
  *   logprobs   DEVICE float [B, k + 1] or NULL: log p of each emitted token (at
  *              temperature 1 for a row with t < 1e-5), 0 after.
- * V and k are the context's.  Two launches on `stream`; calls of one context
- * must not overlap.  SGD_EINVAL for sizes or NULL arguments. */
+ * V and k are the context's.  Two launches on `stream`, on the context's device
+ * whichever is current; calls of one context must not overlap.  SGD_EINVAL for
+ * sizes or NULL arguments. */
 int sgd_verify(sgd_ctx *ctx, const void *logits, int32_t dtype, int64_t row_stride,
                int64_t num_rows, const int32_t *row_start, const int32_t *drafts,
                const int32_t *num_valid, const uint8_t *active, int32_t B,
@@ -519,7 +520,8 @@ int sgd_memory(sgd_ctx *ctx, int64_t *device_bytes, int64_t *pinned_bytes);
  * 0; position j of row b lives in page block_table[b, j / page_size], slot
  * j % page_size.  A rejected draft needs no call: the next write starts at its
  * position.  All calls can be captured in a CUDA graph; calls of one handle
- * must not overlap. */
+ * must not overlap.  They run on the handle's device whichever is current, and
+ * leave the caller's current. */
 typedef struct sgd_kv sgd_kv; /* opaque, library-owned */
 
 typedef struct {

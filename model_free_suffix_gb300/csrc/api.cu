@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "delta_sig.cuh"
+#include "device_scope.h"
 #include "row_index.cuh"
 #include "sgd_internal.h"
 #include "verify.h"
@@ -831,6 +832,8 @@ int sgd_verify(sgd_ctx *x, const void *logits, int32_t dtype, int64_t row_stride
   a.err = x->d_err;
   a.stat = reinterpret_cast<float4 *>(x->d_verify + l.stat);
   a.stop = reinterpret_cast<int *>(x->d_verify + l.stop);
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   x->launches += 2;
   return check_cuda(launch_verify(a, dtype, (cudaStream_t)stream));
 }

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <new>
 
+#include "device_scope.h"
 #include "kv_internal.h"
 #include "sgd_internal.h"
 
@@ -64,7 +65,8 @@ int sgd_kv_create(const sgd_kv_config *cfg, int device, sgd_kv **out) {
   *out = nullptr;
   const int v = validate(*cfg);
   if (v != SGD_OK) return v;
-  if (cudaSetDevice(device) != cudaSuccess) return SGD_ECUDA;
+  const DeviceScope on(device);
+  if (!on.ok()) return SGD_ECUDA;
   sgd_kv *x = new (std::nothrow) sgd_kv;
   if (!x) return SGD_ENOMEM;
   x->cfg = *cfg;
@@ -90,7 +92,7 @@ int sgd_kv_create(const sgd_kv_config *cfg, int device, sgd_kv **out) {
 
 int sgd_kv_destroy(sgd_kv *x) {
   if (!x) return SGD_EINVAL;
-  cudaSetDevice(x->device);
+  const DeviceScope on(x->device);
   cudaDeviceSynchronize();
   cudaFree(x->d_err);
   cudaFree(x->d_work);
@@ -121,6 +123,8 @@ int sgd_kv_write(sgd_kv *x, const sgd_kv_layer *layer, const void *k, const void
   a.vec = aligned(k, 16) && aligned(v, 16) && k_token_stride % per == 0 && k_head_stride % per == 0 &&
           v_token_stride % per == 0 && v_head_stride % per == 0;
   a.err = x->d_err;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   x->launches++;
   return check_cuda(launch_kv_write(a, dtype, (cudaStream_t)stream));
 }
@@ -144,6 +148,8 @@ int sgd_kv_read(sgd_kv *x, const sgd_kv_layer *layer, const int32_t *block_table
   a.k = k;
   a.v = v;
   a.err = x->d_err;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   x->launches++;
   return check_cuda(launch_kv_read(a, dtype, (cudaStream_t)stream));
 }
@@ -177,6 +183,8 @@ int sgd_kv_attend(sgd_kv *x, const sgd_kv_layer *layer, const void *q, int32_t d
   a.sms = x->sms;
   a.work = x->d_work;
   a.err = x->d_err;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   int launches = 0;
   const cudaError_t e = launch_kv_attend(a, dtype, (cudaStream_t)stream, &launches);
   x->launches += launches;
@@ -185,7 +193,8 @@ int sgd_kv_attend(sgd_kv *x, const sgd_kv_layer *layer, const void *q, int32_t d
 
 int sgd_kv_get_error(sgd_kv *x, uint32_t *flags, int clear) {
   if (!x || !flags) return SGD_EINVAL;
-  if (cudaSetDevice(x->device) != cudaSuccess) return SGD_ECUDA;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return SGD_ECUDA;
   if (cudaMemcpy(flags, x->d_err, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return SGD_ECUDA;
   if (clear && cudaMemset(x->d_err, 0, 4) != cudaSuccess) return SGD_ECUDA;
