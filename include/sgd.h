@@ -21,7 +21,9 @@
  *   - Pointers marked DEVICE are caller-owned device memory of the context's
  *     GPU; the library never frees or keeps them past the call's stream work.
  *     Token buffers must be 16-byte aligned.
- *   - `stream` is a cudaStream_t (NULL = the legacy default stream).
+ *   - `stream` is a cudaStream_t of the context's GPU (NULL = its legacy default
+ *     stream).  Calls run on that GPU whichever is current, and leave the
+ *     caller's current (sgd_create leaves the new context's).
  *   - Problems found on the device (bad token ids, out-of-range lengths) are
  *     never traps: they set bits in a sticky device word (SGD_ERR_*), read by
  *     sgd_get_error, and the offending id or document is treated as a stop.
@@ -330,9 +332,8 @@ int sgd_step_host(sgd_ctx *ctx, int32_t *token_ids, int32_t *num_tokens, const i
  *   num_accepted DEVICE int32 [B]: accepted drafts (without the token).
  *   logprobs   DEVICE float [B, k + 1] or NULL: log p of each emitted token (at
  *              temperature 1 for a row with t < 1e-5), 0 after.
- * V and k are the context's.  Two launches on `stream`, on the context's device
- * whichever is current; calls of one context must not overlap.  SGD_EINVAL for
- * sizes or NULL arguments. */
+ * V and k are the context's.  Two launches on `stream`; calls of one context
+ * must not overlap.  SGD_EINVAL for sizes or NULL arguments. */
 int sgd_verify(sgd_ctx *ctx, const void *logits, int32_t dtype, int64_t row_stride,
                int64_t num_rows, const int32_t *row_start, const int32_t *drafts,
                const int32_t *num_valid, const uint8_t *active, int32_t B,
@@ -520,8 +521,7 @@ int sgd_memory(sgd_ctx *ctx, int64_t *device_bytes, int64_t *pinned_bytes);
  * 0; position j of row b lives in page block_table[b, j / page_size], slot
  * j % page_size.  A rejected draft needs no call: the next write starts at its
  * position.  All calls can be captured in a CUDA graph; calls of one handle
- * must not overlap.  They run on the handle's device whichever is current, and
- * leave the caller's current. */
+ * must not overlap.  Creating a cache leaves the caller's device current too. */
 typedef struct sgd_kv sgd_kv; /* opaque, library-owned */
 
 typedef struct {

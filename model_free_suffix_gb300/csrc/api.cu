@@ -522,7 +522,7 @@ int sgd_create(const sgd_config *cfg, int device, sgd_ctx **out) {
 
 int sgd_destroy(sgd_ctx *x) {
   if (!x) return SGD_EINVAL;
-  cudaSetDevice(x->device);
+  const DeviceScope on(x->device);
   if (x->worker.joinable()) {
     {
       std::unique_lock<std::mutex> lk(x->mu);
@@ -586,6 +586,8 @@ int sgd_update_state(sgd_ctx *x, int32_t *token_ids, int32_t *num_tokens, const 
   if (B == 0) return SGD_OK;
   if (!token_ids || !num_tokens || !sampled) return SGD_EINVAL;
   if (!aligned16(token_ids)) return SGD_EINVAL;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   x->launches++;
   return check_cuda(launch_update(token_ids, num_tokens, sampled, B, T, x->cfg.seq_capacity,
                                   x->cfg.vocab_size, x->d_err, x->ri, (cudaStream_t)stream));
@@ -613,6 +615,8 @@ static int propose_impl(sgd_ctx *x, int32_t *token_ids, int32_t *num_tokens, con
   a.score = score;
   a.probs = probs;
   a.match_info = match_info;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   if (a.nb > 1) {  // multi-length backoff: one kernel, the update included
     x->launches++;
     return check_cuda(launch_backoff(a, (cudaStream_t)stream));
@@ -690,6 +694,8 @@ int sgd_step(sgd_ctx *x, int32_t *token_ids, int32_t *num_tokens, const int32_t 
       x->inject = SGD_INJECT_NONE;
     }
   }
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   x->launches++;
   return check_cuda(launch_propose(a, (cudaStream_t)stream));
 }
@@ -704,6 +710,8 @@ int sgd_step_host(sgd_ctx *x, int32_t *token_ids, int32_t *num_tokens, const int
   if (B == 0) return SGD_OK;
   if (!h_sampled || !h_drafts || !h_num_valid) return SGD_EINVAL;
   if (n_docs > 0 && (!h_rows || !h_starts || !h_lengths)) return SGD_EINVAL;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   const size_t k = (size_t)x->cfg.k, BT = (size_t)B * T, m = (size_t)n_docs, Bk = (size_t)B * k;
   // In place: when every host buffer is page-locked and mapped into the GPU's
   // address space (cudaHostAlloc, pinned torch tensors), the kernel reads the
@@ -846,6 +854,8 @@ int sgd_ingest(sgd_ctx *x, const int32_t *token_ids, const int32_t *num_tokens, 
   if (n_docs < 0 || n_docs > x->cfg.max_ingest_docs || B < 0) return SGD_EINVAL;
   if (n_docs == 0) return SGD_OK;
   if (!token_ids || !rows || !starts || !lengths) return SGD_EINVAL;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   int launches = 0;
   const cudaError_t e =
       launch_ingest(token_ids, num_tokens, B, x->cfg.seq_capacity, x->cfg.vocab_size, rows, starts,
@@ -861,6 +871,8 @@ int sgd_build_sa(sgd_ctx *x, void *stream, void *side_stream) {
   if (!x->corpus) return SGD_ENOCORPUS;
   std::unique_lock<std::mutex> lk(x->mu);
   if (x->bstate != B_IDLE || x->job_ready) return SGD_EBUSY;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   const int back = 1 - x->front;
   int launches = 0;
   cudaError_t e = launch_linearize(x->d_ring, x->cfg.corpus_capacity, x->d_rs, x->d_doc_start,
@@ -899,6 +911,8 @@ int sgd_poll(sgd_ctx *x, int wait, int64_t timeout_us, void *stream, uint64_t *g
       return SGD_ETIMEDOUT;
     }
   }
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   x->bstate = B_IDLE;
   if (x->bstatus != SGD_OK) {
     if (generation) *generation = x->gen;
@@ -923,6 +937,8 @@ int sgd_suffix_array(sgd_ctx *x, const int32_t *text, int64_t n, int32_t *sa, vo
   if (n < 0 || n > x->cfg.corpus_capacity || (n > 0 && (!text || !sa))) return SGD_EINVAL;
   std::unique_lock<std::mutex> lk(x->mu);
   if (x->bstate != B_IDLE || x->job_ready) return SGD_EBUSY;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   cudaStream_t st = (cudaStream_t)stream;
   SaStats stats;
   int launches = 0;
@@ -952,7 +968,8 @@ int sgd_suffix_array(sgd_ctx *x, const int32_t *text, int64_t n, int32_t *sa, vo
 
 int sgd_get_error(sgd_ctx *x, uint32_t *flags, int clear) {
   if (!x || !flags) return SGD_EINVAL;
-  if (cudaSetDevice(x->device) != cudaSuccess) return SGD_ECUDA;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return SGD_ECUDA;
   uint32_t a = 0, b = 0;
   if (cudaMemcpy(&a, x->d_err, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return SGD_ECUDA;
@@ -970,6 +987,8 @@ int sgd_export_snapshot(sgd_ctx *x, int32_t *text, int32_t *sa, int64_t capacity
                         uint64_t *generation) {
   if (!x || !n) return SGD_EINVAL;
   if (!x->corpus) return SGD_ENOCORPUS;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return SGD_ECUDA;
   *n = x->front_n;
   if (generation) *generation = x->gen;
@@ -1026,6 +1045,8 @@ int sgd_save(sgd_ctx *x, const char *path, void *stream) {
     std::unique_lock<std::mutex> lk(x->mu);
     if (x->bstate != B_IDLE || x->job_ready) return SGD_EBUSY;
   }
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   cudaStream_t st = (cudaStream_t)stream;
   if (cudaStreamSynchronize(st) != cudaSuccess) return SGD_ECUDA;
   const int64_t C = x->cfg.corpus_capacity;
@@ -1111,6 +1132,8 @@ int sgd_load(sgd_ctx *x, const char *path, void *stream) {
     pos = (pos + dl[slot] + 1) % C;
   }
   if (tot != h.live || pos != h.wp) return SGD_EINVAL;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   cudaStream_t st = (cudaStream_t)stream;
   RingState r{};
   r.wp = h.wp;
@@ -1162,6 +1185,8 @@ int sgd_load(sgd_ctx *x, const char *path, void *stream) {
 int sgd_corpus_stats(sgd_ctx *x, int64_t *live_tokens, int32_t *ndocs) {
   if (!x) return SGD_EINVAL;
   if (!x->corpus) return SGD_ENOCORPUS;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return SGD_ECUDA;
   RingState r;
   if (cudaMemcpy(&r, x->d_rs, sizeof(r), cudaMemcpyDeviceToHost) != cudaSuccess) return SGD_ECUDA;
@@ -1194,6 +1219,8 @@ int sgd_reset_rows(sgd_ctx *x, const int32_t *token_ids, const int32_t *num_toke
   if (!x || m < 0 || m > (1 << 20)) return SGD_EINVAL;
   if (m == 0 || x->ri.tab == nullptr) return SGD_OK;
   if (!token_ids || !num_tokens || !rows) return SGD_EINVAL;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
   x->launches += 2;
   return check_cuda(launch_row_index_reset(x->ri, token_ids, num_tokens, x->cfg.seq_capacity, rows,
                                            m, x->cfg.max_batch, x->d_ri_claim, ++x->ri_epoch,

@@ -36,9 +36,9 @@ def _rational(x: Rational, denom: int = 10 ** 6) -> Tuple[int, int]:
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream_handle(stream, index: Optional[int] = None) -> int:
+def _stream_handle(stream, index: int) -> int:
     if stream is None:
-        return _raw_stream(torch.cuda.current_device() if index is None else index)
+        return _raw_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -166,7 +166,7 @@ class SuffixDrafter:
         self._check(self._lib.sgd_update_state(self._h, self._t(token_ids, name="token_ids"),
                                                self._t(num_tokens, name="num_tokens"),
                                                self._t(sampled, name="sampled"), B, T,
-                                               _stream_handle(stream)), "sgd_update_state")
+                                               _stream_handle(stream, self._index)), "sgd_update_state")
 
     def propose(self, token_ids: torch.Tensor, num_tokens: torch.Tensor,
                 active: Optional[torch.Tensor] = None, out: Optional[Proposal] = None,
@@ -177,7 +177,7 @@ class SuffixDrafter:
             self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"),
             self._t(active, torch.uint8, "active"), B, self._t(out.drafts), self._t(out.num_valid),
             self._t(out.score, torch.float32), self._t(out.probs, torch.float32),
-            self._t(out.match_info), _stream_handle(stream)), "sgd_propose")
+            self._t(out.match_info), _stream_handle(stream, self._index)), "sgd_propose")
         return out
 
     def propose_with_update(self, token_ids: torch.Tensor, num_tokens: torch.Tensor,
@@ -189,7 +189,7 @@ class SuffixDrafter:
             self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"),
             self._t(sampled, name="sampled"), T, self._t(active, torch.uint8, "active"), B,
             self._t(out.drafts), self._t(out.num_valid), self._t(out.score, torch.float32),
-            self._t(out.probs, torch.float32), self._t(out.match_info), _stream_handle(stream)),
+            self._t(out.probs, torch.float32), self._t(out.match_info), _stream_handle(stream, self._index)),
             "sgd_propose_with_update")
         return out
 
@@ -208,7 +208,7 @@ class SuffixDrafter:
             self._t(out.drafts), self._t(out.num_valid), self._t(out.score, torch.float32),
             self._t(out.probs, torch.float32), self._t(out.match_info),
             self._t(rows, name="rows"), self._t(starts, name="starts"),
-            self._t(lengths, name="lengths"), m, _stream_handle(stream)), "sgd_step")
+            self._t(lengths, name="lengths"), m, _stream_handle(stream, self._index)), "sgd_step")
         return out
 
     def step_host(self, token_ids: torch.Tensor, num_tokens: torch.Tensor, h_sampled: torch.Tensor,
@@ -228,7 +228,7 @@ class SuffixDrafter:
             H(h_starts, name="h_starts"), H(h_lengths, name="h_lengths"), m,
             H(h_drafts, name="h_drafts"), H(h_num_valid, name="h_num_valid"),
             H(h_score, torch.float32, "h_score"), H(h_probs, torch.float32, "h_probs"),
-            H(h_match_info, name="h_match_info"), _stream_handle(stream)), "sgd_step_host")
+            H(h_match_info, name="h_match_info"), _stream_handle(stream, self._index)), "sgd_step_host")
 
     def bind_step_host(self, token_ids: torch.Tensor, num_tokens: torch.Tensor,
                        h_sampled: torch.Tensor, h_rows: torch.Tensor, h_starts: torch.Tensor,
@@ -246,7 +246,7 @@ class SuffixDrafter:
                 H(h_starts, name="h_starts"), H(h_lengths, name="h_lengths"), h_rows.shape[0],
                 H(h_drafts, name="h_drafts"), H(h_num_valid, name="h_num_valid"),
                 H(h_score, torch.float32, "h_score"), H(h_probs, torch.float32, "h_probs"),
-                H(h_match_info, name="h_match_info"), _stream_handle(stream))
+                H(h_match_info, name="h_match_info"), _stream_handle(stream, self._index))
         keep = (token_ids, num_tokens, h_sampled, h_rows, h_starts, h_lengths, h_drafts, h_num_valid,
                 h_score, h_probs, h_match_info)  # the buffers outlive the bound call
 
@@ -338,17 +338,17 @@ class SuffixDrafter:
         self._check(self._lib.sgd_ingest(
             self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"), B,
             self._t(rows, name="rows"), self._t(starts, name="starts"), self._t(lengths, name="lengths"),
-            m, _stream_handle(stream)), "sgd_ingest")
+            m, _stream_handle(stream, self._index)), "sgd_ingest")
 
     harvest_finished = ingest
 
     def build_sa(self, side_stream, stream=None) -> int:
-        return self._check(self._lib.sgd_build_sa(self._h, _stream_handle(stream),
-                                                  _stream_handle(side_stream)), "sgd_build_sa")
+        return self._check(self._lib.sgd_build_sa(self._h, _stream_handle(stream, self._index),
+                                                  _stream_handle(side_stream, self._index)), "sgd_build_sa")
 
     def try_build_sa(self, side_stream, stream=None) -> int:
         """Like build_sa but returns SGD_EBUSY instead of raising."""
-        st = self._lib.sgd_build_sa(self._h, _stream_handle(stream), _stream_handle(side_stream))
+        st = self._lib.sgd_build_sa(self._h, _stream_handle(stream, self._index), _stream_handle(side_stream, self._index))
         if st < 0 and st != L.SGD_EBUSY:
             raise L.SgdError(st, "sgd_build_sa")
         return st
@@ -356,7 +356,7 @@ class SuffixDrafter:
     def poll(self, wait: bool = False, timeout_us: int = -1, stream=None,
              raise_on_error: bool = True) -> Tuple[int, int]:
         gen = ctypes.c_uint64()
-        st = self._lib.sgd_poll(self._h, int(bool(wait)), int(timeout_us), _stream_handle(stream),
+        st = self._lib.sgd_poll(self._h, int(bool(wait)), int(timeout_us), _stream_handle(stream, self._index),
                                 ctypes.byref(gen))
         if st < 0 and raise_on_error and st not in (L.SGD_ETIMEDOUT, L.SGD_EBUILD):
             raise L.SgdError(st, "sgd_poll")
@@ -367,7 +367,7 @@ class SuffixDrafter:
         n = text.shape[0]
         out = out if out is not None else torch.empty(n, dtype=torch.int32, device=self.device)
         self._check(self._lib.sgd_suffix_array(self._h, self._t(text, name="text"), n,
-                                               self._t(out, name="sa"), _stream_handle(stream)),
+                                               self._t(out, name="sa"), _stream_handle(stream, self._index)),
                     "sgd_suffix_array")
         return out
 
@@ -392,13 +392,13 @@ class SuffixDrafter:
     def save(self, path: str, stream=None) -> None:
         """Writes the corpus (ring, document FIFO, current snapshot) to `path`
         once the work queued on `stream` is done."""
-        self._check(self._lib.sgd_save(self._h, os.fsencode(path), _stream_handle(stream)),
+        self._check(self._lib.sgd_save(self._h, os.fsencode(path), _stream_handle(stream, self._index)),
                     "sgd_save")
 
     def load(self, path: str, stream=None) -> None:
         """Replaces the corpus with a saved one and rebuilds its index (on
         `stream`, waited for): the context then drafts as the saved one did."""
-        self._check(self._lib.sgd_load(self._h, os.fsencode(path), _stream_handle(stream)),
+        self._check(self._lib.sgd_load(self._h, os.fsencode(path), _stream_handle(stream, self._index)),
                     "sgd_load")
 
     def build_stats(self) -> dict:
@@ -422,7 +422,7 @@ class SuffixDrafter:
         row written other than through the library's updates."""
         self._check(self._lib.sgd_reset_rows(self._h, self._t(token_ids), self._t(num_tokens),
                                              self._t(rows, name="rows"), rows.shape[0],
-                                             _stream_handle(stream)),
+                                             _stream_handle(stream, self._index)),
                     "sgd_reset_rows")
 
     def set_row_stats(self, row_stats: Optional[torch.Tensor]) -> None:
