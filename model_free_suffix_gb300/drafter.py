@@ -279,7 +279,8 @@ class SuffixDrafter:
         [B, V], Exp(1) draws (``tensor.exponential_()``), are the random
         numbers; draft_probs [rows, V] float32 are the probabilities the drafts
         were drawn from (None: proposed outright, as by this drafter).
-        temperature [B] float32 (None: 1; below 1e-5: greedy)."""
+        temperature [B] float32 (None: 1; below 1e-5: greedy).  out, a Verdict
+        for B rows or more, takes the results in its first B rows."""
         B, (rows, V) = num_valid.shape[0], self._pair(logits, "logits")
         dtype = _DTYPES.get(logits.dtype)
         if dtype is None:
@@ -301,6 +302,11 @@ class SuffixDrafter:
             raise ValueError("active must have an entry per row")
         if out is None:
             out = self.new_verdict(B)
+        else:
+            self._room(out.sampled, B, (self.k + 1,), "out.sampled")
+            self._room(out.num_accepted, B, (), "out.num_accepted")
+            if out.logprobs is not None:
+                self._room(out.logprobs, B, (self.k + 1,), "out.logprobs")
         t = self._t
         x, x_stride = self._rows(logits, rows, logits.dtype, "logits")
         n, n_stride = self._rows(noise, B, torch.float32, "noise")
@@ -319,6 +325,11 @@ class SuffixDrafter:
         if t.dim() != 2:
             raise ValueError("%s must have two dimensions" % name)
         return tuple(t.shape)
+
+    @staticmethod
+    def _room(t: torch.Tensor, n: int, row: Tuple[int, ...], name: str) -> None:
+        if t.shape[1:] != row or t.dim() == 0 or t.shape[0] < n:
+            raise ValueError("%s must have at least %d rows of shape %s" % (name, n, row))
 
     def _rows(self, t: torch.Tensor, n: int, dtype, name: str):
         """Address and row stride of a tensor whose n rows may be apart but are
