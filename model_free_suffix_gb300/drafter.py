@@ -159,6 +159,19 @@ class SuffixDrafter:
                         torch.empty((B, self.k), dtype=torch.float32, device=d),
                         torch.empty((B, 2), dtype=torch.int32, device=d))
 
+    def _outputs(self, out: Optional[Proposal], B: int) -> Proposal:
+        if out is None:
+            return self.new_outputs(B)
+        self._sizes(B, out.drafts, out.num_valid, out.score, out.probs, out.match_info)
+        return out
+
+    def _sizes(self, B: int, drafts, num_valid, score, probs, match_info) -> None:
+        """A caller's outputs hold what B rows write (those that may be left out: None)."""
+        for t, n, name in ((drafts, B * self.k, "drafts"), (num_valid, B, "num_valid"), (score, B, "score"),
+                           (probs, B * self.k, "probs"), (match_info, 2 * B, "match_info")):
+            if t is not None and t.numel() < n:
+                raise ValueError("%s must hold %d values for %d rows" % (name, n, B))
+
     # -- drafting -----------------------------------------------------------
     def update_state(self, token_ids: torch.Tensor, num_tokens: torch.Tensor, sampled: torch.Tensor,
                      stream=None) -> None:
@@ -172,7 +185,7 @@ class SuffixDrafter:
                 active: Optional[torch.Tensor] = None, out: Optional[Proposal] = None,
                 stream=None) -> Proposal:
         B = num_tokens.shape[0]
-        out = out or self.new_outputs(B)
+        out = self._outputs(out, B)
         self._check(self._lib.sgd_propose(
             self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"),
             self._t(active, torch.uint8, "active"), B, self._t(out.drafts), self._t(out.num_valid),
@@ -184,7 +197,7 @@ class SuffixDrafter:
                             sampled: torch.Tensor, active: Optional[torch.Tensor] = None,
                             out: Optional[Proposal] = None, stream=None) -> Proposal:
         B, T = sampled.shape
-        out = out or self.new_outputs(B)
+        out = self._outputs(out, B)
         self._check(self._lib.sgd_propose_with_update(
             self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"),
             self._t(sampled, name="sampled"), T, self._t(active, torch.uint8, "active"), B,
@@ -201,7 +214,7 @@ class SuffixDrafter:
         read after the update: one kernel launch for up to 64 docs."""
         B, T = sampled.shape
         m = rows.shape[0]
-        out = out or self.new_outputs(B)
+        out = self._outputs(out, B)
         self._check(self._lib.sgd_step(
             self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"),
             self._t(sampled, name="sampled"), T, self._t(active, torch.uint8, "active"), B,
@@ -221,6 +234,7 @@ class SuffixDrafter:
         `stream`; the host outputs are valid once that stream is synchronised."""
         B, T = h_sampled.shape
         m = h_rows.shape[0]
+        self._sizes(B, h_drafts, h_num_valid, h_score, h_probs, h_match_info)
         H = self._host
         self._check(self._lib.sgd_step_host(
             self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"),
@@ -239,6 +253,7 @@ class SuffixDrafter:
         once: the returned function queues one step per call (new inputs are
         written into the same host buffers between calls)."""
         B, T = h_sampled.shape
+        self._sizes(B, h_drafts, h_num_valid, h_score, h_probs, h_match_info)
         H = self._host
         fn = self._lib.sgd_step_host
         args = (self._h, self._t(token_ids, name="token_ids"), self._t(num_tokens, name="num_tokens"),
