@@ -31,14 +31,11 @@ def _rational(x: Rational, denom: int = 10 ** 6) -> Tuple[int, int]:
     return f.numerator, f.denominator
 
 
-# (the current stream's handle, without the Stream object that
-# torch.cuda.current_stream() makes first)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _stream_handle(stream, index: int) -> int:
     if stream is None:
-        return _raw_stream(index)
+        # (the handle alone, without the Stream object that torch.cuda.current_stream()
+        # makes; looked up here since a torch built without CUDA has no such name)
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
