@@ -570,6 +570,9 @@ int sgd_kv_destroy(sgd_kv *kv);
  * A block's scale is the smallest power of two that brings its largest
  * magnitude, over the entries before the first new token and the new ones, to
  * at most 448; entries already there are encoded again where that changes it.
+ * That is exact but where they become subnormal, within 2^-10 of the new scale
+ * then, and is not undone: after a rejected draft much larger than its block's
+ * other entries the scale comes down again, the bits that they lost do not.
  * Pages that two rows share must not be written by both. */
 int sgd_kv_write(sgd_kv *kv, const sgd_kv_layer *layer, const void *k, const void *v,
                  int32_t dtype, int64_t k_token_stride, int64_t k_head_stride,

@@ -10,9 +10,12 @@
 //     for magnitudes that become subnormal; a larger mantissa in the scale
 //     would gain at most one bit of headroom and round every old entry again.
 // The scale is made anew at each write from the entries that count (those
-// before the write's first token, and the new ones): a rejected draft's values
-// leave nothing behind.  Infinities do not count towards the scale and
-// saturate, NaN is stored as 0; both set an error bit.
+// before the write's first token, and the new ones), so a rejected draft's
+// values do not stay in it.  What they may have cost the block's other entries
+// does: while the draft was there they were held at its scale s, each within
+// 2^-10 s of what it was, and those of up to 2^-10 s as 0.
+// Infinities do not count towards the scale and saturate, NaN is stored as 0;
+// both set an error bit.
 #include <math_constants.h>
 
 #include "kv_internal.h"

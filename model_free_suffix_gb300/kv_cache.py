@@ -31,7 +31,9 @@ class KVCache:
     The tokens of a call are packed: row b's are q_start[b] .. q_start[b + 1],
     the last ones of its seq_lens[b] tokens.  For a verification pass these are
     the row's last token and its drafts; after it, seq_lens simply does not
-    advance past a rejected draft and the next write overwrites it.
+    advance past a rejected draft and the next write overwrites it.  (A draft of
+    much larger keys or values than its page's other tokens holds these at its
+    scale, within 2^-10 of it, and they stay so rounded when it is rejected.)
     """
 
     def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_batch: int,
