@@ -549,9 +549,10 @@ typedef struct {
                                      tokens are not written, read as 0, not attended to  */
 #define SGD_KV_ERR_LENGTH    0x2u /* fewer tokens in a row than new ones, or more than its
                                      table holds, or starts that do not ascend within the
-                                     call's tokens: such a row is passed over. A first
-                                     position below 0: the row reads as 0. Outputs of
-                                     sgd_kv_read from out_start[B] on are 0              */
+                                     call's tokens: such a row is passed over (outputs of
+                                     sgd_kv_attend are 0 where only its length is wrong).
+                                     A first position below 0: the row reads as 0. Outputs
+                                     of sgd_kv_read from out_start[B] on are 0           */
 #define SGD_KV_ERR_WAIT      0x8u /* sgd_kv_attend: a copy never arrived; results are not valid */
 #define SGD_KV_ERR_NONFINITE 0x4u /* written as the largest magnitude (infinities) or 0 (NaN) */
 

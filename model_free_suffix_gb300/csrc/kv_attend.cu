@@ -9,7 +9,7 @@
 // 2^(m - m') before the tile's 2^(s - m') are added (kv_attend.cuh has the
 // scales of the blocks, and when this scaling is due).
 // Rows of the query heads that share a head of keys and values go together, so
-// that each byte of the cache is read once for all of them.
+// that each byte of the cache is read once for all rows of a unit (16 here).
 //
 // Bound by reading the cache: at 256 batch rows of one token over 1024 to 4096
 // cached ones, 8 heads of 128, 1.35 GB: 228 us, 5.9 TB/s, with 8 query heads a
@@ -55,10 +55,11 @@ struct KvFew {
 // unit ends.
 //
 // e4m3 is taken to f16, exactly, on the way into the registers that feed the
-// matrix instructions, so the products carry no rounding of the cache's; q goes
-// to f16 after each row is scaled to [1, 2) by a power of two (bf16 has fewer
-// bits than f16: only elements 2^-24 times the row's largest lose any), and the
-// probabilities to f16 (relative 2^-12 each; the sum l is taken before that
+// matrix instructions, so the products carry no rounding of the cache's.  q goes
+// to f16 after each row is scaled by a power of two that brings its largest
+// element to [1, 2): exact down to 2^-17 of it for bf16 and 2^-14 for f16, where
+// f16's last place is 2^-24; smaller elements move by 2^-25 at most.  The
+// probabilities go to f16 (relative 2^-12 each; the sum l is taken before that
 // rounding).
 //
 // The order of the elements of a product's long axis is free as long as both

@@ -131,7 +131,7 @@ __device__ __forceinline__ void kv_queries(const KvAttendArgs &a, const Walk &w,
 }
 
 // The parts of a unit that cuts go through, by all threads of the CTAs that hold
-// them, once each has stored its part: the last joins them.  Sixteen rows at a
+// them, once each has stored its part: the last joins them.  JOIN_ROWS rows at a
 // time: the parts' weights 2^(m - max) first, then the sums with the loads of
 // several parts in flight.  scratch: kv_join_floats() of shared memory.
 constexpr int JOIN_ROWS = 8;

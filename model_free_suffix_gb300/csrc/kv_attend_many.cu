@@ -5,8 +5,8 @@
 // The mathematics is that of kv_attend.cu.  Here the 4 warps of a CTA take every
 // 64-token tile together: each has 16 of its tokens for s = q . k, of all rows,
 // and a quarter of the dims for o += p v, of all rows and all tokens, so that
-// each byte of the cache is taken from e4m3 to f16 by one lane once, however
-// many rows there are.  The probabilities cross over through shared memory.
+// each byte of the cache is taken from e4m3 to f16 by one lane once for all rows
+// of the unit.  The probabilities cross over through shared memory.
 // Two barriers a tile: one that also tells whether any row's maximum has moved
 // (else there is nothing to exchange), one before the probabilities are read.
 //

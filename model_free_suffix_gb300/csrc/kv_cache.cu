@@ -232,10 +232,11 @@ __device__ __forceinline__ __half2 top_of(__half2 top, const uint4 &v) {
 // 8 heads of 128, 31 MB with the entries already there: 12 us, 2.5 TB/s; 4 tokens
 // of one row: 4 us), by the bytes and the conversions at prompts (8 rows, 30620
 // tokens, 188 MB: 46 us, 4.1 TB/s).  A page and head is one team's, since the
-// scale needs every entry before any is encoded, and the new ones are read once:
-// a lane keeps its entries in registers.  (Eight loads of old entries in flight
-// instead of four, or wider ones, cost more registers than they gain: 36 us for
-// that step and its read back against 32.)
+// scale needs every entry before any is encoded.  A warp keeps 1024 new entries
+// in registers; where its share of a page is larger (single warps at prompts) it
+// reads them a second time, from L2, to encode them.  (Eight loads of old entries
+// in flight instead of four, or wider ones, cost more registers than they gain:
+// 36 us for that step and its read back against 32.)
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 3 : 4) kv_write_kernel(KvWriteArgs a) {
   __shared__ float team_max[2][WARPS];

@@ -567,7 +567,8 @@ cudaError_t launch(const VerifyArgs &a, cudaStream_t st) {
 }
 
 // CTAs of a row of logits: a power of two, until there are three CTAs per SM,
-// in pieces of at least 2048 elements (a 16-byte load per thread).  Measured
+// in pieces of more than 1024 elements (a 16-byte load for each thread at 32
+// bits, for half of them at 16).  Measured
 // at V = 151936, B = 256, k = 16: 1 piece 142 us, 2 150, 4 182, 8 269 (each CTA
 // costs its start and its joining); at V = 128256, B = 48, k = 5, 32-bit logits:
 // 1 piece 48 us, 2 41, 8 44; at V = 32000, B = 4, k = 8: 1 piece 11.5 us, 8 10.5.
