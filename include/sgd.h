@@ -554,6 +554,8 @@ typedef struct {
                                      A first position below 0: the row reads as 0. Outputs
                                      of sgd_kv_read from out_start[B] on are 0           */
 #define SGD_KV_ERR_WAIT      0x8u /* sgd_kv_attend: a copy never arrived; results are not valid */
+#define SGD_KV_ERR_ROOM      0x10u /* sgd_kv_assign: new tokens of a row had no place among the
+                                     call's N, or no free pages: the row got none of them */
 #define SGD_KV_ERR_NONFINITE 0x4u /* written as the largest magnitude (infinities) or 0 (NaN) */
 
 /* SGD_EINVAL for a geometry outside the limits above. */
@@ -606,6 +608,80 @@ int sgd_kv_attend(sgd_kv *kv, const sgd_kv_layer *layer, const void *q, int32_t 
                   int64_t q_token_stride, int64_t q_head_stride, const int32_t *block_table,
                   const int32_t *seq_lens, const int32_t *q_start, int32_t B, int32_t N,
                   int32_t max_q, float scale, int32_t window, int32_t sinks, void *out,
+                  void *stream);
+
+/* ---- prompts -------------------------------------------------------------
+ *
+ * A step that takes in prompts, whole or in chunks, next to the rows that
+ * decode: sgd_kv_assign finds pages for all of its tokens, sgd_kv_write puts
+ * their keys and values there, and the attention below is for rows of many new
+ * tokens, on the tensor cores, with the new tokens' keys and values as the model
+ * gave them (in 16 bits; whether they were written yet makes no difference). */
+
+/* Whole prompts: packed sequences, row b's tokens q_start[b] .. q_start[b + 1] at
+ * positions 0, 1, ..  The token at position p sees positions j <= p of its row;
+ * with window > 0 those with j > p - window or j < sinks.
+ *   q    DEVICE dtype (SGD_F16 or SGD_BF16) [N, q_heads, head_dim], k, v likewise
+ *        [N, kv_heads, head_dim]: strides in elements, the last dimension
+ *        contiguous (parts of one projection's output are taken as they are;
+ *        starts and strides of whole 16 bytes are faster).
+ *   q_start DEVICE int32 [B + 1], ascending from 0 to at most N.
+ *   out  DEVICE dtype [N, q_heads, head_dim], contiguous, 16-byte aligned.
+ * Infinities and NaN in q, k or v reach the tokens that see them, and no others.
+ * Tokens from q_start[B] on belong to no row: nothing is read or written there.
+ * Rows with bad starts are passed over and reported (SGD_KV_ERR_LENGTH).
+ * B <= SGD_KV_NEW_MAX_ROWS (SGD_ETOOLARGE). */
+#define SGD_KV_NEW_MAX_ROWS 8192
+int sgd_kv_attend_prompt(sgd_kv *kv, const void *q, const void *k, const void *v, int32_t dtype,
+                         int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const int32_t *q_start, int32_t B, int32_t N, float scale,
+                         int32_t window, int32_t sinks, void *out, void *stream);
+
+/* Chunks: as sgd_kv_attend_prompt, with row b's new tokens the last ones of its
+ * seq_lens[b] tokens; what they see of the positions before them is read from
+ * the cache, as sgd_kv_attend does, by block_table (its entries for the earlier
+ * positions; positions in a page that is not there are not seen, and reported).
+ * Rows whose lengths make no sense give 0 and are reported (SGD_KV_ERR_LENGTH).
+ * The bytes 0x7f and 0xff, which no write leaves, count as +-480 times the scale. */
+int sgd_kv_attend_chunk(sgd_kv *kv, const sgd_kv_layer *layer, const void *q, const void *k,
+                        const void *v, int32_t dtype, int64_t q_token_stride,
+                        int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride,
+                        const int32_t *block_table, const int32_t *seq_lens,
+                        const int32_t *q_start, int32_t B, int32_t N, float scale,
+                        int32_t window, int32_t sinks, void *out, void *stream);
+
+/* Who holds which page, all DEVICE memory of the caller.  To begin with: held 0,
+ * block_table -1, free the ids of all pages, free_count their number. */
+typedef struct {
+  int32_t *block_table; /* [max_batch, max_pages_per_row]: -1 from a row's pages on   */
+  int32_t *held;        /* [max_batch] pages of each row                              */
+  int32_t *free;        /* [num_pages] free page ids, the first free_count of them    */
+  int32_t *free_count;  /* [1]                                                        */
+} sgd_kv_pages;
+
+/* Pages for a step: row b keeps its first keep[b] tokens and gets fresh[b] new ones
+ * behind them, so it needs ceil((keep + fresh) / page_size) pages.  (After a
+ * verification keep is what was accepted; keep = fresh = 0 gives a row's pages
+ * back.)  In this order: rows of which a length makes no sense (negative, keep
+ * beyond the row's pages, both together beyond the table) keep their pages and get
+ * nothing; new tokens are packed row by row, and a row whose tokens would end
+ * beyond N gets none; pages that rows no longer need go to the end of the free
+ * list, in the order of the rows and of their tables; pages wanted come from
+ * the end of the list, in that order too, and a row whose pages, with those wanted
+ * by the rows before it, are more than there are gets neither pages nor tokens.
+ * All such rows are reported (SGD_KV_ERR_LENGTH, SGD_KV_ERR_ROOM).
+ *   keep, fresh DEVICE int32 [B] (B <= SGD_KV_ASSIGN_MAX_ROWS, else SGD_ETOOLARGE).
+ *   seq_lens DEVICE int32 [B]: keep + what it got of fresh (a row that makes no
+ *            sense: 0); q_start DEVICE int32 [B + 1].  seq_lens may be keep or fresh.
+ *   positions, slots, rows DEVICE int32 [N] or null: of each packed token its
+ *            position, its place page * page_size + slot in a layer, and its row;
+ *            from q_start[B] on 0, -1 and -1. */
+#define SGD_KV_ASSIGN_MAX_ROWS 8192
+int sgd_kv_assign(sgd_kv *kv, const sgd_kv_pages *pages, const int32_t *keep,
+                  const int32_t *fresh, int32_t B, int32_t N, int32_t *seq_lens,
+                  int32_t *q_start, int32_t *positions, int32_t *slots, int32_t *rows,
                   void *stream);
 
 /* As sgd_get_error, sgd_memory and sgd_launch_count, of a cache handle. */

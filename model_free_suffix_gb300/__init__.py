@@ -5,7 +5,7 @@ include/sgd.h); this package holds the ctypes binding, the build step and the
 seeded workload generators.
 """
 from .drafter import Proposal, SuffixDrafter, Verdict  # noqa: F401
-from .kv_cache import KVCache  # noqa: F401
+from .kv_cache import KVCache, KVPages, PagePlan  # noqa: F401
 from . import _lib  # noqa: F401
 
-__all__ = ["SuffixDrafter", "Proposal", "Verdict", "KVCache"]
+__all__ = ["SuffixDrafter", "Proposal", "Verdict", "KVCache", "KVPages", "PagePlan"]

@@ -37,6 +37,7 @@ KV_ERR_PAGE = 0x1
 KV_ERR_LENGTH = 0x2
 KV_ERR_NONFINITE = 0x4
 KV_ERR_WAIT = 0x8
+KV_ERR_ROOM = 0x10
 
 F32 = 0
 F16 = 1
@@ -115,6 +116,15 @@ class SgdKvLayer(ctypes.Structure):
     ]
 
 
+class SgdKvPages(ctypes.Structure):
+    _fields_ = [
+        ("block_table", ctypes.c_void_p),
+        ("held", ctypes.c_void_p),
+        ("free", ctypes.c_void_p),
+        ("free_count", ctypes.c_void_p),
+    ]
+
+
 class SgdError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -154,6 +164,11 @@ def load() -> ctypes.CDLL:
         "sgd_kv_read": (ctypes.c_int, [P, P, P, P, P, i32, i32, P, P, i32, P]),
         "sgd_kv_attend": (ctypes.c_int, [P, P, P, i32, i64, i64, P, P, P, i32, i32, i32,
                                          ctypes.c_float, i32, i32, P, P]),
+        "sgd_kv_attend_prompt": (ctypes.c_int, [P, P, P, P, i32, i64, i64, i64, i64, i64, i64, P, i32, i32,
+                                                ctypes.c_float, i32, i32, P, P]),
+        "sgd_kv_attend_chunk": (ctypes.c_int, [P, P, P, P, P, i32, i64, i64, i64, i64, i64, i64, P, P, P, i32,
+                                               i32, ctypes.c_float, i32, i32, P, P]),
+        "sgd_kv_assign": (ctypes.c_int, [P, P, P, P, i32, i32, P, P, P, P, P, P]),
         "sgd_kv_get_error": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]),
         "sgd_kv_memory": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_int64)]),
         "sgd_kv_launch_count": (ctypes.c_int, [P, u64p]),

@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libsgd.so")
 SOURCES = ["propose.cu", "backoff.cu", "corpus.cu", "sa_build.cu", "verify.cu", "kv_cache.cu",
-           "kv_attend.cu", "kv_attend_many.cu", "kv_api.cu", "api.cu", "noalloc.cu"]
+           "kv_attend.cu", "kv_attend_many.cu", "kv_prompt.cu", "kv_assign.cu", "kv_api.cu", "api.cu", "noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

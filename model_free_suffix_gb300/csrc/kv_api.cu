@@ -1,6 +1,7 @@
 // kv_api.cu -- host side of the paged 8-bit cache: argument checks and launches
 // on the caller's streams.  The cache's memory is the caller's; a handle holds
 // its geometry, the attention's workspace and an error word.
+#include <algorithm>
 #include <atomic>
 #include <new>
 
@@ -71,13 +72,15 @@ int sgd_kv_create(const sgd_kv_config *cfg, int device, sgd_kv **out) {
   if (!x) return SGD_ENOMEM;
   x->cfg = *cfg;
   x->device = device;
-  x->work_bytes = kv_attend_workspace();
-  cudaError_t e = cudaMalloc((void **)&x->d_err, 4);
+  cudaError_t e = cudaDeviceGetAttribute(&x->sms, cudaDevAttrMultiProcessorCount, device);
+  x->work_bytes = std::max(kv_attend_workspace(), kv_new_workspace(x->sms));
+  if (e == cudaSuccess) e = cudaMalloc((void **)&x->d_err, 4);
   if (e == cudaSuccess) e = cudaMemset(x->d_err, 0, 4);
   if (e == cudaSuccess) e = cudaMalloc((void **)&x->d_work, x->work_bytes);
   if (e == cudaSuccess) e = cudaMemset(x->d_work, 0, x->work_bytes);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&x->sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) e = kv_attend_set_limits();
+  if (e == cudaSuccess) e = kv_new_set_limits();
+  if (e == cudaSuccess) e = kv_assign_set_limits();
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     cudaFree(x->d_err);
@@ -189,6 +192,119 @@ int sgd_kv_attend(sgd_kv *x, const sgd_kv_layer *layer, const void *q, int32_t d
   const cudaError_t e = launch_kv_attend(a, dtype, (cudaStream_t)stream, &launches);
   x->launches += launches;
   return check_cuda(e);
+}
+
+}  // extern "C"
+
+// What sgd_kv_attend_prompt and sgd_kv_attend_chunk share, once their rows and layer are checked.
+static int attend_new(sgd_kv *x, KvNewArgs &a, const void *q, const void *k, const void *v, int32_t dtype,
+                      int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, float scale,
+                      int32_t window, int32_t sinks, void *out, void *stream) {
+  if (!q || !k || !v || !out || !aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(out, 16))
+    return SGD_EINVAL;
+  if (q_token_stride < 0 || q_head_stride < 0 || k_token_stride < 0 || k_head_stride < 0 ||
+      v_token_stride < 0 || v_head_stride < 0)
+    return SGD_EINVAL;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
+  a.q_vec = aligned(q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
+  a.k_vec = aligned(k, 16) && k_token_stride % 8 == 0 && k_head_stride % 8 == 0;
+  a.v_vec = aligned(v, 16) && v_token_stride % 8 == 0 && v_head_stride % 8 == 0;
+  a.out = out;
+  a.q_heads = x->cfg.q_heads;
+  a.group = x->cfg.q_heads / x->cfg.kv_heads;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.sms = x->sms;
+  a.work = x->d_work;
+  a.err = x->d_err;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
+  int launches = 0;
+  const cudaError_t e = launch_kv_new(a, dtype, (cudaStream_t)stream, &launches);
+  x->launches += launches;
+  return check_cuda(e);
+}
+
+extern "C" {
+
+int sgd_kv_attend_prompt(sgd_kv *x, const void *q, const void *k, const void *v, int32_t dtype,
+                         int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const int32_t *q_start, int32_t B, int32_t N, float scale, int32_t window,
+                         int32_t sinks, void *out, void *stream) {
+  if (!x || (dtype != SGD_F16 && dtype != SGD_BF16)) return SGD_EINVAL;
+  if (B < 0 || B > x->cfg.max_batch || N < 0 || window < 0 || sinks < 0 || !(scale == scale)) return SGD_EINVAL;
+  if (B > SGD_KV_NEW_MAX_ROWS) return SGD_ETOOLARGE;
+  if (B == 0 || N == 0) return SGD_OK;
+  if (!q_start) return SGD_EINVAL;
+  KvNewArgs a{};
+  a.c.heads = x->cfg.kv_heads;
+  a.c.page = x->cfg.page_size;
+  a.c.dim = x->cfg.head_dim;
+  while (1 << a.c.page_bits < a.c.page) ++a.c.page_bits;
+  a.r = KvRows{nullptr, q_start, nullptr, B, N, 0};
+  return attend_new(x, a, q, k, v, dtype, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                    v_token_stride, v_head_stride, scale, window, sinks, out, stream);
+}
+
+int sgd_kv_attend_chunk(sgd_kv *x, const sgd_kv_layer *layer, const void *q, const void *k, const void *v,
+                        int32_t dtype, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                        int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                        const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_start, int32_t B,
+                        int32_t N, float scale, int32_t window, int32_t sinks, void *out, void *stream) {
+  if (!x || (dtype != SGD_F16 && dtype != SGD_BF16)) return SGD_EINVAL;
+  KvNewArgs a{};
+  int s = rows(x, block_table, seq_lens, q_start, B, N, &a.r);
+  if (s != SGD_OK) return s;
+  if (window < 0 || sinks < 0 || !(scale == scale)) return SGD_EINVAL;
+  if (B > SGD_KV_NEW_MAX_ROWS) return SGD_ETOOLARGE;
+  if (B == 0 || N == 0) return SGD_OK;
+  s = view(x, layer, &a.c);
+  if (s != SGD_OK) return s;
+  return attend_new(x, a, q, k, v, dtype, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                    v_token_stride, v_head_stride, scale, window, sinks, out, stream);
+}
+
+int sgd_kv_assign(sgd_kv *x, const sgd_kv_pages *pages, const int32_t *keep, const int32_t *fresh, int32_t B,
+                  int32_t N, int32_t *seq_lens, int32_t *q_start, int32_t *positions, int32_t *slots,
+                  int32_t *row_ids, void *stream) {
+  if (!x || !pages) return SGD_EINVAL;
+  if (B < 0 || B > x->cfg.max_batch || N < 0) return SGD_EINVAL;
+  if (B > SGD_KV_ASSIGN_MAX_ROWS) return SGD_ETOOLARGE;
+  if (!pages->block_table || !pages->held || !pages->free || !pages->free_count || !q_start) return SGD_EINVAL;
+  if (B > 0 && (!keep || !fresh || !seq_lens)) return SGD_EINVAL;
+  KvAssignArgs a{};
+  a.table = pages->block_table;
+  a.held = pages->held;
+  a.free = pages->free;
+  a.free_count = pages->free_count;
+  a.keep = keep;
+  a.fresh = fresh;
+  a.B = B;
+  a.N = N;
+  a.max_pages = x->cfg.max_pages_per_row;
+  a.num_pages = x->cfg.num_pages;
+  while (1 << a.page_bits < x->cfg.page_size) ++a.page_bits;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.positions = positions;
+  a.slots = slots;
+  a.rows = row_ids;
+  a.err = x->d_err;
+  const DeviceScope on(x->device);
+  if (!on.ok()) return SGD_ECUDA;
+  x->launches++;
+  return check_cuda(launch_kv_assign(a, (cudaStream_t)stream));
 }
 
 int sgd_kv_get_error(sgd_kv *x, uint32_t *flags, int clear) {

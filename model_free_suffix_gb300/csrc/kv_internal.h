@@ -60,11 +60,43 @@ struct KvAttendArgs {
   uint32_t *err;
 };
 
+// Attention of new tokens whose keys and values are given: over these, and over
+// what the cache holds of the positions before them (r.seq_lens null: nothing).
+struct KvNewArgs {
+  KvView c;
+  KvRows r;
+  const void *q, *k, *v;
+  long long q_token, q_head, k_token, k_head, v_token, v_head;  // strides in elements
+  int q_vec, k_vec, v_vec;                                      // 16-byte loads allowed
+  void *out;                                                    // [N, q_heads, dim]
+  int q_heads, group;
+  float scale;
+  int window, sinks;
+  int sms;
+  unsigned char *work;  // as KvAttendArgs: the counters in front are not touched
+  uint32_t *err;
+};
+
+// Pages and places of a step's tokens.
+struct KvAssignArgs {
+  int32_t *table, *held, *free, *free_count;  // the pages' state
+  const int32_t *keep, *fresh;                // [B] tokens that stay, new tokens
+  int B, N, max_pages, num_pages, page_bits;
+  int32_t *seq_lens, *q_start;          // [B], [B + 1]
+  int32_t *positions, *slots, *rows;    // [N] each, or null
+  uint32_t *err;
+};
+
 cudaError_t launch_kv_write(const KvWriteArgs &a, int dtype, cudaStream_t st);
 cudaError_t launch_kv_read(const KvReadArgs &a, int dtype, cudaStream_t st);
 size_t kv_attend_workspace();
 cudaError_t kv_attend_set_limits();
 cudaError_t launch_kv_attend(KvAttendArgs a, int dtype, cudaStream_t st, int *launches);
+size_t kv_new_workspace(int sms);
+cudaError_t kv_new_set_limits();
+cudaError_t launch_kv_new(const KvNewArgs &a, int dtype, cudaStream_t st, int *launches);
+cudaError_t kv_assign_set_limits();
+cudaError_t launch_kv_assign(const KvAssignArgs &a, cudaStream_t st);
 
 #ifdef __CUDACC__
 // Two e4m3 bytes (the low 16 bits) as two f16: exact, every e4m3 value is one.

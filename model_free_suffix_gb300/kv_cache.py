@@ -8,6 +8,7 @@ point of include/sgd.h.
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 from typing import Optional, Tuple
 
 import torch
@@ -16,6 +17,25 @@ from . import _lib as L
 from .drafter import _DTYPES, SuffixDrafter, _stream_handle
 
 _F8 = torch.float8_e4m3fn
+
+
+@dataclass
+class KVPages:
+    """Who holds which page (KVCache.new_pages, KVCache.assign)."""
+    block_table: torch.Tensor  # [max_batch, max_pages_per_row] int32, -1 from a row's pages on
+    held: torch.Tensor         # [max_batch] int32: pages of each row
+    free: torch.Tensor         # [num_pages] int32, the first free_count of them
+    free_count: torch.Tensor   # [1] int32
+
+
+@dataclass
+class PagePlan:
+    """A step's tokens: what write, attend and the like take, and each token's place."""
+    seq_lens: torch.Tensor                    # [B] int32
+    q_start: torch.Tensor                     # [B + 1] int32
+    positions: Optional[torch.Tensor] = None  # [N] int32; 0 from q_start[B] on
+    slots: Optional[torch.Tensor] = None      # [N] int32: page * page_size + slot; -1
+    rows: Optional[torch.Tensor] = None       # [N] int32; -1
 
 
 class KVCache:
@@ -158,6 +178,108 @@ class KVCache:
             _stream_handle(stream, self._index))
         if st < 0:
             raise L.SgdError(st, "sgd_kv_attend")
+        return out
+
+    # -- prompts ----------------------------------------------------------------
+    def _new_tokens(self, q, k, v, out, scale):
+        """What attend_prompt and attend_chunk check alike: the C call's dtype, out and scale,
+        and q, k, v with their strides."""
+        dtype = _DTYPES.get(q.dtype)
+        if dtype is None or dtype == L.F32 or k.dtype is not q.dtype or v.dtype is not q.dtype:
+            raise ValueError("q, k and v must be of one type, float16 or bfloat16")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+        at = (self._new(q, self.q_heads, "q"), self._new(k, self.kv_heads, "k"), self._new(v, self.kv_heads, "v"))
+        if k.shape[0] != q.shape[0] or v.shape[0] != q.shape[0]:
+            raise ValueError("q, k and v must hold the same tokens")
+        qt, qh, _ = q.stride()
+        kt, kh, _ = k.stride()
+        vt, vh, _ = v.stride()
+        return (*at, dtype, qt, qh, kt, kh, vt, vh), out, scale if scale is not None else self.head_dim ** -0.5
+
+    def attend_prompt(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
+                      scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Causal attention over whole prompts: packed q [N, q_heads, head_dim], k and v [N,
+        kv_heads, head_dim] (float16 or bfloat16; slices of one projection's output are
+        taken as they are), row b's tokens q_start[b] .. q_start[b + 1].  With window > 0
+        a token sees the last `window` positions and the first `sinks`.  The cache is
+        not read."""
+        args, out, scale = self._new_tokens(q, k, v, out, scale)
+        t = self._t
+        st = self._lib.sgd_kv_attend_prompt(
+            self._h, *args, t(q_start, name="q_start"), q_start.shape[0] - 1, q.shape[0], scale, window, sinks,
+            t(out, q.dtype, "out"), _stream_handle(stream, self._index))
+        if st < 0:
+            raise L.SgdError(st, "sgd_kv_attend_prompt")
+        return out
+
+    def attend_chunk(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+                     seq_lens: torch.Tensor, q_start: torch.Tensor, scale: Optional[float] = None,
+                     window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None, layer: int = 0,
+                     stream=None) -> torch.Tensor:
+        """As attend_prompt, for rows some of whose tokens are already in the cache: row b's
+        new tokens are the last ones of its seq_lens[b], those before them are read from
+        the cache, and their own keys and values are taken from k and v (whether they
+        have been written makes no difference).  For rows of many new tokens what attend
+        is for rows of few."""
+        B = self._rows(block_table, seq_lens, q_start)
+        args, out, scale = self._new_tokens(q, k, v, out, scale)
+        t = self._t
+        st = self._lib.sgd_kv_attend_chunk(
+            self._h, self._layer_refs[layer], *args, t(block_table, name="block_table"),
+            t(seq_lens, name="seq_lens"), t(q_start, name="q_start"), B, q.shape[0], scale, window, sinks,
+            t(out, q.dtype, "out"), _stream_handle(stream, self._index))
+        if st < 0:
+            raise L.SgdError(st, "sgd_kv_attend_chunk")
+        return out
+
+    # -- pages ------------------------------------------------------------------
+    def new_pages(self) -> KVPages:
+        """The state of a cache none of whose pages is held."""
+        d, n = self.device, self.cfg.num_pages
+        i32 = dict(dtype=torch.int32, device=d)
+        return KVPages(torch.full((self.max_batch, self.max_pages), -1, **i32), torch.zeros(self.max_batch, **i32),
+                       torch.arange(n - 1, -1, -1, **i32), torch.full((1,), n, **i32))
+
+    def new_plan(self, B: int, total: int) -> PagePlan:
+        i32 = dict(dtype=torch.int32, device=self.device)
+        return PagePlan(torch.empty(B, **i32), torch.empty(B + 1, **i32),
+                        *(torch.empty(total, **i32) for _ in range(3)))
+
+    def assign(self, pages: KVPages, keep: torch.Tensor, new: torch.Tensor, total: Optional[int] = None,
+               out: Optional[PagePlan] = None, stream=None) -> PagePlan:
+        """Pages for a step in which row b keeps its first keep[b] tokens and gets new[b]
+        behind them: pages it no longer needs go back, those it lacks are handed out
+        (`pages` changes), and the packed tokens get their places.  keep after a
+        verification is what was accepted; keep = new = 0 ends a row.  `total`: the room
+        for packed tokens (`out` has its own).  Rows that the room or the free pages do
+        not suffice for get no new tokens, and get_error tells."""
+        B = keep.shape[0]
+        if out is None:
+            if total is None:
+                raise ValueError("assign needs out or total")
+            out = self.new_plan(B, total)
+        per_token = [x for x in (out.positions, out.slots, out.rows) if x is not None]
+        N = per_token[0].shape[0] if per_token else total
+        if N is None or any(x.shape != (N,) for x in per_token):
+            raise ValueError("positions, slots and rows must be [N], of one N (without any of them total gives it)")
+        if new.shape != (B,) or keep.shape != (B,) or out.seq_lens.shape != (B,) or out.q_start.shape != (B + 1,):
+            raise ValueError("keep, new and seq_lens must be [B], q_start [B + 1]")
+        if pages.block_table.shape != (self.max_batch, self.max_pages) or pages.held.shape != (self.max_batch,) \
+                or pages.free.shape != (self.cfg.num_pages,) or pages.free_count.numel() != 1:
+            raise ValueError("pages must be of this cache (new_pages)")
+        t = self._t
+        state = L.SgdKvPages(t(pages.block_table, name="block_table"), t(pages.held, name="held"),
+                             t(pages.free, name="free"), t(pages.free_count, name="free_count"))
+        st = self._lib.sgd_kv_assign(
+            self._h, ctypes.addressof(state), t(keep, name="keep"), t(new, name="new"), B, N,
+            t(out.seq_lens, name="seq_lens"), t(out.q_start, name="q_start"), t(out.positions, name="positions"),
+            t(out.slots, name="slots"), t(out.rows, name="rows"), _stream_handle(stream, self._index))
+        if st < 0:
+            raise L.SgdError(st, "sgd_kv_assign")
         return out
 
     # -- diagnostics ----------------------------------------------------------
