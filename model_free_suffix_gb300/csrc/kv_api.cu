@@ -222,11 +222,12 @@ static int attend_new(sgd_kv *x, KvNewArgs &a, const void *q, const void *k, con
   a.q_heads = x->cfg.q_heads;
   a.group = x->cfg.q_heads / x->cfg.kv_heads;
   a.scale = scale;
-  a.window = window;
-  a.sinks = sinks;
+  a.window = std::min(window, 1 << 30);  // (no position is beyond)
+  a.sinks = std::min(sinks, 1 << 30);
   a.sms = x->sms;
   a.work = x->d_work;
   a.err = x->d_err;
+  if ((int64_t)a.r.N * a.group > 1 << 30) return SGD_ETOOLARGE;
   const DeviceScope on(x->device);
   if (!on.ok()) return SGD_ECUDA;
   int launches = 0;

@@ -441,6 +441,19 @@ bool kv_make_map(CUtensorMap *map, const KvView &c, void *base, int tokens) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool kv_make_token_map(CUtensorMap *map, const void *base, int dim, int heads, int N, long long head_stride,
+                       long long token_stride, int tokens) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  // (of one head, or one token, the stride means nothing and may be anything)
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)N};
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads == 1 ? dim : head_stride) * 2, (cuuint64_t)(N == 1 ? dim : token_stride) * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)tokens}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 template <int D, int S>

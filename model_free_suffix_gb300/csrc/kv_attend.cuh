@@ -211,6 +211,11 @@ __device__ __forceinline__ void kv_join(const KvAttendArgs &a, const KvShare &sh
 // boxes of `tokens`, with the 128-byte swizzle.
 bool kv_make_map(CUtensorMap *map, const KvView &c, void *base, int tokens);
 
+// 16-bit tensors [N, heads, dim] of the caller, in boxes of `tokens` x 64 elements
+// of one head, with the 128-byte swizzle.  Strides in elements, multiples of 8.
+bool kv_make_token_map(CUtensorMap *map, const void *base, int dim, int heads, int N, long long head_stride,
+                       long long token_stride, int tokens);
+
 // Attention for units of more than 16 rows, up to KV_MANY_ROWS.
 constexpr int KV_MANY_ROWS = 32;
 cudaError_t attend_many_limits();

@@ -1,118 +1,1104 @@
-// kv_prompt.cu -- attention of whole prompts, and of chunks over the paged cache.
+// kv_prompt.cu -- attention of rows of many new tokens: whole prompts, and chunks
+// over the paged cache.
+//
+// A unit is up to 256 rows (new token, query head of the group) of one batch row
+// and one head of keys and values, in two tiles of 128.  Its work is a list of
+// 128-token tiles: those of the cache that its rows see, then those of the new
+// tokens.  Per tile and 128 rows the tensor cores form s = q k^T into tensor
+// memory (TMEM), a warpgroup turns s into p = 2^(z - m) with a running maximum
+// and sum, a row per thread, and writes p over s, and o += p v accumulates in
+// TMEM.  The two row tiles take turns: one's products run beside the other's
+// exponentials.
+//
+// One persistent CTA per SM, its warps in roles that run ahead of one another
+// through barriers:
+//   8 softmax warps   a warpgroup per row tile;
+//   4 loading warps   queries, then keys and values through a ring: the caller's
+//                     by TMA, the cache's converted from e4m3 in registers;
+//   1 thread          issues the products.
+// The tiles of all units, one after the other, are cut into equal shares, one
+// per CTA; a unit that a cut goes through leaves parts, which a second kernel
+// joins in their order (no atomics: the result does not depend on timing).
 #include <math_constants.h>
 
-#include "async_copy.cuh"
-#include "kv_internal.h"
+#include "kv_attend.cuh"
 #include "num_types.cuh"
 #include "sgd_internal.h"
+#include "tensor_core.cuh"
 
 namespace sgd {
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr int M = 128, ROWS = 2 * M, TILE = 128;
+constexpr int WARPS = 16, THREADS = 32 * WARPS;
+// (warps 0 to 7: softmax)
+constexpr int W_LOAD = 8, W_ISSUE = 12, W_JOIN = 13;
+constexpr int LOADERS = 4;
+// Registers a thread by role: together what 512 threads are launched with (128 each).
+constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
+static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHER <= THREADS * 128, "the pool of the launch");
+constexpr int OVERHEAD = 2;   // of a unit, in tiles
+constexpr int LEAST_PART = 2; // tiles of a part
+constexpr int LEAST_SHARE = 4;
+constexpr int META = 16;      // outlasts how far the loaders run ahead
+constexpr int BAD_SEGMENTS = 4, BAD_TILES = 8;
 
-// One warp per (new token, query head), a running maximum and sum: the plainest
-// form, one key at a time.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) new_kernel(KvNewArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < a.r.B; b += 128) {
-      const int q0 = __ldg(a.r.q_start + b), q1 = __ldg(a.r.q_start + b + 1);
-      if (q0 < 0 || q1 > a.r.N || q1 < q0) atomicOr(a.err, SGD_KV_ERR_LENGTH);
-    }
-  const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(unit / a.q_heads), hq = (int)(unit % a.q_heads), h = hq / a.group;
-  if (t >= a.r.N || t >= __ldg(a.r.q_start + a.r.B)) return;
-  int lo = 0, hi = a.r.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.r.q_start + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  const int b = lo, q0 = __ldg(a.r.q_start + b), q1 = __ldg(a.r.q_start + b + 1);
-  uint32_t bits = 0;
-  if (q0 < 0 || q1 > a.r.N || t < q0 || t >= q1) {
-    if (lane == 0) atomicOr(a.err, SGD_KV_ERR_LENGTH);
-    return;
-  }
-  const int ql = q1 - q0, n = a.r.seq_lens ? __ldg(a.r.seq_lens + b) : ql, old = n < ql ? -1 : n - ql, p = old + t - q0;
-  T *out = static_cast<T *>(a.out) + ((long long)t * a.q_heads + hq) * D + lane * E;
-  if (old < 0 || (a.r.seq_lens && n > (long long)a.r.max_pages * a.c.page)) {
-    for (int e = 0; e < E; ++e) out[e] = from_f32<T>(0.f);
-    if (lane == 0) atomicOr(a.err, SGD_KV_ERR_LENGTH);
-    return;
-  }
-  float q[E], o[E] = {}, m = -CUDART_INF_F, l = 0.f;
-  const T *qp = static_cast<const T *>(a.q) + t * a.q_token + hq * a.q_head + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = to_f32(qp[e]);
-  for (int j = 0; j <= p; ++j) {
-    if (a.window > 0 && j <= p - a.window && j >= a.sinks) continue;
-    float k[E], v[E];
-    if (j < old) {
-      const int pg = __ldg(a.r.table + (long long)b * a.r.max_pages + (j >> a.c.page_bits));
-      if (pg < 0 || pg >= a.c.num_pages) {
-        bits |= SGD_KV_ERR_PAGE;
-        continue;
-      }
-      const long long block = (long long)pg * a.c.heads + h;
-      const long long at = (block * a.c.page + (j & (a.c.page - 1))) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const uint32_t k2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(a.c.k + at + e));
-        const uint32_t v2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(a.c.v + at + e));
-        const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(&k2));
-        const float2 vf = __half22float2(*reinterpret_cast<const __half2 *>(&v2));
-        k[e] = kf.x * a.c.ks[block];
-        k[e + 1] = kf.y * a.c.ks[block];
-        v[e] = vf.x * a.c.vs[block];
-        v[e + 1] = vf.y * a.c.vs[block];
-      }
+template <int D>
+struct Plan {
+  static constexpr int HALF = TILE * D * 2;  // bytes of a tile of keys, or of values
+  static constexpr int Q = ROWS * D * 2;
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int SMEM = 1024 + Q + STAGES * HALF;
+  static constexpr int S = 0, O = 2 * TILE;  // TMEM columns: s of either row tile (p over it), then o
+  static constexpr int CHUNKS = D / 8;       // 16-byte chunks of a token
+};
+
+// What the loaders know of a tile and the softmax needs.
+struct Meta {
+  uint32_t gone;  // 16-token groups whose page is not there
+  float k, v;     // f16: the scales that the tile's keys and values were brought to
+};
+// Tokens of a tile whose values are not finite (see `spoil`).
+struct BadTile {
+  int x;                   // the tile's first token, from q0
+  uint32_t word[LOADERS];  // of warp w: bits of the tokens that it loaded
+};
+
+// ---- the work --------------------------------------------------------------------
+
+struct BatchRow {
+  int q0, ql, old;  // first packed token, new tokens, tokens before them
+  bool bad;         // its lengths make no sense: the result is 0
+};
+
+__device__ __forceinline__ BatchRow batch_row(const KvNewArgs &a, int b, uint32_t *bits) {
+  BatchRow r;
+  const int q0 = __ldg(a.r.q_start + b), q1 = __ldg(a.r.q_start + b + 1);
+  r.q0 = q0;
+  r.ql = q1 - q0;
+  r.old = 0;
+  r.bad = false;
+  if (q0 < 0 || q1 > a.r.N || q1 < q0) {
+    *bits |= SGD_KV_ERR_LENGTH;
+    r.ql = 0;
+  } else if (a.r.seq_lens) {
+    const int n = __ldg(a.r.seq_lens + b);
+    if (r.ql > 0 && (n < r.ql || (long long)n > ((long long)a.r.max_pages << a.c.page_bits))) {
+      *bits |= SGD_KV_ERR_LENGTH;
+      r.bad = true;
     } else {
-      const T *kp = static_cast<const T *>(a.k) + (q0 + j - old) * a.k_token + h * a.k_head + lane * E;
-      const T *vp = static_cast<const T *>(a.v) + (q0 + j - old) * a.v_token + h * a.v_head + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        k[e] = to_f32(kp[e]);
-        v[e] = to_f32(vp[e]);
-      }
+      r.old = n - r.ql;
     }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(FULL, s, x);
-    s *= a.scale * LOG2E;
-    const float top = fmaxf(m, s), base = top == -CUDART_INF_F ? 0.f : top;
-    const float keep = ex2_approx(m - base), w = ex2_approx(s - base);
-    m = top;
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * v[e];
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = from_f32<T>(o[e] / l);
-  if (bits && lane == 0) atomicOr(a.err, bits);
+  return r;
+}
+__device__ __forceinline__ int blocks_of(const KvNewArgs &a, const BatchRow &r) {
+  return (r.ql * a.group + ROWS - 1) / ROWS;
 }
 
+struct Unit {
+  int r0, nrows;               // its rows among the batch row's ql * group
+  int p_first, p_last;         // positions of the first and the last row's token
+  int c_sink, c_lo, c_tiles;   // of the cache: tiles of first tokens, then from c_lo on
+  int f_sink, f_lo, tiles;     // of the new tokens likewise; all tiles
+};
+
+__device__ __forceinline__ Unit unit_of(const KvNewArgs &a, const BatchRow &r, int i) {
+  Unit u;
+  u.r0 = i * ROWS;
+  u.nrows = min(ROWS, r.ql * a.group - u.r0);
+  const int t_last = (u.r0 + u.nrows - 1) / a.group;
+  u.p_first = r.old + u.r0 / a.group;
+  u.p_last = r.old + t_last;
+  u.c_sink = u.c_lo = u.c_tiles = u.f_sink = u.f_lo = u.tiles = 0;
+  if (r.bad) return u;
+  const int lo = a.window > 0 ? max(0, u.p_first - a.window + 1) : 0;
+  const int c_end = (r.old + TILE - 1) / TILE, f_end = t_last / TILE + 1;
+  if (lo > 0) {
+    u.c_lo = lo >= r.old ? c_end : lo / TILE;
+    u.c_sink = min((min(a.sinks, r.old) + TILE - 1) / TILE, u.c_lo);
+    u.f_lo = max(0, lo - r.old) / TILE;
+    u.f_sink = min((max(0, a.sinks - r.old) + TILE - 1) / TILE, u.f_lo);
+  }
+  u.c_tiles = u.c_sink + c_end - u.c_lo;
+  u.tiles = u.c_tiles + u.f_sink + f_end - u.f_lo;
+  return u;
+}
+
+// Where a share begins or ends: before tile t of unit u, or past it.
+struct Cut {
+  long long u;
+  int b, i, h, t;
+  bool past;
+};
+struct Share {
+  Cut begin, end;
+  long long all;   // weight of all units
+  long long u_at;  // weight before the unit of `end`
+  int end_tiles;   // its tiles
+  int ctas;
+};
+
+__device__ __forceinline__ long long block_scan(long long x, long long *s, long long *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long scan = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(FULL, scan, o);
+    if (lane >= o) scan += t;
+  }
+  __syncthreads();
+  if (lane == 31) s[warp] = scan;
+  __syncthreads();
+  long long before = scan - x, all = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += s[w];
+    all += s[w];
+  }
+  *total = all;
+  return before;
+}
+
+// A cut at `into` of a unit's weight, moved to the unit's ends where a part would
+// be too small to be worth its join.
+__device__ __forceinline__ void place_cut(Cut &c, long long into, int tiles) {
+  const long long t = into - OVERHEAD;
+  c.t = t < LEAST_PART ? 0 : (int)t;
+  c.past = t >= LEAST_PART && tiles - t < LEAST_PART;
+  if (c.past) c.t = 0;
+}
+
+// By all threads of the block.  first: [B + 1] ints of shared memory.
+__device__ const Share &share_of(const KvNewArgs &a, int *first, uint32_t *bits) {
+  __shared__ long long s_sum[WARPS];
+  __shared__ Share s;
+  const int tid = threadIdx.x, B = a.r.B;
+  const int per = (B + THREADS - 1) / THREADS, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  long long mine = 0, total;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += blocks_of(a, batch_row(a, b, bits));
+  long long at = block_scan(mine, s_sum, &total);
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    first[b] = (int)at;
+    at += blocks_of(a, batch_row(a, b, bits));
+  }
+  if (tid == 0) {
+    first[B] = (int)total;
+    s.ctas = 0;
+  }
+  __syncthreads();
+  const long long blocks = total;
+  const int c0 = (int)(blocks * tid / THREADS), c1 = (int)(blocks * (tid + 1) / THREADS);
+  int b_from = 0;
+  mine = 0;
+  if (c0 < c1) {
+    int hi = B;
+    while (hi - b_from > 1) {
+      const int mid = (b_from + hi) >> 1;
+      if (first[mid] <= c0) b_from = mid;
+      else hi = mid;
+    }
+    int b = b_from;
+    BatchRow r = batch_row(a, b, bits);
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+      while (c >= first[b + 1]) r = batch_row(a, ++b, bits);
+      mine += OVERHEAD + unit_of(a, r, c - first[b]).tiles;
+    }
+  }
+  const long long before = block_scan(mine, s_sum, &total);
+  const long long all = total * a.c.heads;
+  const long long most = (all + LEAST_SHARE - 1) / LEAST_SHARE;
+  const int ctas = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x), g = blockIdx.x;
+  if (g < ctas) {
+    if (tid == 0) {
+      s.ctas = ctas;
+      s.all = all;
+      s.end.u = a.c.heads * blocks;  // (where it is the end of all)
+      s.end.t = 0;
+      s.end.past = false;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const long long pos = all * (g + k) / ctas;
+      const int h = (int)(pos / total);
+      const long long in = pos - h * total;
+      if (h < a.c.heads && c0 < c1 && before <= in && in < before + mine) {
+        int b = b_from, c = c0;
+        long long w = before;
+        BatchRow r = batch_row(a, b, bits);
+        Unit u;
+        for (;; ++c) {
+          while (c >= first[b + 1]) r = batch_row(a, ++b, bits);
+          u = unit_of(a, r, c - first[b]);
+          if (in < w + OVERHEAD + u.tiles) break;
+          w += OVERHEAD + u.tiles;
+        }
+        Cut &cut = k ? s.end : s.begin;
+        cut.u = h * blocks + c;
+        cut.b = b;
+        cut.i = c - first[b];
+        cut.h = h;
+        place_cut(cut, in - w, u.tiles);
+        if (k) {
+          s.u_at = h * total + w;
+          s.end_tiles = u.tiles;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  return s;
+}
+
+// A share's segments: the units that it holds or cuts, each with its range of tiles.
+struct Walk {
+  const KvNewArgs &a;
+  const Share &s;
+  BatchRow row;
+  Unit unit;
+  long long u;
+  int b, i, h, blocks;
+  int t0, t1;
+  bool begun = false;
+
+  __device__ Walk(const KvNewArgs &a_, const Share &s_) : a(a_), s(s_), u(s_.begin.u), b(s_.begin.b), i(s_.begin.i), h(s_.begin.h) {}
+
+  __device__ __forceinline__ bool done() const { return u > s.end.u || (u == s.end.u && s.end.t == 0 && !s.end.past); }
+  __device__ __forceinline__ bool next(uint32_t *bits) {
+    t0 = 0;
+    if (!begun) {
+      begun = true;
+      row = batch_row(a, b, bits);
+      blocks = blocks_of(a, row);
+      if (!s.begin.past) {
+        if (done()) return false;
+        t0 = s.begin.t;
+        return shape();
+      }
+    }
+    ++u;
+    if (done()) return false;
+    if (++i == blocks) {
+      i = 0;
+      do {
+        if (++b == a.r.B) {
+          b = 0;
+          ++h;
+        }
+        row = batch_row(a, b, bits);
+        blocks = blocks_of(a, row);
+      } while (blocks == 0);
+    }
+    return shape();
+  }
+  __device__ __forceinline__ bool shape() {
+    unit = unit_of(a, row, i);
+    t1 = u == s.end.u && !s.end.past ? s.end.t : unit.tiles;
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == unit.tiles; }
+  __device__ __forceinline__ bool cached(int j) const { return j < unit.c_tiles; }
+  // first position of tile j
+  __device__ __forceinline__ int at(int j) const {
+    if (j < unit.c_tiles) return (j < unit.c_sink ? j : unit.c_lo + j - unit.c_sink) * TILE;
+    j -= unit.c_tiles;
+    return row.old + (j < unit.f_sink ? j : unit.f_lo + j - unit.f_sink) * TILE;
+  }
+  // whether some row does not see some token of the tile at x
+  __device__ __forceinline__ bool edge(int j, int x) const {
+    return x + TILE - 1 > (cached(j) ? row.old - 1 : unit.p_first) ||
+           (a.window > 0 && x <= unit.p_last - a.window && x + TILE > a.sinks);
+  }
+  __device__ __forceinline__ int token(int r) const { return row.q0 + (unit.r0 + r) / a.group; }
+  __device__ __forceinline__ int q_head(int r) const { return h * a.group + (unit.r0 + r) % a.group; }
+};
+
+// Parts: [D / 4][ROWS] sums (four dims each), [ROWS] maxima, [ROWS] sums of p; two
+// for each CTA, of the unit that its share begins within (0) and ends within (1).
+struct Join {
+  int parts, q0, r0, nrows, h;
+};
+__device__ __forceinline__ Join *join_of(const KvNewArgs &a, int g) {
+  return reinterpret_cast<Join *>(a.work + MAX_CTAS * 8) + g;
+}
+template <int D>
+__device__ __forceinline__ float *new_part(const KvNewArgs &a, int slot) {
+  return reinterpret_cast<float *>(a.work + MAX_CTAS * 8 + MAX_CTAS * 32) + (long long)slot * (ROWS * (D + 2));
+}
+
+// ---- pieces of the roles ---------------------------------------------------------
+
+__device__ __forceinline__ void st_shared16(uint32_t to, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A 16-byte chunk (c-th of its token or row) of line `line` of an operand.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int line, int c) {
+  return base + (c >> 3) * (TILE * 128) + line * 128 + (((c & 7) ^ (line & 7)) << 4);
+}
+
+// Two e4m3 bytes, each in the high byte of a half, as two T of 2^-120 (bf16) or 2^-8
+// (f16) times their value: sign, exponent and fraction keep their order, so moving
+// the bits is exact, for subnormals too; `f` brings the values to their size (a power
+// of two: exact).
 template <typename T>
-cudaError_t launch(const KvNewArgs &a, cudaStream_t st) {
-  const unsigned blocks = (unsigned)(((long long)a.r.N * a.q_heads + 3) / 4);
-  if (a.c.dim == 128) new_kernel<T, 128><<<blocks, 128, 0, st>>>(a);
-  else new_kernel<T, 64><<<blocks, 128, 0, st>>>(a);
+__device__ __forceinline__ uint32_t widen(uint32_t pair, uint32_t f);
+template <>
+__device__ __forceinline__ uint32_t widen<__nv_bfloat16>(uint32_t pair, uint32_t f) {
+  const uint32_t w = (pair & 0x80008000u) | ((pair >> 4) & 0x07f007f0u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(f));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t widen<__half>(uint32_t pair, uint32_t f) {
+  const uint32_t w = (pair & 0x80008000u) | ((pair >> 1) & 0x3f803f80u);
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(f));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t twice(float x) {
+  return pack2<T>(x, x);
+}
+
+// 2^60, twice: a scale of up to 2^48 times 2^120 is beyond bf16.
+constexpr float BF16_STEP = 1.152921504606847e18f;
+
+template <typename T>
+struct Is;
+template <>
+struct Is<__nv_bfloat16> {
+  static constexpr bool bf16 = true;
+};
+template <>
+struct Is<__half> {
+  static constexpr bool bf16 = false;
+};
+
+// Whether a chunk of 16-bit values holds one that is not finite.
+template <typename T>
+__device__ __forceinline__ bool not_finite(uint4 v) {
+  constexpr uint32_t E = Is<T>::bf16 ? 0x7f807f80u : 0x7c007c00u, LOW = Is<T>::bf16 ? 0x00800080u : 0x04000400u;
+  // (all ones in an exponent: adding its lowest bit carries into the sign's place)
+  const uint32_t x = ((v.x & E) + LOW) | ((v.y & E) + LOW) | ((v.z & E) + LOW) | ((v.w & E) + LOW);
+  return (x & 0x80008000u) != 0;
+}
+// The word with 0 in place of such values.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_word(uint32_t w) {
+  constexpr uint32_t E = Is<T>::bf16 ? 0x7f80u : 0x7c00u;
+  if ((w & E) == E) w &= 0xffff0000u;
+  if ((w >> 16 & E) == E) w &= 0xffffu;
+  return w;
+}
+
+__device__ __forceinline__ uint4 load16(const unsigned short *p, bool vec) {
+  if (vec) return __ldg(reinterpret_cast<const uint4 *>(p));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A tile of the caller's keys or values by the loading warps themselves: `tokens` of
+// them, 0 behind.  CHECK: values that are not finite are taken out; returns
+// the bits of this warp's tokens that had some.
+template <typename T, int D, bool CHECK>
+__device__ __forceinline__ uint32_t copy_tile(uint32_t to, const void *base, long long stride, bool vec, int tokens, int tid) {
+  constexpr int C = Plan<D>::CHUNKS, PER = TILE * C / (32 * LOADERS), STEP = 32 * LOADERS / C, IN_WARP = 32 / C;
+  const int c = tid % C, line0 = tid / C;
+  const unsigned short *p = static_cast<const unsigned short *>(base) + line0 * stride + c * 8;
+  uint32_t bad = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < PER; i0 += 8) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (line0 + (i0 + i) * STEP < tokens) v[i] = load16(p + (long long)(i0 + i) * STEP * stride, vec);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (CHECK) {
+        const uint32_t votes = __ballot_sync(FULL, not_finite<T>(v[i]));
+        if (votes) {
+          v[i] = make_uint4(finite_word<T>(v[i].x), finite_word<T>(v[i].y), finite_word<T>(v[i].z), finite_word<T>(v[i].w));
+#pragma unroll
+          for (int k = 0; k < IN_WARP; ++k)
+            if (votes >> (k * C) & ((1u << C) - 1)) bad |= 1u << ((i0 + i) * IN_WARP + k);
+        }
+      }
+      st_shared16(chunk_at(to, line0 + (i0 + i) * STEP, c), v[i].x, v[i].y, v[i].z, v[i].w);
+    }
+  }
+  return bad;
+}
+
+// The queries of a unit's rows.
+template <typename T, int D>
+__device__ __forceinline__ void copy_queries(const KvNewArgs &a, const Walk &w, uint32_t to, int tid) {
+  constexpr int C = Plan<D>::CHUNKS, STEP = 32 * LOADERS / C;
+  const int c = tid % C;
+  const unsigned short *q = static_cast<const unsigned short *>(a.q) + c * 8;
+  if (a.q_vec && a.scale >= 0.f) {
+#pragma unroll 4
+    for (int r = tid / C; r < w.unit.nrows; r += STEP) {
+      const unsigned short *from = q + w.token(r) * a.q_token + w.q_head(r) * a.q_head;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(chunk_at(to + (r >> 7) * (M * D * 2), r & 127, c)), "l"(from)
+                   : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0;  // (the scale is taken without its sign)
+#pragma unroll 1
+    for (int r = tid / C; r < w.unit.nrows; r += STEP) {
+      const uint4 v = load16(q + w.token(r) * a.q_token + w.q_head(r) * a.q_head, a.q_vec);
+      st_shared16(chunk_at(to + (r >> 7) * (M * D * 2), r & 127, c), v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
+    }
+  }
+}
+
+// Values that are not finite meet p = 0 in rows that do not see their tokens, and 0
+// times them is NaN; so tiles that some row does not see in full hold 0 in their
+// place, and what they do to the rows that see them is done afterwards, here: a row's
+// result plus the value (an infinity, or NaN).  Rare, and out of the way.
+template <typename T, int D>
+__device__ __noinline__ void spoil(const KvNewArgs &a, const BadTile *bad, int n, int q0, int old, int h, int p, T *out,
+                                   float *part) {
+  constexpr int C = Plan<D>::CHUNKS, STEP = 32 * LOADERS / C, IN_WARP = 32 / C;
+  for (int k = 0; k < n; ++k)
+    for (int w = 0; w < LOADERS; ++w)
+      for (uint32_t m = bad[k].word[w]; m; m &= m - 1) {
+        const int bit = __ffs(m) - 1, t = bad[k].x + bit / IN_WARP * STEP + w * IN_WARP + bit % IN_WARP, j = old + t;
+        if (j > p || (a.window > 0 && j <= p - a.window && j >= a.sinks)) continue;
+        const T *v = static_cast<const T *>(a.v) + (long long)(q0 + t) * a.v_token + h * a.v_head;
+        for (int d = 0; d < D; ++d) {
+          const float x = to_f32(v[d]);
+          if (fabsf(x) < CUDART_INF_F) continue;
+          if (out) out[d] = from_f32<T>(to_f32(out[d]) + x);
+          else part[(d >> 2) * (ROWS * 4) + (d & 3)] += x;
+        }
+      }
+}
+
+enum Bar { FULL_AT = 0, EMPTY_AT = 8, Q_FULL = 16, Q_EMPTY, S_FULL, P_FULL = S_FULL + 2, PV_DONE = P_FULL + 2, O_EMPTY = PV_DONE + 2, BARS = O_EMPTY + 2 };
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+__device__ __forceinline__ uint64_t pair64(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    new_kernel(const __grid_constant__ KvNewArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using L = Plan<D>;
+  constexpr bool BF16 = Is<T>::bf16;
+  constexpr int STAGES = L::STAGES;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  __shared__ __align__(8) unsigned long long bars[BARS];
+  __shared__ Meta meta[META];
+  __shared__ BadTile bad_tiles[BAD_SEGMENTS][BAD_TILES];
+  __shared__ int bad_count[BAD_SEGMENTS];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t bits = 0;
+  const Share &share = share_of(a, reinterpret_cast<int *>(smem), &bits);
+  if (share.ctas == 0) {
+    if (tid == 0) join_of(a, blockIdx.x)->parts = 0;
+    if (bits) atomicOr(a.err, bits);
+    return;
+  }
+  const uint32_t q_at = smem_addr(smem), ring = q_at + L::Q;
+  auto bar = [&](int which) { return smem_addr(bars + which); };
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      bar_init(bar(FULL_AT + i), LOADERS);
+      bar_init(bar(EMPTY_AT + i), 1);
+    }
+    bar_init(bar(Q_FULL), LOADERS);
+    bar_init(bar(Q_EMPTY), 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(S_FULL + i), 1);
+      bar_init(bar(P_FULL + i), 4);
+      bar_init(bar(PV_DONE + i), 1);
+      bar_init(bar(O_EMPTY + i), 4);
+    }
+    bar_init_fence();
+    s_abort = 0;
+  }
+  if (warp == W_ISSUE) tmem_alloc(smem_addr(&tmem_slot), 512);
+  tmem_before_sync();
+  __syncthreads();
+  tmem_after_sync();
+  const uint32_t tmem = tmem_slot;
+  // A wait that runs out, in any role, ends the others' as well; each role then
+  // leaves its loops.
+  auto wait = [&](int which, uint32_t parity) {
+    const uint32_t b = bar(which);
+    if (bar_try(b, parity & 1)) return true;
+#pragma unroll 1
+    for (int i = 0; i < (1 << 20); ++i) {
+      if (bar_try(b, parity & 1)) return true;
+      if ((i & 15) == 15 && *reinterpret_cast<volatile int *>(&s_abort)) return false;
+    }
+    *reinterpret_cast<volatile int *>(&s_abort) = 1;
+    bits |= SGD_KV_ERR_WAIT;
+    return false;
+  };
+  auto warp_arrive = [&](int which) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar(which));
+  };
+
+  if (warp >= W_LOAD && warp < W_LOAD + LOADERS) {
+    fewer_registers<REGS_OTHER>();
+    const int me = tid - 32 * W_LOAD, wl = warp - W_LOAD;
+    constexpr int CHUNKS8 = D / 16, PER = TILE * CHUNKS8 / (32 * LOADERS);  // 16-byte chunks of e4m3: of a token, of a thread
+    constexpr int STEP = 32 * LOADERS / CHUNKS8;
+    const int c8 = me % CHUNKS8, line0 = me / CHUNKS8;
+    const int per_tile = TILE >> a.c.page_bits;
+    Walk w(a, share);
+    uint32_t item = 0, segments = 0, g = 0;
+    bool ok = true;
+    auto slot_free = [&]() {
+      if (item >= STAGES) ok = ok && wait(EMPTY_AT + item % STAGES, item / STAGES - 1);
+      ok = __all_sync(FULL, ok);
+      return ok;
+    };
+    // the cached tile in hand: of page `lane` of it, the block and what its keys and values are multiplied by
+    int block = -1;
+    float k_scale = 0.f, v_scale = 0.f;
+    Meta mt{0u, 1.f, 1.f};
+    auto pages = [&](int j) {
+      const int x = w.at(j), index = (x >> a.c.page_bits) + lane;
+      const bool in = lane < per_tile && index << a.c.page_bits < w.row.old;
+      block = -1;
+      k_scale = v_scale = 0.f;
+      if (in) {
+        const int pg = __ldg(a.r.table + (long long)w.b * a.r.max_pages + index);
+        if (pg >= 0 && pg < a.c.num_pages) {
+          block = pg * a.c.heads + w.h;
+          k_scale = __ldg(a.c.ks + block);
+          v_scale = __ldg(a.c.vs + block);
+        } else {
+          bits |= SGD_KV_ERR_PAGE;
+        }
+      }
+      const uint32_t lost = __ballot_sync(FULL, in && block < 0);
+      mt.gone = 0;
+      for (int i = 0; i < per_tile; ++i)
+        if (lost >> i & 1) mt.gone |= ((1u << ((1 << a.c.page_bits) / 16)) - 1) << (i << (a.c.page_bits - 4));
+      mt.k = mt.v = 1.f;
+      if (!BF16) {
+        // f16 has not the range of the scales: keys and values are brought to the largest
+        // scale of the tile (those of much smaller ones lose bits below 2^-24 of it)
+        float km = k_scale, vm = v_scale;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) {
+          km = fmaxf(km, __shfl_xor_sync(FULL, km, o));
+          vm = fmaxf(vm, __shfl_xor_sync(FULL, vm, o));
+        }
+        km = __shfl_sync(FULL, km, 0);
+        vm = __shfl_sync(FULL, vm, 0);
+        mt.k = km > 0.f ? km : 1.f;
+        mt.v = vm > 0.f ? vm : 1.f;
+        k_scale *= 256.f / mt.k;
+        v_scale *= 256.f / mt.v;
+      }
+    };
+    auto load8 = [&](const uint8_t *base, uint4 (&v)[PER]) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int t = line0 + i * STEP, blk = __shfl_sync(FULL, block, t >> a.c.page_bits);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (blk >= 0)
+          v[i] = __ldg(reinterpret_cast<const uint4 *>(base + ((long long)blk * a.c.page + (t & (a.c.page - 1))) * D) + c8);
+      }
+    };
+    auto store8 = [&](uint32_t to, const uint4 (&v)[PER], float scale) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int t = line0 + i * STEP;
+        const float s = __shfl_sync(FULL, scale, t >> a.c.page_bits);
+        const uint32_t f = BF16 ? twice<T>(s * BF16_STEP) : twice<T>(s), f2 = twice<T>(BF16_STEP);
+        const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[2 * e] = widen<T>(__byte_perm(in[e], 0, 0x1404), f);
+          h[2 * e + 1] = widen<T>(__byte_perm(in[e], 0, 0x3424), f);
+        }
+        if (BF16) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f2));
+        }
+        // (lanes of a token's second half write their chunks in the other order: no bank twice)
+        const int swap = D == 128 ? c8 >> 2 & 1 : 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool high = (e ^ swap) != 0;
+          st_shared16(chunk_at(to, t, 2 * c8 + (e ^ swap)), high ? h[4] : h[0], high ? h[5] : h[1], high ? h[6] : h[2],
+                      high ? h[7] : h[3]);
+        }
+      }
+    };
+    // hands the slot in hand to the products
+    auto done = [&]() {
+      async_fence();
+      warp_arrive(FULL_AT + item % STAGES);
+      ++item;
+    };
+    auto by_tma = [&](const CUtensorMap *map, int token) {
+      if (wl == 0 && lane == 0) {
+        const uint32_t to = ring + item % STAGES * L::HALF, b = bar(FULL_AT + item % STAGES);
+        bar_expect(b, L::HALF);
+#pragma unroll
+        for (int d = 0; d < D; d += 64) tma_load_3d(to + d * (TILE * 2), map, d, w.h, token, b);
+      } else if (lane == 0) {
+        bar_arrive(bar(FULL_AT + item % STAGES));
+      }
+      __syncwarp();
+      ++item;
+    };
+    while (ok && w.next(&bits)) {
+      if (w.t0 == w.t1) continue;
+      uint4 kr[PER], vr[PER];
+      if (w.cached(w.t0)) {
+        pages(w.t0);
+        load8(a.c.k, kr);
+      }
+      int bads = 0;
+      for (int j = w.t0; j < w.t1; ++j) {
+        const int x = w.at(j);
+        const bool cached = w.cached(j);
+        const int from = x - w.row.old, tokens = w.row.ql - from;  // (of a tile of new ones: its first, and how many there are)
+        if (wl == 0 && lane == 0) {
+          if (j == w.t0) bad_count[segments % BAD_SEGMENTS] = 0;
+          const Meta none{0u, 1.f, 1.f};
+          meta[g % META] = cached ? mt : none;
+        }
+        ++g;
+        if (!slot_free()) break;
+        if (cached) {
+          load8(a.c.v, vr);
+          store8(ring + item % STAGES * L::HALF, kr, k_scale);
+          done();
+        } else if (a.k_vec) {
+          by_tma(&kmap, w.row.q0 + from);
+        } else {
+          copy_tile<T, D, false>(ring + item % STAGES * L::HALF,
+                                 static_cast<const T *>(a.k) + (w.row.q0 + from) * a.k_token + w.h * a.k_head, a.k_token,
+                                 false, tokens, me);
+          done();
+        }
+        if (j == w.t0) {
+          if (segments > 0) ok = wait(Q_EMPTY, segments - 1);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          copy_queries<T, D>(a, w, q_at, me);
+          async_fence();
+          warp_arrive(Q_FULL);
+        }
+        if (!slot_free()) break;
+        if (cached) {
+          const float vs = v_scale;
+          if (j + 1 < w.t1 && w.cached(j + 1)) {
+            pages(j + 1);
+            load8(a.c.k, kr);
+          }
+          store8(ring + item % STAGES * L::HALF, vr, vs);
+          done();
+        } else if (a.v_vec && !w.edge(j, x)) {
+          by_tma(&vmap, w.row.q0 + from);
+        } else {
+          const uint32_t bad = copy_tile<T, D, true>(
+              ring + item % STAGES * L::HALF, static_cast<const T *>(a.v) + (w.row.q0 + from) * a.v_token + w.h * a.v_head,
+              a.v_token, a.v_vec, tokens, me);
+          BadTile *e = nullptr;
+          // (at most 7 tiles of a unit have an edge: 3 where its rows' tokens are, 3 where
+          // their windows begin, 1 where the first tokens end)
+          if (w.edge(j, x) && bads < BAD_TILES) {
+            e = &bad_tiles[segments % BAD_SEGMENTS][bads++];
+            if (lane == 0) e->word[wl] = bad;
+            if (wl == 0 && lane == 0) {
+              e->x = from;
+              bad_count[segments % BAD_SEGMENTS] = bads;
+            }
+          }
+          done();
+        }
+      }
+      ++segments;
+    }
+    if (!ok) {  // (copies in flight land before the CTA ends, or a bound runs out)
+      for (int i = 0; i < STAGES; ++i)
+        for (int n = 0; n < (1 << 16) && !bar_try(bar(FULL_AT + i), 0) && !bar_try(bar(FULL_AT + i), 1); ++n) {
+        }
+    }
+  } else if (warp >= W_ISSUE) {
+    fewer_registers<REGS_OTHER>();
+    if (warp == W_ISSUE && lane == 0) {
+      constexpr uint32_t QK = product16(BF16, TILE, false), PV = product16(BF16, D, true);
+      Walk w(a, share);
+      uint32_t item = 0, segments = 0, done0 = 0, done1 = 0, segs1 = 0;
+      bool ok = true;
+      auto qk = [&](int i, uint32_t slot) {
+        const uint32_t q = q_at + i * (M * D * 2), k = ring + slot * L::HALF;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = (e / 4) * (TILE * 128) + (e % 4) * 32;
+          mma_ss(tmem + L::S + i * TILE, smem_operand(q + off, 1024, 16), smem_operand(k + off, 1024, 16), QK, e > 0);
+        }
+      };
+      auto pv = [&](int i, uint32_t slot, bool add) {
+        const uint32_t v = ring + slot * L::HALF;
+#pragma unroll
+        for (int e = 0; e < TILE / 16; ++e)
+          mma_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + e * 8, smem_operand(v + e * 2048, 1024, TILE * 128), PV, add || e > 0);
+      };
+      while (ok && w.next(&bits)) {
+        const int n = w.t1 - w.t0;
+        if (n == 0) continue;
+        const bool two = w.unit.nrows > M;
+        ok = wait(FULL_AT + item % STAGES, item / STAGES) && wait(Q_FULL, segments);
+        if (!ok) break;
+        tmem_after_sync();
+        qk(0, item % STAGES);
+        mma_commit(bar(S_FULL));
+        if (two) {
+          qk(1, item % STAGES);
+          mma_commit(bar(S_FULL + 1));
+        }
+        mma_commit(bar(EMPTY_AT + item % STAGES));
+        if (n == 1) mma_commit(bar(Q_EMPTY));
+        for (int j = 0; j < n; ++j) {
+          const uint32_t vi = item + 1, ki = item + 2;
+          const bool more = j + 1 < n;
+          ok = wait(FULL_AT + vi % STAGES, vi / STAGES) && wait(P_FULL, done0);
+          if (ok && j == 0 && segments > 0) ok = wait(O_EMPTY, segments - 1);
+          if (!ok) break;
+          tmem_after_sync();
+          pv(0, vi % STAGES, j > 0);
+          mma_commit(bar(PV_DONE));
+          ++done0;
+          if (!two) mma_commit(bar(EMPTY_AT + vi % STAGES));
+          if (more) {
+            ok = wait(FULL_AT + ki % STAGES, ki / STAGES);
+            if (!ok) break;
+            tmem_after_sync();
+            qk(0, ki % STAGES);
+            mma_commit(bar(S_FULL));
+            if (!two) mma_commit(bar(EMPTY_AT + ki % STAGES));
+          }
+          if (two) {
+            ok = wait(P_FULL + 1, done1);
+            if (ok && j == 0 && segs1 > 0) ok = wait(O_EMPTY + 1, segs1 - 1);
+            if (!ok) break;
+            tmem_after_sync();
+            pv(1, vi % STAGES, j > 0);
+            mma_commit(bar(PV_DONE + 1));
+            ++done1;
+            mma_commit(bar(EMPTY_AT + vi % STAGES));
+            if (more) {
+              qk(1, ki % STAGES);
+              mma_commit(bar(S_FULL + 1));
+              mma_commit(bar(EMPTY_AT + ki % STAGES));
+            }
+          }
+          if (j + 2 == n) mma_commit(bar(Q_EMPTY));
+          item += 2;
+        }
+        ++segments;
+        if (two) ++segs1;
+      }
+    } else if (warp == W_JOIN && lane == 0) {
+      // the unit that this share ends within, if it begins here: how many shares hold it
+      Join join{0, 0, 0, 0, 0};
+      if (share.end.t > 0 && (share.end.u > share.begin.u || (share.begin.t == 0 && !share.begin.past))) {
+        const BatchRow r = batch_row(a, share.end.b, &bits);
+        const Unit u = unit_of(a, r, share.end.i);
+        join.parts = 2;
+        for (int g = blockIdx.x + 2; g < share.ctas; ++g) {
+          const long long into = share.all * g / share.ctas - share.u_at;
+          if (into >= OVERHEAD + share.end_tiles) break;
+          Cut c;
+          place_cut(c, into, share.end_tiles);
+          if (c.past) break;
+          ++join.parts;
+        }
+        join.q0 = r.q0;
+        join.r0 = u.r0;
+        join.nrows = u.nrows;
+        join.h = share.end.h;
+      }
+      *join_of(a, blockIdx.x) = join;
+    }
+    __syncwarp();
+  } else {
+    more_registers<REGS_SOFTMAX>();
+    const int i = warp >> 2, r = tid & 127, R = i * M + r;  // the warpgroup's row tile, the thread's row of it, of the unit
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t s_at = tmem + lanes + L::S + i * TILE, o_at = tmem + lanes + L::O + i * D;
+    const float c0 = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);
+    constexpr float THRESHOLD = BF16 ? 8.f : LAZY, UP = BF16 ? 0.f : LIFT;
+    Walk w(a, share);
+    uint32_t g = 0, mine = 0, segments = 0;
+    bool ok = true;
+    while (ok && w.next(&bits)) {
+      const int tiles = w.t1 - w.t0;
+      const bool on = w.unit.nrows > i * M;
+      const int t = (w.unit.r0 + R) / a.group, p = w.row.old + t;
+      T *out = static_cast<T *>(a.out) + ((long long)(w.row.q0 + t) * a.q_heads + w.h * a.group + (w.unit.r0 + R) % a.group) * D;
+      if (tiles == 0) {
+        if (R < w.unit.nrows)
+          for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(out + d) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      if (!on) {
+        g += tiles;
+        ++segments;
+        continue;
+      }
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int j = w.t0; j < w.t1; ++j, ++g, ++mine) {
+        ok = wait(S_FULL + i, mine);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        tmem_after_sync();
+        float s[TILE];
+#pragma unroll
+        for (int e = 0; e < TILE; e += 32) tmem_ld32(s_at + e, reinterpret_cast<uint32_t *>(s) + e);
+        const Meta mt = meta[g % META];
+        const int x = w.at(j);
+        tmem_wait_ld();
+        if (w.edge(j, x) || mt.gone) {
+          const int lim = min(p, w.cached(j) ? w.row.old - 1 : p) - x;  // the row sees slots up to lim
+          const int from = a.window > 0 ? p - a.window + 1 - x : 0, sink = a.sinks - x;
+#pragma unroll
+          for (int e = 0; e < TILE; ++e)
+            if (e > lim || (e < from && e >= sink) || (mt.gone >> (e / 16) & 1)) s[e] = -CUDART_INF_F;
+        }
+        float top0 = s[0], top1 = s[1], top2 = s[2], top3 = s[3];
+#pragma unroll
+        for (int e = 4; e < TILE; e += 4) {
+          top0 = fmaxf(top0, s[e]);
+          top1 = fmaxf(top1, s[e + 1]);
+          top2 = fmaxf(top2, s[e + 2]);
+          top3 = fmaxf(top3, s[e + 3]);
+        }
+        // m: the running maximum of z + log2 V, V the scale that the tile's values were brought to
+        const float c = BF16 ? c0 : fmaxf(c0 * mt.k, 1e-37f), lv = BF16 ? 0.f : __log2f(mt.v);
+        const float top = fmaf(fmaxf(fmaxf(top0, top1), fmaxf(top2, top3)), c, lv);
+        float o_scale = 1.f;
+        if (top > m + THRESHOLD || (m == -CUDART_INF_F && top > m)) {
+          o_scale = m == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
+          l *= o_scale;
+          m = top;
+        }
+        if (j > w.t0 && __any_sync(FULL, o_scale != 1.f)) {
+          ok = wait(PV_DONE + i, mine - 1);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          tmem_after_sync();
+#pragma unroll
+          for (int d = 0; d < D; d += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_at + d, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * o_scale);
+            tmem_st16(o_at + d, o);
+          }
+        }
+        const float base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
+        const uint64_t c2 = pair64(c, c), b2 = pair64(-base, -base);
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const int at = half * 64 + e;
+            float y[4];
+            unpair(fma2(pair64(s[at], s[at + 1]), c2, b2), y[0], y[1]);
+            unpair(fma2(pair64(s[at + 2], s[at + 3]), c2, b2), y[2], y[3]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] = ex2_approx(y[q]);
+            sum0 = add2(sum0, pair64(y[0], y[1]));
+            sum1 = add2(sum1, pair64(y[2], y[3]));
+            pk[e / 2] = pack2<T>(y[0], y[1]);
+            pk[e / 2 + 1] = pack2<T>(y[2], y[3]);
+          }
+          tmem_st32(s_at + half * 32, pk);
+        }
+        tmem_wait_st();
+        tmem_before_sync();
+        warp_arrive(P_FULL + i);
+        float u0, u1;
+        unpair(add2(sum0, sum1), u0, u1);
+        if (BF16) l += u0 + u1;
+        else l = fmaf(u0 + u1, 1.f / mt.v, l);
+      }
+      if (!ok) break;
+      // ---- the segment's result
+      ok = wait(PV_DONE + i, mine - 1);
+      ok = __all_sync(FULL, ok);
+      if (!ok) break;
+      tmem_after_sync();
+      const bool whole = w.whole();
+      const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+      float *part = new_part<D>(a, slot) + R * 4;
+      const float inv = 1.f / l;  // (a row sees itself: 0 only where its scores are all -inf, and then the result is NaN)
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_at + d, o);
+        tmem_wait_ld();
+        if (R >= w.unit.nrows) continue;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(o[8 * e + q]) * inv;
+            reinterpret_cast<uint4 *>(out + d)[e] =
+                make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4 *>(part + (d / 4 + e) * (ROWS * 4)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      tmem_before_sync();
+      warp_arrive(O_EMPTY + i);
+      if (R < w.unit.nrows) {
+        if (!whole) {
+          float *ml = new_part<D>(a, slot) + ROWS * D + R;
+          ml[0] = m;
+          ml[ROWS] = l;
+        }
+        const int n = bad_count[segments % BAD_SEGMENTS];
+        uint32_t any = 0;
+        for (int k = 0; k < n; ++k)
+          for (int q = 0; q < LOADERS; ++q) any |= bad_tiles[segments % BAD_SEGMENTS][k].word[q];
+        if (any)
+          spoil<T, D>(a, bad_tiles[segments % BAD_SEGMENTS], n, w.row.q0, w.row.old, w.h, p, whole ? out : nullptr, part);
+      }
+      ++segments;
+    }
+  }
+  if (bits) atomicOr(a.err, bits);
+  tmem_before_sync();
+  __syncthreads();
+  tmem_after_sync();
+  if (warp == W_ISSUE) tmem_free(tmem, 512);
+}
+
+// The parts of the units that cuts went through: 32 rows a block, lanes along rows.
+constexpr int JOIN_THREADS = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ KvNewArgs a) {
+  const Join join = *join_of(a, blockIdx.x);
+  const int R = blockIdx.y * 32 + (threadIdx.x & 31);
+  if (R >= join.nrows || join.parts == 0) return;
+  auto slot = [&](int p) { return new_part<D>(a, 2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)); };
+  float top = -CUDART_INF_F, l = 0.f;
+  for (int p = 0; p < join.parts; ++p) top = fmaxf(top, slot(p)[ROWS * D + R]);
+  const float base = top == -CUDART_INF_F ? 0.f : top;
+  for (int p = 0; p < join.parts; ++p) {
+    const float *ml = slot(p) + ROWS * D + R;
+    l = fmaf(ml[ROWS], ex2_approx(ml[0] - base), l);
+  }
+  const float inv = 1.f / l;
+  const int row = join.r0 + R;
+  T *out = static_cast<T *>(a.out) +
+           ((long long)(join.q0 + row / a.group) * a.q_heads + join.h * a.group + row % a.group) * D;
+#pragma unroll 1
+  for (int d = threadIdx.x >> 5; d < D / 4; d += JOIN_THREADS / 32) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < join.parts; ++p) {
+      const float *from = slot(p);
+      const float4 v = *reinterpret_cast<const float4 *>(from + (d * ROWS + R) * 4);
+      const float k = ex2_approx(from[ROWS * D + R] - base);
+      x.x = fmaf(v.x, k, x.x);
+      x.y = fmaf(v.y, k, x.y);
+      x.z = fmaf(v.z, k, x.z);
+      x.w = fmaf(v.w, k, x.w);
+    }
+    *reinterpret_cast<uint2 *>(out + d * 4) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(KvNewArgs a, cudaStream_t st, int *launches) {
+  CUtensorMap k = {}, v = {};
+  // (strides that a map does not take: the loading warps copy the tiles)
+  a.k_vec = a.k_vec && kv_make_token_map(&k, a.k, D, a.c.heads, a.r.N, a.k_head, a.k_token, TILE);
+  a.v_vec = a.v_vec && kv_make_token_map(&v, a.v, D, a.c.heads, a.r.N, a.v_head, a.v_token, TILE);
+  const int ctas = a.sms < MAX_CTAS ? a.sms : MAX_CTAS;
+  new_kernel<T, D><<<ctas, THREADS, Plan<D>::SMEM, st>>>(a, k, v);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  *launches = 2;
+  join_kernel<T, D><<<dim3(ctas, ROWS / 32), JOIN_THREADS, 0, st>>>(a);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t limit() {
+  return cudaFuncSetAttribute(new_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<D>::SMEM);
 }
 
 }  // namespace
 
-size_t kv_new_workspace(int sms) { return 0; }
-cudaError_t kv_new_set_limits() { return cudaSuccess; }
+size_t kv_new_workspace(int sms) {
+  const size_t ctas = sms < MAX_CTAS ? sms : MAX_CTAS;
+  return (size_t)MAX_CTAS * 8 + MAX_CTAS * 32 + ctas * 2 * (ROWS * (128 + 2) * 4);
+}
+
+cudaError_t kv_new_set_limits() {
+  cudaError_t e = limit<__half, 128>();
+  if (e == cudaSuccess) e = limit<__half, 64>();
+  if (e == cudaSuccess) e = limit<__nv_bfloat16, 128>();
+  if (e == cudaSuccess) e = limit<__nv_bfloat16, 64>();
+  return e;
+}
 
 cudaError_t launch_kv_new(const KvNewArgs &a, int dtype, cudaStream_t st, int *launches) {
   *launches = 1;
-  return dtype == SGD_F16 ? launch<__half>(a, st) : launch<__nv_bfloat16>(a, st);
+  if (a.c.dim == 128) return dtype == SGD_F16 ? launch<__half, 128>(a, st, launches) : launch<__nv_bfloat16, 128>(a, st, launches);
+  return dtype == SGD_F16 ? launch<__half, 64>(a, st, launches) : launch<__nv_bfloat16, 64>(a, st, launches);
 }
 
 }  // namespace sgd
