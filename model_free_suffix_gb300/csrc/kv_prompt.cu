@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int bad_count[BAD_SEGMENTS];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL, tid >> 5, 0);
   uint32_t bits = 0;
   const Share &share = share_of(a, reinterpret_cast<int *>(smem), &bits);
   if (share.ctas == 0) {
@@ -766,75 +766,99 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= W_ISSUE) {
     fewer_registers<REGS_OTHER>();
-    if (warp == W_ISSUE && lane == 0) {
-      constexpr uint32_t QK = product16(BF16, TILE, false), PV = product16(BF16, D, true);
+    if (warp == W_ISSUE) {
+      // The whole warp walks, so that addresses and counters are the warp's (in its
+      // uniform registers, where the products take them from); one thread issues.
+      constexpr uint32_t QK = product16(BF16, TILE, false), PV = product16(BF16, D, true), HIGH = operand_high(1024);
       Walk w(a, share);
       uint32_t item = 0, segments = 0, done0 = 0, done1 = 0, segs1 = 0;
       bool ok = true;
+      auto wait_all = [&](int which, uint32_t parity) {
+        const uint32_t b = bar(which);
+        if (__all_sync(FULL, bar_try(b, parity & 1))) return true;
+        return (bool)__all_sync(FULL, wait(which, parity));
+      };
+      const uint32_t q_low = operand_low(q_at, 0), k_low = operand_low(ring, 0), v_low = operand_low(ring, TILE * 128);
       auto qk = [&](int i, uint32_t slot) {
-        const uint32_t q = q_at + i * (M * D * 2), k = ring + slot * L::HALF;
+        const uint32_t q = q_low + i * (M * D * 2 / 16), k = k_low + slot * (L::HALF / 16);
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) {
-          const uint32_t off = (e / 4) * (TILE * 128) + (e % 4) * 32;
-          mma_ss(tmem + L::S + i * TILE, smem_operand(q + off, 1024, 16), smem_operand(k + off, 1024, 16), QK, e > 0);
+          const uint32_t off = ((e / 4) * (TILE * 128) + (e % 4) * 32) / 16;
+          mma_ss(tmem + L::S + i * TILE, q + off, k + off, HIGH, QK, e > 0);
         }
       };
       auto pv = [&](int i, uint32_t slot, bool add) {
-        const uint32_t v = ring + slot * L::HALF;
+        const uint32_t v = v_low + slot * (L::HALF / 16), p = tmem + L::S + i * TILE, o = tmem + L::O + i * D;
+        mma_ts(o, p, v, HIGH, PV, add);
 #pragma unroll
-        for (int e = 0; e < TILE / 16; ++e)
-          mma_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + e * 8, smem_operand(v + e * 2048, 1024, TILE * 128), PV, add || e > 0);
+        for (int e = 1; e < TILE / 16; ++e) mma_ts(o, p + e * 8, v + e * (2048 / 16), HIGH, PV, true);
       };
       while (ok && w.next(&bits)) {
-        const int n = w.t1 - w.t0;
+        const int n = __shfl_sync(FULL, w.t1 - w.t0, 0);
         if (n == 0) continue;
-        const bool two = w.unit.nrows > M;
-        ok = wait(FULL_AT + item % STAGES, item / STAGES) && wait(Q_FULL, segments);
+        const bool two = __shfl_sync(FULL, w.unit.nrows, 0) > M;
+        ok = wait_all(FULL_AT + item % STAGES, item / STAGES) && wait_all(Q_FULL, segments);
         if (!ok) break;
         tmem_after_sync();
-        qk(0, item % STAGES);
-        mma_commit(bar(S_FULL));
-        if (two) {
-          qk(1, item % STAGES);
-          mma_commit(bar(S_FULL + 1));
+        if (elect_one()) {
+          const uint32_t slot = item % STAGES;
+          qk(0, slot);
+          mma_commit(bar(S_FULL));
+          if (two) {
+            qk(1, slot);
+            mma_commit(bar(S_FULL + 1));
+          }
+          mma_commit(bar(EMPTY_AT + slot));
+          if (n == 1) mma_commit(bar(Q_EMPTY));
         }
-        mma_commit(bar(EMPTY_AT + item % STAGES));
-        if (n == 1) mma_commit(bar(Q_EMPTY));
+        __syncwarp();
         for (int j = 0; j < n; ++j) {
-          const uint32_t vi = item + 1, ki = item + 2;
+          const uint32_t vi = item + 1, ki = item + 2, vs = vi % STAGES, ks = ki % STAGES;
           const bool more = j + 1 < n;
-          ok = wait(FULL_AT + vi % STAGES, vi / STAGES) && wait(P_FULL, done0);
-          if (ok && j == 0 && segments > 0) ok = wait(O_EMPTY, segments - 1);
+          ok = wait_all(FULL_AT + vs, vi / STAGES) && wait_all(P_FULL, done0);
+          if (ok && j == 0 && segments > 0) ok = wait_all(O_EMPTY, segments - 1);
           if (!ok) break;
           tmem_after_sync();
-          pv(0, vi % STAGES, j > 0);
-          mma_commit(bar(PV_DONE));
+          if (elect_one()) {
+            pv(0, vs, j > 0);
+            mma_commit(bar(PV_DONE));
+            if (!two) mma_commit(bar(EMPTY_AT + vs));
+          }
+          __syncwarp();
           ++done0;
-          if (!two) mma_commit(bar(EMPTY_AT + vi % STAGES));
           if (more) {
-            ok = wait(FULL_AT + ki % STAGES, ki / STAGES);
+            ok = wait_all(FULL_AT + ks, ki / STAGES);
             if (!ok) break;
             tmem_after_sync();
-            qk(0, ki % STAGES);
-            mma_commit(bar(S_FULL));
-            if (!two) mma_commit(bar(EMPTY_AT + ki % STAGES));
+            if (elect_one()) {
+              qk(0, ks);
+              mma_commit(bar(S_FULL));
+              if (!two) {
+                mma_commit(bar(EMPTY_AT + ks));
+                if (j + 2 == n) mma_commit(bar(Q_EMPTY));
+              }
+            }
+            __syncwarp();
           }
           if (two) {
-            ok = wait(P_FULL + 1, done1);
-            if (ok && j == 0 && segs1 > 0) ok = wait(O_EMPTY + 1, segs1 - 1);
+            ok = wait_all(P_FULL + 1, done1);
+            if (ok && j == 0 && segs1 > 0) ok = wait_all(O_EMPTY + 1, segs1 - 1);
             if (!ok) break;
             tmem_after_sync();
-            pv(1, vi % STAGES, j > 0);
-            mma_commit(bar(PV_DONE + 1));
-            ++done1;
-            mma_commit(bar(EMPTY_AT + vi % STAGES));
-            if (more) {
-              qk(1, ki % STAGES);
-              mma_commit(bar(S_FULL + 1));
-              mma_commit(bar(EMPTY_AT + ki % STAGES));
+            if (elect_one()) {
+              pv(1, vs, j > 0);
+              mma_commit(bar(PV_DONE + 1));
+              mma_commit(bar(EMPTY_AT + vs));
+              if (more) {
+                qk(1, ks);
+                mma_commit(bar(S_FULL + 1));
+                mma_commit(bar(EMPTY_AT + ks));
+                if (j + 2 == n) mma_commit(bar(Q_EMPTY));
+              }
             }
+            __syncwarp();
+            ++done1;
           }
-          if (j + 2 == n) mma_commit(bar(Q_EMPTY));
           item += 2;
         }
         ++segments;

@@ -65,10 +65,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 // Lines along the operand's rows, elements of the product's long axis in a
 // line (K-major): `blocks` is the step from 8 rows to the next 8.  Lines along
 // the long axis (MN-major): `blocks` is the step from 8 of them to the next 8,
-// `panels` the step to the next 64 (16-bit) rows.
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t blocks, uint32_t panels) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(panels >> 4) << 16 | (uint64_t)(blocks >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// `panels` the step to the next 64 (16-bit) rows.  The high word has the layout,
+// the low word the address (a step within it is one addition) and the panels.
+__host__ __device__ constexpr uint32_t operand_high(uint32_t blocks) { return blocks >> 4 | 1u << 14 | 2u << 29; }
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t panels) {
+  return (addr & 0x3ffff) >> 4 | panels >> 4 << 16;
 }
 
 // 16-bit operands (both bf16, or both f16), f32 accumulators, M = 128; b_mn: B is MN-major.
@@ -77,22 +78,38 @@ __host__ __device__ constexpr uint32_t product16(bool bf16, int N, bool b_mn) {
          (128u >> 4) << 24;
 }
 
-// D[tmem] (+)= A[tmem] B[smem], 16 elements of the long axis.  By one thread.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+// One thread of the warp, all of whose threads are here.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
       "{.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d),
-      "r"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// D[tmem] (+)= A[tmem] B[smem], 16 elements of the long axis.  By one thread.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t b_high, uint32_t what, bool add) {
+  asm volatile(
+      "{.reg .pred p;\n\t"
+      ".reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;}" ::"r"(d),
+      "r"(a), "r"(b_low), "r"(b_high), "r"(what), "r"((uint32_t)add)
       : "memory");
 }
-// D[tmem] (+)= A[smem] B[smem], likewise.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+// D[tmem] (+)= A[smem] B[smem], likewise; the operands' layouts are the same.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t high, uint32_t what, bool add) {
   asm volatile(
       "{.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d),
-      "l"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      ".reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;}" ::"r"(d),
+      "r"(a_low), "r"(b_low), "r"(high), "r"(what), "r"((uint32_t)add)
       : "memory");
 }
 // Arrives at the barrier when all products that this thread has issued are done.
