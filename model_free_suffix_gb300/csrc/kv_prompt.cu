@@ -31,12 +31,16 @@ namespace {
 
 constexpr int M = 128, ROWS = 2 * M, TILE = 128;
 constexpr int WARPS = 16, THREADS = 32 * WARPS;
-// (warps 0 to 7: softmax)
+// (warps 0 to W_LOAD - 1: softmax)
 constexpr int W_LOAD = 8, W_ISSUE = 12, W_JOIN = 13;
 constexpr int LOADERS = 4;
 // Registers a thread by role: together what 512 threads are launched with (128 each).
 constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
-static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHER <= THREADS * 128, "the pool of the launch");
+static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
+// How far, as a power of 2, the maximum may grow before o is scaled to it; and what p is
+// multiplied by for f16, so that its range is used to the end (2^15.99 of 2^16), and p
+// keeps all bits down to 2^-21 of the largest, and 2^-33 of it in absolute terms below.
+constexpr float THRESHOLD = 8.f;
 constexpr int OVERHEAD = 2;   // of a unit, in tiles
 constexpr int LEAST_PART = 2; // tiles of a part
 constexpr int LEAST_SHARE = 4;
@@ -49,7 +53,8 @@ struct Plan {
   static constexpr int Q = ROWS * D * 2;
   static constexpr int STAGES = D == 128 ? 4 : 8;
   static constexpr int SMEM = 1024 + Q + STAGES * HALF;
-  static constexpr int S = 0, O = 2 * TILE;  // TMEM columns: s of either row tile (p over it), then o
+  // TMEM columns: s of a row tile and a key tile (p over it), in turn; then o of either row tile
+  static constexpr int BUFFERS = D == 128 ? 2 : 3, S = 0, O = BUFFERS * TILE;
   static constexpr int CHUNKS = D / 8;       // 16-byte chunks of a token
 };
 
@@ -487,7 +492,12 @@ __device__ __noinline__ void spoil(const KvNewArgs &a, const BadTile *bad, int n
       }
 }
 
-enum Bar { FULL_AT = 0, EMPTY_AT = 8, Q_FULL = 16, Q_EMPTY, S_FULL, P_FULL = S_FULL + 2, PV_DONE = P_FULL + 2, O_EMPTY = PV_DONE + 2, BARS = O_EMPTY + 2 };
+// A barrier's phases are told apart by their parity alone: whoever waits for one of
+// them waits for all, and none completes before the one before it was waited for.
+// S_FULL: BUFFERS for each row tile, in turn, since that many scores may be ahead.
+enum Bar {
+  FULL_AT = 0, EMPTY_AT = 8, Q_FULL = 16, Q_EMPTY = 17, S_FULL = 18, P_HALF = 24, P_FULL = 27, PV_HALF = 30, PV_DONE = 32, O_EMPTY = 34, SEGMENT_OVER = 36, BARS = SEGMENT_OVER + BAD_SEGMENTS
+};
 
 template <int REGS>
 __device__ __forceinline__ void more_registers() {
@@ -507,6 +517,12 @@ __device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) { asm("mo
 __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+// the largest of three, as fmaxf (NaN only where all are)
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
@@ -546,12 +562,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     bar_init(bar(Q_FULL), LOADERS);
     bar_init(bar(Q_EMPTY), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < L::BUFFERS; ++i) {
       bar_init(bar(S_FULL + i), 1);
+      bar_init(bar(S_FULL + L::BUFFERS + i), 1);
+      bar_init(bar(P_HALF + i), 4);
       bar_init(bar(P_FULL + i), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(PV_HALF + i), 1);
       bar_init(bar(PV_DONE + i), 1);
       bar_init(bar(O_EMPTY + i), 4);
     }
+    for (int i = 0; i < BAD_SEGMENTS; ++i) bar_init(bar(SEGMENT_OVER + i), W_LOAD);
     bar_init_fence();
     s_abort = 0;
   }
@@ -594,34 +616,42 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = __all_sync(FULL, ok);
       return ok;
     };
-    // the cached tile in hand: of page `lane` of it, the block and what its keys and values are multiplied by
+    // the cached tile in hand: of page `lane` of it, the block and what its keys and values
+    // are multiplied by (packed), and whether that is done in two steps
     int block = -1;
-    float k_scale = 0.f, v_scale = 0.f;
+    uint32_t k_by = 0, v_by = 0;
+    bool twice_k = false, twice_v = false;
     Meta mt{0u, 1.f, 1.f};
     auto pages = [&](int j) {
       const int x = w.at(j), index = (x >> a.c.page_bits) + lane;
       const bool in = lane < per_tile && index << a.c.page_bits < w.row.old;
       block = -1;
-      k_scale = v_scale = 0.f;
+      float ks = 0.f, vs = 0.f;
       if (in) {
         const int pg = __ldg(a.r.table + (long long)w.b * a.r.max_pages + index);
         if (pg >= 0 && pg < a.c.num_pages) {
           block = pg * a.c.heads + w.h;
-          k_scale = __ldg(a.c.ks + block);
-          v_scale = __ldg(a.c.vs + block);
+          ks = __ldg(a.c.ks + block);
+          vs = __ldg(a.c.vs + block);
         } else {
           bits |= SGD_KV_ERR_PAGE;
         }
       }
       const uint32_t lost = __ballot_sync(FULL, in && block < 0);
       mt.gone = 0;
-      for (int i = 0; i < per_tile; ++i)
-        if (lost >> i & 1) mt.gone |= ((1u << ((1 << a.c.page_bits) / 16)) - 1) << (i << (a.c.page_bits - 4));
-      mt.k = mt.v = 1.f;
-      if (!BF16) {
+      if (lost)
+        for (int i = 0; i < per_tile; ++i)
+          if (lost >> i & 1) mt.gone |= ((1u << ((1 << a.c.page_bits) / 16)) - 1) << (i << (a.c.page_bits - 4));
+      if (BF16) {
+        // 2^120 times a scale above 2^7 is beyond bf16
+        twice_k = __any_sync(FULL, ks > 128.f);
+        twice_v = __any_sync(FULL, vs > 128.f);
+        k_by = twice<T>(ks * (twice_k ? BF16_STEP : BF16_STEP * BF16_STEP));
+        v_by = twice<T>(vs * (twice_v ? BF16_STEP : BF16_STEP * BF16_STEP));
+      } else {
         // f16 has not the range of the scales: keys and values are brought to the largest
         // scale of the tile (those of much smaller ones lose bits below 2^-24 of it)
-        float km = k_scale, vm = v_scale;
+        float km = ks, vm = vs;
 #pragma unroll
         for (int o = 4; o; o >>= 1) {
           km = fmaxf(km, __shfl_xor_sync(FULL, km, o));
@@ -631,45 +661,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         vm = __shfl_sync(FULL, vm, 0);
         mt.k = km > 0.f ? km : 1.f;
         mt.v = vm > 0.f ? vm : 1.f;
-        k_scale *= 256.f / mt.k;
-        v_scale *= 256.f / mt.v;
+        k_by = twice<T>(ks * (256.f / mt.k));
+        v_by = twice<T>(vs * (256.f / mt.v));
       }
     };
-    auto load8 = [&](const uint8_t *base, uint4 (&v)[PER]) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int t = line0 + i * STEP, blk = __shfl_sync(FULL, block, t >> a.c.page_bits);
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (blk >= 0)
-          v[i] = __ldg(reinterpret_cast<const uint4 *>(base + ((long long)blk * a.c.page + (t & (a.c.page - 1))) * D) + c8);
-      }
+    uint4 raw[PER];  // what the thread has of the item in hand, then of the next
+    auto load8 = [&](const uint8_t *base, int i) {
+      const int t = line0 + i * STEP, blk = __shfl_sync(FULL, block, t >> a.c.page_bits);
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (blk >= 0)
+        raw[i] = __ldg(reinterpret_cast<const uint4 *>(base + ((long long)blk * a.c.page + (t & (a.c.page - 1))) * D) + c8);
     };
-    auto store8 = [&](uint32_t to, const uint4 (&v)[PER], float scale) {
+    // the i-th chunk into the ring
+    const int swap = D == 128 ? c8 >> 2 & 1 : 0;  // (lanes of a token's second half store in the other order: no bank twice)
+    auto store8 = [&](uint32_t to, int i, uint32_t by_lane, bool twice_by) {
+      const int t = line0 + i * STEP;
+      const uint32_t by = __shfl_sync(FULL, by_lane, t >> a.c.page_bits);
+      const uint4 v = swap ? make_uint4(raw[i].z, raw[i].w, raw[i].x, raw[i].y) : raw[i];
+      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+      uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int t = line0 + i * STEP;
-        const float s = __shfl_sync(FULL, scale, t >> a.c.page_bits);
-        const uint32_t f = BF16 ? twice<T>(s * BF16_STEP) : twice<T>(s), f2 = twice<T>(BF16_STEP);
-        const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[2 * e] = widen<T>(__byte_perm(in[e], 0, 0x1404), f);
-          h[2 * e + 1] = widen<T>(__byte_perm(in[e], 0, 0x3424), f);
-        }
-        if (BF16) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f2));
-        }
-        // (lanes of a token's second half write their chunks in the other order: no bank twice)
-        const int swap = D == 128 ? c8 >> 2 & 1 : 0;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool high = (e ^ swap) != 0;
-          st_shared16(chunk_at(to, t, 2 * c8 + (e ^ swap)), high ? h[4] : h[0], high ? h[5] : h[1], high ? h[6] : h[2],
-                      high ? h[7] : h[3]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        h[2 * e] = widen<T>(__byte_perm(in[e], 0, 0x1404), by);
+        h[2 * e + 1] = widen<T>(__byte_perm(in[e], 0, 0x3424), by);
       }
+      if (BF16 && twice_by) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(twice<T>(BF16_STEP)));
+      }
+      st_shared16(chunk_at(to, t, 2 * c8 + swap), h[0], h[1], h[2], h[3]);
+      st_shared16(chunk_at(to, t, 2 * c8 + 1 - swap), h[4], h[5], h[6], h[7]);
     };
     // hands the slot in hand to the products
     auto done = [&]() {
@@ -691,10 +712,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     while (ok && w.next(&bits)) {
       if (w.t0 == w.t1) continue;
-      uint4 kr[PER], vr[PER];
+      if (segments >= BAD_SEGMENTS) {
+        ok = wait(SEGMENT_OVER + segments % BAD_SEGMENTS, segments / BAD_SEGMENTS - 1);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+      }
       if (w.cached(w.t0)) {
         pages(w.t0);
-        load8(a.c.k, kr);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) load8(a.c.k, i);
       }
       int bads = 0;
       for (int j = w.t0; j < w.t1; ++j) {
@@ -709,8 +735,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++g;
         if (!slot_free()) break;
         if (cached) {
-          load8(a.c.v, vr);
-          store8(ring + item % STAGES * L::HALF, kr, k_scale);
+          // (a chunk's registers take the next item's, with as long as this item takes to arrive)
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            store8(ring + item % STAGES * L::HALF, i, k_by, twice_k);
+            load8(a.c.v, i);
+          }
           done();
         } else if (a.k_vec) {
           by_tma(&kmap, w.row.q0 + from);
@@ -730,12 +760,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!slot_free()) break;
         if (cached) {
-          const float vs = v_scale;
-          if (j + 1 < w.t1 && w.cached(j + 1)) {
-            pages(j + 1);
-            load8(a.c.k, kr);
+          const uint32_t by = v_by;
+          const bool two_steps = twice_v, more = j + 1 < w.t1 && w.cached(j + 1);
+          if (more) pages(j + 1);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            store8(ring + item % STAGES * L::HALF, i, by, two_steps);
+            if (more) load8(a.c.k, i);
           }
-          store8(ring + item % STAGES * L::HALF, vr, vs);
           done();
         } else if (a.v_vec && !w.edge(j, x)) {
           by_tma(&vmap, w.row.q0 + from);
@@ -771,7 +803,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       // uniform registers, where the products take them from); one thread issues.
       constexpr uint32_t QK = product16(BF16, TILE, false), PV = product16(BF16, D, true), HIGH = operand_high(1024);
       Walk w(a, share);
-      uint32_t item = 0, segments = 0, done0 = 0, done1 = 0, segs1 = 0;
+      uint32_t item = 0, segments = 0, segs1 = 0;
+      uint32_t s_buf = 0, p_buf = 0, p_use = 0;  // of the products in turn: the buffer, and how often it was used before
+      uint32_t s_bar0 = 0, s_bar1 = 0;           // of either row tile: the barrier of its next scores
       bool ok = true;
       auto wait_all = [&](int which, uint32_t parity) {
         const uint32_t b = bar(which);
@@ -784,85 +818,75 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) {
           const uint32_t off = ((e / 4) * (TILE * 128) + (e % 4) * 32) / 16;
-          mma_ss(tmem + L::S + i * TILE, q + off, k + off, HIGH, QK, e > 0);
+          mma_ss(tmem + L::S + s_buf * TILE, q + off, k + off, HIGH, QK, e > 0);
         }
       };
-      auto pv = [&](int i, uint32_t slot, bool add) {
-        const uint32_t v = v_low + slot * (L::HALF / 16), p = tmem + L::S + i * TILE, o = tmem + L::O + i * D;
+      // half of the tile's tokens at a time: the first products run while the second half of p is made
+      auto pv = [&](int i, uint32_t slot, int half, bool add) {
+        const uint32_t v = v_low + slot * (L::HALF / 16) + half * (64 * 128 / 16), p = tmem + L::S + p_buf * TILE + half * 32,
+                       o = tmem + L::O + i * D;
         mma_ts(o, p, v, HIGH, PV, add);
 #pragma unroll
-        for (int e = 1; e < TILE / 16; ++e) mma_ts(o, p + e * 8, v + e * (2048 / 16), HIGH, PV, true);
+        for (int e = 1; e < 4; ++e) mma_ts(o, p + e * 8, v + e * (2048 / 16), HIGH, PV, true);
       };
       while (ok && w.next(&bits)) {
         const int n = __shfl_sync(FULL, w.t1 - w.t0, 0);
         if (n == 0) continue;
-        const bool two = __shfl_sync(FULL, w.unit.nrows, 0) > M;
-        ok = wait_all(FULL_AT + item % STAGES, item / STAGES) && wait_all(Q_FULL, segments);
-        if (!ok) break;
-        tmem_after_sync();
-        if (elect_one()) {
-          const uint32_t slot = item % STAGES;
-          qk(0, slot);
-          mma_commit(bar(S_FULL));
-          if (two) {
-            qk(1, slot);
-            mma_commit(bar(S_FULL + 1));
+        const int two = __shfl_sync(FULL, w.unit.nrows, 0) > M, all = n << two;
+        ok = wait_all(Q_FULL, segments);
+        // the x-th product q k^T of the segment: row tile x & two of key tile x >> two
+        auto issue_qk = [&](int x) {
+          const int i = x & two, j = x >> two;
+          const uint32_t ki = item + 2 * j, ks = ki % STAGES;
+          if (i == 0) ok = ok && wait_all(FULL_AT + ks, ki / STAGES);
+          if (!ok) return;
+          tmem_after_sync();
+          if (elect_one()) {
+            qk(i, ks);
+            mma_commit(bar(S_FULL + (i ? L::BUFFERS + s_bar1 : s_bar0)));
+            if (i == two) mma_commit(bar(EMPTY_AT + ks));
+            if (x + 1 == all) mma_commit(bar(Q_EMPTY));
           }
-          mma_commit(bar(EMPTY_AT + slot));
-          if (n == 1) mma_commit(bar(Q_EMPTY));
-        }
-        __syncwarp();
-        for (int j = 0; j < n; ++j) {
-          const uint32_t vi = item + 1, ki = item + 2, vs = vi % STAGES, ks = ki % STAGES;
-          const bool more = j + 1 < n;
-          ok = wait_all(FULL_AT + vs, vi / STAGES) && wait_all(P_FULL, done0);
-          if (ok && j == 0 && segments > 0) ok = wait_all(O_EMPTY, segments - 1);
+          __syncwarp();
+          if (++s_buf == L::BUFFERS) s_buf = 0;
+          uint32_t &s_bar = i ? s_bar1 : s_bar0;
+          if (++s_bar == L::BUFFERS) s_bar = 0;
+        };
+        for (int x = 0; x < min(all, L::BUFFERS); ++x) issue_qk(x);
+        for (int x = 0; ok && x < all; ++x) {
+          const int i = x & two, j = x >> two;
+          const uint32_t vi = item + 2 * j + 1, vs = vi % STAGES;
+          if (i == 0) ok = wait_all(FULL_AT + vs, vi / STAGES);
+          ok = ok && wait_all(P_HALF + p_buf, p_use);
+          if (ok && j == 0) {
+            const uint32_t before = i ? segs1 : segments;
+            if (before > 0) ok = wait_all(O_EMPTY + i, before - 1);
+          }
           if (!ok) break;
           tmem_after_sync();
           if (elect_one()) {
-            pv(0, vs, j > 0);
-            mma_commit(bar(PV_DONE));
-            if (!two) mma_commit(bar(EMPTY_AT + vs));
+            pv(i, vs, 0, j > 0);
+            mma_commit(bar(PV_HALF + i));
           }
           __syncwarp();
-          ++done0;
-          if (more) {
-            ok = wait_all(FULL_AT + ks, ki / STAGES);
-            if (!ok) break;
-            tmem_after_sync();
-            if (elect_one()) {
-              qk(0, ks);
-              mma_commit(bar(S_FULL));
-              if (!two) {
-                mma_commit(bar(EMPTY_AT + ks));
-                if (j + 2 == n) mma_commit(bar(Q_EMPTY));
-              }
-            }
-            __syncwarp();
+          ok = wait_all(P_FULL + p_buf, p_use);
+          if (!ok) break;
+          tmem_after_sync();
+          if (elect_one()) {
+            pv(i, vs, 1, true);
+            mma_commit(bar(PV_DONE + i));
+            if (i == two) mma_commit(bar(EMPTY_AT + vs));
           }
-          if (two) {
-            ok = wait_all(P_FULL + 1, done1);
-            if (ok && j == 0 && segs1 > 0) ok = wait_all(O_EMPTY + 1, segs1 - 1);
-            if (!ok) break;
-            tmem_after_sync();
-            if (elect_one()) {
-              pv(1, vs, j > 0);
-              mma_commit(bar(PV_DONE + 1));
-              mma_commit(bar(EMPTY_AT + vs));
-              if (more) {
-                qk(1, ks);
-                mma_commit(bar(S_FULL + 1));
-                mma_commit(bar(EMPTY_AT + ks));
-                if (j + 2 == n) mma_commit(bar(Q_EMPTY));
-              }
-            }
-            __syncwarp();
-            ++done1;
+          __syncwarp();
+          if (++p_buf == L::BUFFERS) {
+            p_buf = 0;
+            ++p_use;
           }
-          item += 2;
+          if (x + L::BUFFERS < all) issue_qk(x + L::BUFFERS);
         }
+        item += 2 * n;
         ++segments;
-        if (two) ++segs1;
+        segs1 += two;
       }
     } else if (warp == W_JOIN && lane == 0) {
       // the unit that this share ends within, if it begins here: how many shares hold it
@@ -891,15 +915,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     more_registers<REGS_SOFTMAX>();
     const int i = warp >> 2, r = tid & 127, R = i * M + r;  // the warpgroup's row tile, the thread's row of it, of the unit
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t s_at = tmem + lanes + L::S + i * TILE, o_at = tmem + lanes + L::O + i * D;
+    const uint32_t o_at = tmem + lanes + L::O + i * D;
     const float c0 = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);
-    constexpr float THRESHOLD = BF16 ? 8.f : LAZY, UP = BF16 ? 0.f : LIFT;
+    constexpr float UP = BF16 ? 0.f : 7.99f;
     Walk w(a, share);
     uint32_t g = 0, mine = 0, segments = 0;
+    uint32_t buf = 0;                // of the next segment's first scores
+    uint32_t s_bar = 0, s_use = 0;   // of the row tile's next scores: their barrier, and how often it was used before
     bool ok = true;
     while (ok && w.next(&bits)) {
-      const int tiles = w.t1 - w.t0;
-      const bool on = w.unit.nrows > i * M;
+      const int tiles = w.t1 - w.t0, two = w.unit.nrows > M;
       const int t = (w.unit.r0 + R) / a.group, p = w.row.old + t;
       T *out = static_cast<T *>(a.out) + ((long long)(w.row.q0 + t) * a.q_heads + w.h * a.group + (w.unit.r0 + R) % a.group) * D;
       if (tiles == 0) {
@@ -907,90 +932,138 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(out + d) = make_uint4(0, 0, 0, 0);
         continue;
       }
-      if (!on) {
+      uint32_t s_buf = (buf + i) % L::BUFFERS;
+      buf = (buf + ((uint32_t)tiles << two)) % L::BUFFERS;
+      if (i > two) {
+        // (no rows here.  Not further ahead than the phase before, or this warpgroup would
+        // arrive in the other's place)
+        if (segments >= BAD_SEGMENTS) ok = wait(SEGMENT_OVER + segments % BAD_SEGMENTS, segments / BAD_SEGMENTS - 1);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
         g += tiles;
+        warp_arrive(SEGMENT_OVER + segments % BAD_SEGMENTS);
         ++segments;
         continue;
       }
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = w.t0; j < w.t1; ++j, ++g, ++mine) {
-        ok = wait(S_FULL + i, mine);
+        ok = wait(S_FULL + i * L::BUFFERS + s_bar, s_use);
         ok = __all_sync(FULL, ok);
         if (!ok) break;
         tmem_after_sync();
-        float s[TILE];
-#pragma unroll
-        for (int e = 0; e < TILE; e += 32) tmem_ld32(s_at + e, reinterpret_cast<uint32_t *>(s) + e);
+        const uint32_t s_at = tmem + lanes + L::S + s_buf * TILE;
+        uint32_t sa[32], sb[32], pk[32];
+        tmem_ld32(s_at, sa);
         const Meta mt = meta[g % META];
         const int x = w.at(j);
-        tmem_wait_ld();
-        if (w.edge(j, x) || mt.gone) {
-          const int lim = min(p, w.cached(j) ? w.row.old - 1 : p) - x;  // the row sees slots up to lim
-          const int from = a.window > 0 ? p - a.window + 1 - x : 0, sink = a.sinks - x;
+        const bool masked = w.edge(j, x) || mt.gone;
+        const int lim = min(p, w.cached(j) ? w.row.old - 1 : p) - x;  // the row sees slots up to lim
+        const int from = a.window > 0 ? p - a.window + 1 - x : 0, sink = a.sinks - x;
+        // z = s c; m is kept relative to z + log2 V, V the scale that the tile's values were brought to
+        const float c = BF16 ? c0 : fmaxf(c0 * mt.k, 1e-37f), lv = BF16 ? 0.f : __log2f(mt.v), iv = BF16 ? 1.f : __fdividef(1.f, mt.v);
+        const uint64_t c2 = pair64(c, c);
+        float base, top0, top1;
+        uint64_t sum0, sum1;
+        // 32 tokens' p relative to m as it is, with the largest score and the sum beside it
+        auto exps = [&](uint32_t (&s)[32], int e0, uint32_t *to) {
+          if (masked) {
 #pragma unroll
-          for (int e = 0; e < TILE; ++e)
-            if (e > lim || (e < from && e >= sink) || (mt.gone >> (e / 16) & 1)) s[e] = -CUDART_INF_F;
-        }
-        float top0 = s[0], top1 = s[1], top2 = s[2], top3 = s[3];
-#pragma unroll
-        for (int e = 4; e < TILE; e += 4) {
-          top0 = fmaxf(top0, s[e]);
-          top1 = fmaxf(top1, s[e + 1]);
-          top2 = fmaxf(top2, s[e + 2]);
-          top3 = fmaxf(top3, s[e + 3]);
-        }
-        // m: the running maximum of z + log2 V, V the scale that the tile's values were brought to
-        const float c = BF16 ? c0 : fmaxf(c0 * mt.k, 1e-37f), lv = BF16 ? 0.f : __log2f(mt.v);
-        const float top = fmaf(fmaxf(fmaxf(top0, top1), fmaxf(top2, top3)), c, lv);
-        float o_scale = 1.f;
-        if (top > m + THRESHOLD || (m == -CUDART_INF_F && top > m)) {
-          o_scale = m == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
-          l *= o_scale;
-          m = top;
-        }
-        if (j > w.t0 && __any_sync(FULL, o_scale != 1.f)) {
-          ok = wait(PV_DONE + i, mine - 1);
-          ok = __all_sync(FULL, ok);
-          if (!ok) break;
-          tmem_after_sync();
-#pragma unroll
-          for (int d = 0; d < D; d += 16) {
-            uint32_t o[16];
-            tmem_ld16(o_at + d, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * o_scale);
-            tmem_st16(o_at + d, o);
+            for (int e = 0; e < 32; ++e)
+              if (e0 + e > lim || (e0 + e < from && e0 + e >= sink) || (mt.gone >> ((e0 + e) / 16) & 1)) s[e] = 0xff800000u;
           }
-        }
-        const float base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
-        const uint64_t c2 = pair64(c, c), b2 = pair64(-base, -base);
-        uint64_t sum0 = 0, sum1 = 0;
+          const uint64_t b2 = pair64(-base, -base);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const int at = half * 64 + e;
+          for (int e = 0; e < 32; e += 4) {
             float y[4];
-            unpair(fma2(pair64(s[at], s[at + 1]), c2, b2), y[0], y[1]);
-            unpair(fma2(pair64(s[at + 2], s[at + 3]), c2, b2), y[2], y[3]);
+            top0 = max3(top0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            top1 = max3(top1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+            unpair(fma2(pair64(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), y[0], y[1]);
+            unpair(fma2(pair64(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), y[2], y[3]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) y[q] = ex2_approx(y[q]);
             sum0 = add2(sum0, pair64(y[0], y[1]));
             sum1 = add2(sum1, pair64(y[2], y[3]));
-            pk[e / 2] = pack2<T>(y[0], y[1]);
-            pk[e / 2 + 1] = pack2<T>(y[2], y[3]);
+            to[e / 2] = pack2<T>(y[0], y[1]);
+            to[e / 2 + 1] = pack2<T>(y[2], y[3]);
           }
+        };
+        auto begin = [&]() {
+          base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
+          top0 = top1 = -CUDART_INF_F;
+          sum0 = sum1 = 0;
+        };
+        // A half's end: where the maximum has grown too far for p to be relative to the old
+        // one (rarely but for a segment's first), o and l are scaled and the half is made anew.
+        auto end = [&](int half) {
+          const float top = fmaf(fmaxf(top0, top1), c, lv);
+          const bool grown = top > m + THRESHOLD || (m == -CUDART_INF_F && top > m);
+          if (__any_sync(FULL, grown)) {
+            float o_scale = 1.f;
+            if (grown) {
+              o_scale = m == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
+              l *= o_scale;
+              m = top;
+            }
+            if (j > w.t0 || half > 0) {
+              if (j > w.t0) ok = wait(PV_DONE + i, mine - 1);
+              if (half > 0) ok = ok && wait(PV_HALF + i, mine);
+              ok = __all_sync(FULL, ok);
+              if (ok) {
+                tmem_after_sync();
+#pragma unroll 1
+                for (int d = 0; d < D; d += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(o_at + d, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * o_scale);
+                  tmem_st16(o_at + d, o);
+                }
+              }
+            }
+            begin();
+            tmem_wait_ld();
+            uint32_t s[32];
+            tmem_ld32(s_at + half * 64, s);
+            tmem_wait_ld();
+            exps(s, half * 64, pk);
+            tmem_ld32(s_at + half * 64 + 32, s);
+            tmem_wait_ld();
+            exps(s, half * 64 + 32, pk + 16);
+          }
+          float u0, u1;
+          unpair(add2(sum0, sum1), u0, u1);
+          l = BF16 ? l + (u0 + u1) : fmaf(u0 + u1, iv, l);
           tmem_st32(s_at + half * 32, pk);
-        }
-        tmem_wait_st();
+          tmem_wait_st();
+        };
+        begin();
+        tmem_wait_ld();
+        tmem_ld32(s_at + 32, sb);
+        exps(sa, 0, pk);
+        tmem_wait_ld();
+        tmem_ld32(s_at + 64, sa);
+        exps(sb, 32, pk + 16);
+        end(0);
         tmem_before_sync();
-        warp_arrive(P_FULL + i);
-        float u0, u1;
-        unpair(add2(sum0, sum1), u0, u1);
-        if (BF16) l += u0 + u1;
-        else l = fmaf(u0 + u1, 1.f / mt.v, l);
+        warp_arrive(P_HALF + s_buf);
+        begin();
+        tmem_wait_ld();
+        tmem_ld32(s_at + 96, sb);
+        exps(sa, 64, pk);
+        tmem_wait_ld();
+        exps(sb, 96, pk + 16);
+        if (j > w.t0) ok = ok && wait(PV_DONE + i, mine - 1);
+        end(1);
+        tmem_before_sync();
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        warp_arrive(P_FULL + s_buf);
+        if ((s_buf += 1 + two) >= L::BUFFERS) s_buf -= L::BUFFERS;
+        if (++s_bar == L::BUFFERS) {
+          s_bar = 0;
+          ++s_use;
+        }
       }
       if (!ok) break;
       // ---- the segment's result
@@ -1038,6 +1111,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (any)
           spoil<T, D>(a, bad_tiles[segments % BAD_SEGMENTS], n, w.row.q0, w.row.old, w.h, p, whole ? out : nullptr, part);
       }
+      warp_arrive(SEGMENT_OVER + segments % BAD_SEGMENTS);
       ++segments;
     }
   }
