@@ -953,112 +953,104 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_after_sync();
         const uint32_t s_at = tmem + lanes + L::S + s_buf * TILE;
         uint32_t sa[32], sb[32], pk[32];
-        tmem_ld32(s_at, sa);
         const Meta mt = meta[g % META];
         const int x = w.at(j);
-        const bool masked = w.edge(j, x) || mt.gone;
-        const int lim = min(p, w.cached(j) ? w.row.old - 1 : p) - x;  // the row sees slots up to lim
-        const int from = a.window > 0 ? p - a.window + 1 - x : 0, sink = a.sinks - x;
+        if (w.edge(j, x) || mt.gone) {
+          // s of what a row does not see becomes -inf, in place
+          const int lim = min(p, w.cached(j) ? w.row.old - 1 : p) - x;  // the row sees slots up to lim
+          const int from = a.window > 0 ? p - a.window + 1 - x : 0, sink = a.sinks - x;
+#pragma unroll 1
+          for (int e0 = 0; e0 < TILE; e0 += 16) {
+            tmem_ld16(s_at + e0, sa);
+            tmem_wait_ld();
+            const bool gone = mt.gone >> (e0 / 16) & 1;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e0 + e > lim || (e0 + e < from && e0 + e >= sink) || gone) sa[e] = 0xff800000u;
+            tmem_st16(s_at + e0, sa);
+          }
+          tmem_wait_st();
+        }
         // z = s c; m is kept relative to z + log2 V, V the scale that the tile's values were brought to
         const float c = BF16 ? c0 : fmaxf(c0 * mt.k, 1e-37f), lv = BF16 ? 0.f : __log2f(mt.v), iv = BF16 ? 1.f : __fdividef(1.f, mt.v);
         const uint64_t c2 = pair64(c, c);
-        float base, top0, top1;
-        uint64_t sum0, sum1;
-        // 32 tokens' p relative to m as it is, with the largest score and the sum beside it
-        auto exps = [&](uint32_t (&s)[32], int e0, uint32_t *to) {
-          if (masked) {
+        tmem_ld32(s_at, sa);
+        // Half of the tokens at a time, so that the products with the first run beside the
+        // exponentials of the second.  (Loops rather than straight code: what 16 warps in
+        // three roles run has to stay in the instruction cache.)
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float top;
+          uint64_t sum;
+          for (;;) {
+            const float base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
+            const uint64_t b2 = pair64(-base, -base);
+            float top0 = -CUDART_INF_F, top1 = -CUDART_INF_F;
+            uint64_t sum0 = 0, sum1 = 0;
+            // 32 tokens' p relative to m as it is, with the largest score and the sum beside it
+            auto exps = [&](const uint32_t (&s)[32], uint32_t *to) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e0 + e > lim || (e0 + e < from && e0 + e >= sink) || (mt.gone >> ((e0 + e) / 16) & 1)) s[e] = 0xff800000u;
-          }
-          const uint64_t b2 = pair64(-base, -base);
+              for (int e = 0; e < 32; e += 4) {
+                float y[4];
+                top0 = max3(top0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                top1 = max3(top1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                unpair(fma2(pair64(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), y[0], y[1]);
+                unpair(fma2(pair64(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), y[2], y[3]);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float y[4];
-            top0 = max3(top0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-            top1 = max3(top1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
-            unpair(fma2(pair64(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), y[0], y[1]);
-            unpair(fma2(pair64(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), y[2], y[3]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) y[q] = ex2_approx(y[q]);
-            sum0 = add2(sum0, pair64(y[0], y[1]));
-            sum1 = add2(sum1, pair64(y[2], y[3]));
-            to[e / 2] = pack2<T>(y[0], y[1]);
-            to[e / 2 + 1] = pack2<T>(y[2], y[3]);
-          }
-        };
-        auto begin = [&]() {
-          base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
-          top0 = top1 = -CUDART_INF_F;
-          sum0 = sum1 = 0;
-        };
-        // A half's end: where the maximum has grown too far for p to be relative to the old
-        // one (rarely but for a segment's first), o and l are scaled and the half is made anew.
-        auto end = [&](int half) {
-          const float top = fmaf(fmaxf(top0, top1), c, lv);
-          const bool grown = top > m + THRESHOLD || (m == -CUDART_INF_F && top > m);
-          if (__any_sync(FULL, grown)) {
+                for (int q = 0; q < 4; ++q) y[q] = ex2_approx(y[q]);
+                sum0 = add2(sum0, pair64(y[0], y[1]));
+                sum1 = add2(sum1, pair64(y[2], y[3]));
+                to[e / 2] = pack2<T>(y[0], y[1]);
+                to[e / 2 + 1] = pack2<T>(y[2], y[3]);
+              }
+            };
+            tmem_wait_ld();
+            tmem_ld32(s_at + half * 64 + 32, sb);
+            exps(sa, pk);
+            tmem_wait_ld();
+            if (half == 0) tmem_ld32(s_at + 64, sa);
+            exps(sb, pk + 16);
+            top = fmaf(fmaxf(top0, top1), c, lv);
+            sum = add2(sum0, sum1);
+            // Where the maximum has grown too far for p to be relative to the old one (rarely
+            // but for a segment's first half), o and l are scaled and the half is made anew.
+            const bool grown = top > m + THRESHOLD || (m == -CUDART_INF_F && top > m);
+            if (!__any_sync(FULL, grown)) break;
             float o_scale = 1.f;
             if (grown) {
               o_scale = m == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
               l *= o_scale;
               m = top;
             }
+            tmem_wait_ld();
             if (j > w.t0 || half > 0) {
-              if (j > w.t0) ok = wait(PV_DONE + i, mine - 1);
+              if (j > w.t0) ok = ok && wait(PV_DONE + i, mine - 1);
               if (half > 0) ok = ok && wait(PV_HALF + i, mine);
-              ok = __all_sync(FULL, ok);
-              if (ok) {
-                tmem_after_sync();
+              if (!__all_sync(FULL, ok)) break;
+              tmem_after_sync();
 #pragma unroll 1
-                for (int d = 0; d < D; d += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(o_at + d, o);
-                  tmem_wait_ld();
+              for (int d = 0; d < D; d += 16) {
+                tmem_ld16(o_at + d, sa);
+                tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * o_scale);
-                  tmem_st16(o_at + d, o);
-                }
+                for (int e = 0; e < 16; ++e) sa[e] = __float_as_uint(__uint_as_float(sa[e]) * o_scale);
+                tmem_st16(o_at + d, sa);
               }
+              tmem_wait_st();
             }
-            begin();
-            tmem_wait_ld();
-            uint32_t s[32];
-            tmem_ld32(s_at + half * 64, s);
-            tmem_wait_ld();
-            exps(s, half * 64, pk);
-            tmem_ld32(s_at + half * 64 + 32, s);
-            tmem_wait_ld();
-            exps(s, half * 64 + 32, pk + 16);
+            tmem_ld32(s_at + half * 64, sa);
           }
           float u0, u1;
-          unpair(add2(sum0, sum1), u0, u1);
+          unpair(sum, u0, u1);
           l = BF16 ? l + (u0 + u1) : fmaf(u0 + u1, iv, l);
           tmem_st32(s_at + half * 32, pk);
+          if (half > 0 && j > w.t0) ok = ok && wait(PV_DONE + i, mine - 1);
           tmem_wait_st();
-        };
-        begin();
-        tmem_wait_ld();
-        tmem_ld32(s_at + 32, sb);
-        exps(sa, 0, pk);
-        tmem_wait_ld();
-        tmem_ld32(s_at + 64, sa);
-        exps(sb, 32, pk + 16);
-        end(0);
-        tmem_before_sync();
-        warp_arrive(P_HALF + s_buf);
-        begin();
-        tmem_wait_ld();
-        tmem_ld32(s_at + 96, sb);
-        exps(sa, 64, pk);
-        tmem_wait_ld();
-        exps(sb, 96, pk + 16);
-        if (j > w.t0) ok = ok && wait(PV_DONE + i, mine - 1);
-        end(1);
-        tmem_before_sync();
+          tmem_before_sync();
+          warp_arrive((half ? P_FULL : P_HALF) + s_buf);
+        }
         ok = __all_sync(FULL, ok);
         if (!ok) break;
-        warp_arrive(P_FULL + s_buf);
         if ((s_buf += 1 + two) >= L::BUFFERS) s_buf -= L::BUFFERS;
         if (++s_bar == L::BUFFERS) {
           s_bar = 0;
