@@ -30,12 +30,13 @@ namespace sgd {
 namespace {
 
 constexpr int M = 128, ROWS = 2 * M, TILE = 128;
-// (warps 0 to W_LOAD - 1: softmax; the last three: nothing, but registers go by warpgroups)
-constexpr int W_LOAD = 16, LOADERS = 4, W_ISSUE = W_LOAD + LOADERS;
-constexpr int WARPS = W_ISSUE + 4, THREADS = 32 * WARPS;
-// Registers a thread by role: together what the threads are launched with (80 each).
-constexpr int REGS_SOFTMAX = 88, REGS_LOAD = 80, REGS_ISSUE = 48;
-static_assert(32 * W_LOAD * REGS_SOFTMAX + 128 * REGS_LOAD + 128 * REGS_ISSUE <= THREADS * 80, "the pool of the launch");
+constexpr int WARPS = 16, THREADS = 32 * WARPS;
+// (warps 0 to W_LOAD - 1: softmax)
+constexpr int W_LOAD = 8, W_ISSUE = 12, W_JOIN = 13;
+constexpr int LOADERS = 4;
+// Registers a thread by role: together what 512 threads are launched with (128 each).
+constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
+static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
 // How far, as a power of 2, the maximum may grow before o is scaled to it; and what p is
 // multiplied by for f16, so that its range is used to the end (2^15.99 of 2^16), and p
 // keeps all bits down to 2^-21 of the largest, and 2^-33 of it in absolute terms below.
@@ -58,7 +59,7 @@ struct Plan {
 };
 
 // What the loaders know of a tile and the softmax needs.
-struct __align__(16) Meta {
+struct __align__(8) Meta {
   int edge;       // some row does not see some token; then:
   int x, last;    // the tile's first position, the last one that it holds
   uint32_t gone;  // 16-token groups whose page is not there
@@ -472,10 +473,10 @@ __device__ __forceinline__ void copy_queries(const KvNewArgs &a, const Walk &w, 
 
 // Values that are not finite meet p = 0 in rows that do not see their tokens, and 0
 // times them is NaN; so tiles that some row does not see in full hold 0 in their
-// place, and what they do to the rows that see them is done afterwards, here: half of a
-// row's result plus the value (an infinity, or NaN).  Rare, and out of the way.
+// place, and what they do to the rows that see them is done afterwards, here: a row's
+// result plus the value (an infinity, or NaN).  Rare, and out of the way.
 template <typename T, int D>
-__device__ __noinline__ void spoil(const KvNewArgs &a, const BadTile *bad, int n, int q0, int old, int h, int p, int d0, T *out,
+__device__ __noinline__ void spoil(const KvNewArgs &a, const BadTile *bad, int n, int q0, int old, int h, int p, T *out,
                                    float *part) {
   constexpr int C = Plan<D>::CHUNKS, STEP = 32 * LOADERS / C, IN_WARP = 32 / C;
   for (int k = 0; k < n; ++k)
@@ -483,8 +484,8 @@ __device__ __noinline__ void spoil(const KvNewArgs &a, const BadTile *bad, int n
       for (uint32_t m = bad[k].word[w]; m; m &= m - 1) {
         const int bit = __ffs(m) - 1, t = bad[k].x + bit / IN_WARP * STEP + w * IN_WARP + bit % IN_WARP, j = old + t;
         if (j > p || (a.window > 0 && j <= p - a.window && j >= a.sinks)) continue;
-        const T *v = static_cast<const T *>(a.v) + (long long)(q0 + t) * a.v_token + h * a.v_head + d0;
-        for (int d = 0; d < D / 2; ++d) {
+        const T *v = static_cast<const T *>(a.v) + (long long)(q0 + t) * a.v_token + h * a.v_head;
+        for (int d = 0; d < D; ++d) {
           const float x = to_f32(v[d]);
           if (fabsf(x) < CUDART_INF_F) continue;
           if (out) out[d] = from_f32<T>(to_f32(out[d]) + x);
@@ -494,16 +495,14 @@ __device__ __noinline__ void spoil(const KvNewArgs &a, const BadTile *bad, int n
 }
 
 // A barrier's phases are told apart by their parity alone: whoever waits for one knows
-// that the one before is complete, and none completes before the one before it was waited
-// for or need not be.  Those of the row tiles' scores and p's: BUFFERS each, in turn, since
-// so many may be ahead.
+// that the one before it is complete and that the next one cannot be.  Those of the row
+// tiles' scores and products: BUFFERS each, in turn, since so many may be ahead.
 enum Bar {
   FULL_AT = 0, EMPTY_AT = 8, Q_FULL = 16, Q_EMPTY = 17,
-  S_FULL = 18,        // [row tile][BUFFERS]
-  P_FULL = 24,        // [row tile][half][BUFFERS]
-  PV_HALF = 36,       // [row tile][BUFFERS]: the products with the first half's p are done
-  PV_DONE = 42,       // [row tile][BUFFERS]
-  O_EMPTY = 48, ROWS_MET = 50, SEGMENT_OVER = 52, BARS = SEGMENT_OVER + BAD_SEGMENTS
+  S_FULL = 18,             // [row tile][BUFFERS]
+  P_HALF = 24, P_FULL = 27,  // [buffer]: p of the first half of the tile's tokens, of the second
+  PV_HALF = 30, PV_DONE = 36,  // [row tile][BUFFERS]: the products with them are done
+  O_EMPTY = 42, SEGMENT_OVER = 44, BARS = SEGMENT_OVER + BAD_SEGMENTS
 };
 
 template <int REGS>
@@ -549,8 +548,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int bad_count[BAD_SEGMENTS];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
-  __shared__ float s_m[ROWS];       // what the rows' o is relative to
-  __shared__ float2 s_end[2][ROWS];  // of either half: m and l at a segment's end
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL, tid >> 5, 0);
   uint32_t bits = 0;
   const Share &share = share_of(a, reinterpret_cast<int *>(smem), &bits);
@@ -570,14 +567,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     bar_init(bar(Q_EMPTY), 1);
     for (int i = 0; i < 2 * L::BUFFERS; ++i) {
       bar_init(bar(S_FULL + i), 1);
-      bar_init(bar(P_FULL + i), 4);
-      bar_init(bar(P_FULL + 2 * L::BUFFERS + i), 4);
       bar_init(bar(PV_HALF + i), 1);
       bar_init(bar(PV_DONE + i), 1);
     }
+    for (int i = 0; i < L::BUFFERS; ++i) {
+      bar_init(bar(P_HALF + i), 4);
+      bar_init(bar(P_FULL + i), 4);
+    }
     for (int i = 0; i < 2; ++i) {
-      bar_init(bar(O_EMPTY + i), 8);
-      bar_init(bar(ROWS_MET + i), 8);
+      bar_init(bar(O_EMPTY + i), 4);
     }
     for (int i = 0; i < BAD_SEGMENTS; ++i) bar_init(bar(SEGMENT_OVER + i), W_LOAD);
     bar_init_fence();
@@ -608,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp >= W_LOAD && warp < W_LOAD + LOADERS) {
-    fewer_registers<REGS_LOAD>();
+    fewer_registers<REGS_OTHER>();
     const int me = tid - 32 * W_LOAD, wl = warp - W_LOAD;
     constexpr int CHUNKS8 = D / 16, PER = TILE * CHUNKS8 / (32 * LOADERS);  // 16-byte chunks of e4m3: of a token, of a thread
     constexpr int STEP = 32 * LOADERS / CHUNKS8;
@@ -808,39 +806,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
   } else if (warp >= W_ISSUE) {
-    fewer_registers<REGS_ISSUE>();
-    if (warp == W_ISSUE && lane == 0) {
-      // the unit that this share ends within, if it begins here: how many shares hold it
-      Join join{0, 0, 0, 0, 0};
-      if (share.end.t > 0 && (share.end.u > share.begin.u || (share.begin.t == 0 && !share.begin.past))) {
-        const BatchRow r = batch_row(a, share.end.b, &bits);
-        const Unit u = unit_of(a, r, share.end.i);
-        join.parts = 2;
-        for (int g = blockIdx.x + 2; g < share.ctas; ++g) {
-          const long long into = share.all * g / share.ctas - share.u_at;
-          if (into >= OVERHEAD + share.end_tiles) break;
-          Cut c;
-          place_cut(c, into, share.end_tiles);
-          if (c.past) break;
-          ++join.parts;
-        }
-        join.q0 = r.q0;
-        join.r0 = u.r0;
-        join.nrows = u.nrows;
-        join.h = share.end.h;
-      }
-      *join_of(a, blockIdx.x) = join;
-    }
-    __syncwarp();
+    fewer_registers<REGS_OTHER>();
     if (warp == W_ISSUE) {
       // The whole warp walks, so that addresses and counters are the warp's (in its
       // uniform registers, where the products take them from); one thread issues.
       constexpr uint32_t QK = product16(BF16, TILE, false), PV = product16(BF16, D, true), HIGH = operand_high(1024);
       Walk w(a, share);
       uint32_t item = 0, segments = 0, segs1 = 0;
-      uint32_t s_buf = 0, p_buf = 0;    // of the products in turn: the buffer
-      uint32_t s_bar0 = 0, s_bar1 = 0;  // of either row tile: the barrier of its next scores, that of its next p,
-      uint32_t p_bar0 = 0, p_bar1 = 0, p_use0 = 0, p_use1 = 0;  // and how often that was used before
+      uint32_t s_buf = 0, p_buf = 0, p_use = 0;  // of the products in turn: the buffer, and how often it was used before
+      uint32_t s_bar0 = 0, s_bar1 = 0, p_bar0 = 0, p_bar1 = 0;  // of either row tile: the barriers of its next scores, its next p
       bool ok = true;
       auto wait_all = [&](int which, uint32_t parity) {
         const uint32_t b = bar(which);
@@ -856,7 +830,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_ss(tmem + L::S + s_buf * TILE, q + off, k + off, HIGH, QK, e > 0);
         }
       };
-      // half of the tile's tokens at a time, as their p comes from two warpgroups
+      // half of the tile's tokens at a time: the first products run while the second half of p is made
       auto pv = [&](int i, uint32_t slot, int half, bool add) {
         const uint32_t v = v_low + slot * (L::HALF / 16) + half * (64 * 128 / 16), p = tmem + L::S + p_buf * TILE + half * 32,
                        o = tmem + L::O + i * D;
@@ -892,8 +866,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int i = x & two, j = x >> two;
           const uint32_t vi = item + 2 * j + 1, vs = vi % STAGES;
           if (i == 0) ok = wait_all(FULL_AT + vs, vi / STAGES);
-          const uint32_t p_bar = i ? p_bar1 : p_bar0, p_use = i ? p_use1 : p_use0;
-          ok = ok && wait_all(P_FULL + 2 * i * L::BUFFERS + p_bar, p_use);
+          ok = ok && wait_all(P_HALF + p_buf, p_use);
           if (ok && j == 0) {
             const uint32_t before = i ? segs1 : segments;
             if (before > 0) ok = wait_all(O_EMPTY + i, before - 1);
@@ -902,23 +875,23 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_after_sync();
           if (elect_one()) {
             pv(i, vs, 0, j > 0);
-            mma_commit(bar(PV_HALF + i * L::BUFFERS + p_bar));
+            mma_commit(bar(PV_HALF + (i ? L::BUFFERS + p_bar1 : p_bar0)));
           }
           __syncwarp();
-          ok = wait_all(P_FULL + (2 * i + 1) * L::BUFFERS + p_bar, p_use);
+          ok = wait_all(P_FULL + p_buf, p_use);
           if (!ok) break;
           tmem_after_sync();
           if (elect_one()) {
             pv(i, vs, 1, true);
-            mma_commit(bar(PV_DONE + i * L::BUFFERS + p_bar));
+            mma_commit(bar(PV_DONE + (i ? L::BUFFERS + p_bar1 : p_bar0)));
             if (i == two) mma_commit(bar(EMPTY_AT + vs));
           }
           __syncwarp();
-          if (++p_buf == L::BUFFERS) p_buf = 0;
-          uint32_t &next = i ? p_bar1 : p_bar0;
-          if (++next == L::BUFFERS) {
-            next = 0;
-            ++(i ? p_use1 : p_use0);
+          uint32_t &p_bar = i ? p_bar1 : p_bar0;
+          if (++p_bar == L::BUFFERS) p_bar = 0;
+          if (++p_buf == L::BUFFERS) {
+            p_buf = 0;
+            ++p_use;
           }
           if (x + L::BUFFERS < all) issue_qk(x + L::BUFFERS);
         }
@@ -926,16 +899,32 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++segments;
         segs1 += two;
       }
+    } else if (warp == W_JOIN && lane == 0) {
+      // the unit that this share ends within, if it begins here: how many shares hold it
+      Join join{0, 0, 0, 0, 0};
+      if (share.end.t > 0 && (share.end.u > share.begin.u || (share.begin.t == 0 && !share.begin.past))) {
+        const BatchRow r = batch_row(a, share.end.b, &bits);
+        const Unit u = unit_of(a, r, share.end.i);
+        join.parts = 2;
+        for (int g = blockIdx.x + 2; g < share.ctas; ++g) {
+          const long long into = share.all * g / share.ctas - share.u_at;
+          if (into >= OVERHEAD + share.end_tiles) break;
+          Cut c;
+          place_cut(c, into, share.end_tiles);
+          if (c.past) break;
+          ++join.parts;
+        }
+        join.q0 = r.q0;
+        join.r0 = u.r0;
+        join.nrows = u.nrows;
+        join.h = share.end.h;
+      }
+      *join_of(a, blockIdx.x) = join;
     }
     __syncwarp();
   } else {
     more_registers<REGS_SOFTMAX>();
-    // Two threads have a row, half of a tile's tokens each: they share m (what o and p are
-    // relative to) and keep their own l.  Their warps finish their halves in turn, the
-    // first half of a tile, the second, the first of the next: so each knows m as the one
-    // before left it, and may change it, while the exponentials of both run side by side.
-    const int i = warp >> 3, half = warp >> 2 & 1;        // the warp's row tile, its half
-    const int r = (warp & 3) * 32 + lane, R = i * M + r;  // the thread's row of it, of the unit
+    const int i = warp >> 2, r = tid & 127, R = i * M + r;  // the warpgroup's row tile, the thread's row of it, of the unit
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t o_at = tmem + lanes + L::O + i * D;
     const float c0 = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);
@@ -943,25 +932,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     // tells that the maximum has grown by 2^THRESHOLD.  f16: its range is used to the end.
     constexpr float UP = BF16 ? 1.f - THRESHOLD : 15.99f - THRESHOLD;
     Walk w(a, share);
-    uint32_t g = 0, segments = 0, met = 0;
-    uint32_t buf = 0;             // of the next segment's first scores
-    uint32_t turn = 0, use = 0;   // of the row tile's next scores: their barriers, and how often those were used before
+    uint32_t g = 0, segments = 0;
+    uint32_t buf = 0;            // of the next segment's first scores
+    uint32_t turn = 0, use = 0;  // of the row tile's next scores: their barriers, and how often those were used before
     bool ok = true;
     while (ok && w.next(&bits)) {
       const int tiles = w.t1 - w.t0, two = w.unit.nrows > M;
       const int t = (w.unit.r0 + R) / a.group, p = w.row.old + t;
-      T *out = static_cast<T *>(a.out) +
-               ((long long)(w.row.q0 + t) * a.q_heads + w.h * a.group + (w.unit.r0 + R) % a.group) * D + half * (D / 2);
+      T *out = static_cast<T *>(a.out) + ((long long)(w.row.q0 + t) * a.q_heads + w.h * a.group + (w.unit.r0 + R) % a.group) * D;
       if (tiles == 0) {
         if (R < w.unit.nrows)
-          for (int d = 0; d < D / 2; d += 8) *reinterpret_cast<uint4 *>(out + d) = make_uint4(0, 0, 0, 0);
+          for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(out + d) = make_uint4(0, 0, 0, 0);
         continue;
       }
       uint32_t s_buf = (buf + i) % L::BUFFERS;
       buf = (buf + ((uint32_t)tiles << two)) % L::BUFFERS;
       if (i > two) {
-        // (no rows here.  Not further ahead than the phase before, or this warp would
-        // arrive in another's place)
+        // (no rows here.  Not further ahead than the phase before, or this warpgroup would
+        // arrive in the other's place)
         if (segments >= BAD_SEGMENTS) ok = wait(SEGMENT_OVER + segments % BAD_SEGMENTS, segments / BAD_SEGMENTS - 1);
         ok = __all_sync(FULL, ok);
         if (!ok) break;
@@ -971,18 +959,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         continue;
       }
       const bool live = R < w.unit.nrows;
-      float m = live ? -CUDART_INF_F : 0.f, l = 0.f;
+      float m = live ? -CUDART_INF_F : 0.f, l = 0.f;  // (what rows that are not there hold does not matter)
       uint32_t turn_before = 0, use_before = 0;
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j, ++g) {
         ok = wait(S_FULL + i * L::BUFFERS + turn, use);
-        if (!__all_sync(FULL, ok)) break;
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
         tmem_after_sync();
         const uint32_t s_at = tmem + lanes + L::S + s_buf * TILE;
+        uint32_t sa[32], sb[32], pk[32];
+        if (j > 0) tmem_ld32(s_at, sa);
         const Meta &mt = meta[g % META];
         const int edge = mt.edge;
         // z = s c; m is kept relative to z + log2 V, V the scale that the tile's values were brought to
         const float c = BF16 ? c0 : fmaxf(c0 * mt.k, 1e-37f), lv = BF16 ? 0.f : __log2f(mt.v);
+        const uint64_t c2 = pair64(c, c), one = pair64(1.f, 1.f);
         // -inf in place of what the row does not see, of 32 tokens from e0 on
         auto mask = [&](uint32_t (&s)[32], int e0) {
           const int x = mt.x + e0;
@@ -995,128 +987,108 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 32; ++e)
             if (!(see >> e & 1)) s[e] = 0xff800000u;
         };
-        uint32_t pk[32];
-        bool first = j == 0 && half == 0;  // (of a segment: there is no m yet)
-        bool turn_came = first;
-        auto wait_turn = [&]() {
-          turn_came = true;
-          if (half == 0) ok = wait(P_FULL + (2 * i + 1) * L::BUFFERS + turn_before, use_before);
-          else ok = wait(P_FULL + 2 * i * L::BUFFERS + turn, use);
-          ok = __all_sync(FULL, ok);
-          return s_m[R];
-        };
-        if (j == 0 && half > 0) m = wait_turn();
-        while (ok) {
+        // Half of the tokens at a time, so that the products with the first run beside the
+        // exponentials of the second.  (Loops rather than straight code: what 16 warps in
+        // three roles run has to stay in the instruction cache.)
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          bool first = j + half == 0;  // (of a segment: there is no m yet)
           uint64_t sum = 0;
-          float top = -CUDART_INF_F;
-          bool grown = first;
-          if (!first) {
-            const float base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
-            const uint64_t c2 = pair64(c, c), b2 = pair64(-base, -base), one = pair64(1.f, 1.f);
-            uint64_t sum0 = 0, sum1 = 0;
-            uint32_t high = 0;
-            float top0 = -CUDART_INF_F, top1 = -CUDART_INF_F;
-            auto exps = [&](uint32_t (&s)[32], uint32_t *to) {
+          while (true) {
+            bool grown = first;
+            if (!first) {
+              const float base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
+              const uint64_t b2 = pair64(-base, -base);
+              uint64_t sum0 = 0, sum1 = 0;
+              uint32_t high = 0;
+              float top0 = -CUDART_INF_F, top1 = -CUDART_INF_F;
+              // 32 tokens' p relative to m as it is, and their sum
+              auto exps = [&](const uint32_t (&s)[32], uint32_t *to) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                float y[4];
-                if (!BF16) {
-                  top0 = max3(top0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                  top1 = max3(top1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                for (int e = 0; e < 32; e += 4) {
+                  float y[4];
+                  if (!BF16) {
+                    top0 = max3(top0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    top1 = max3(top1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                  }
+                  unpair(fma2(pair64(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), y[0], y[1]);
+                  unpair(fma2(pair64(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), y[2], y[3]);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) y[q] = ex2_approx(y[q]);
+                  sum0 = fma2(pair64(y[0], y[1]), one, sum0);
+                  sum1 = fma2(pair64(y[2], y[3]), one, sum1);
+                  to[e / 2] = pack2<T>(y[0], y[1]);
+                  to[e / 2 + 1] = pack2<T>(y[2], y[3]);
+                  if (BF16) high |= to[e / 2] | to[e / 2 + 1];
                 }
-                unpair(fma2(pair64(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), y[0], y[1]);
-                unpair(fma2(pair64(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), y[2], y[3]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) y[q] = ex2_approx(y[q]);
-                sum0 = fma2(pair64(y[0], y[1]), one, sum0);
-                sum1 = fma2(pair64(y[2], y[3]), one, sum1);
-                to[e / 2] = pack2<T>(y[0], y[1]);
-                to[e / 2 + 1] = pack2<T>(y[2], y[3]);
-                if (BF16) high |= to[e / 2] | to[e / 2 + 1];
-              }
-            };
-            uint32_t sa[32], sb[32];
-            tmem_ld32(s_at + half * 64, sa);
-            tmem_wait_ld();
-            tmem_ld32(s_at + half * 64 + 32, sb);
-            if (edge) mask(sa, half * 64);
-            exps(sa, pk);
-            tmem_wait_ld();
-            if (edge) mask(sb, half * 64 + 32);
-            exps(sb, pk + 16);
-            sum = fma2(sum0, one, sum1);
-            if (BF16) {
-              grown = live && ((high & 0x40004000u) != 0 || m == -CUDART_INF_F);
-            } else {
-              top = fmaf(fmaxf(top0, top1), c, lv);
-              grown = live && (top > m + THRESHOLD || (m == -CUDART_INF_F && top > m));
-            }
-          }
-          if (!turn_came) {
-            const float now = wait_turn();
-            if (__any_sync(FULL, !ok || now != m)) {
-              l *= now != m ? ex2_approx(m - now) : 1.f;  // (m grows, and l is 0 where it was -inf)
-              m = now;
-              continue;
-            }
-          }
-          if (!__any_sync(FULL, grown)) {
-            float u0, u1;
-            unpair(sum, u0, u1);
-            l = BF16 ? l + (u0 + u1) : fmaf(u0 + u1, __fdividef(1.f, mt.v), l);
-            break;
-          }
-          // The maximum may have grown too far for p to be relative to the old one (rarely but
-          // for a segment's first): o and l are scaled to it, and p is made anew.
-          float largest = -CUDART_INF_F;
-#pragma unroll 1
-          for (int e0 = half * 64; e0 < half * 64 + 64; e0 += 32) {
-            uint32_t s[32];
-            tmem_ld32(s_at + e0, s);
-            tmem_wait_ld();
-            if (edge) mask(s, e0);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) largest = max3(largest, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-          }
-          top = fmaf(largest, c, lv);
-          const bool up = live && (top > m + (THRESHOLD - 1.f) || (m == -CUDART_INF_F && top > m));
-          if (!first && !__any_sync(FULL, up)) {  // (NaN, or nothing seen so far)
-            float u0, u1;
-            unpair(sum, u0, u1);
-            l = BF16 ? l + (u0 + u1) : fmaf(u0 + u1, __fdividef(1.f, mt.v), l);
-            break;
-          }
-          float o_scale = 1.f;
-          if (up) {
-            o_scale = m == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
-            l *= o_scale;
-            m = top;
-          }
-          if (j > 0 || half > 0) {
-            if (j > 0) ok = wait(PV_DONE + i * L::BUFFERS + turn_before, use_before);
-            if (half > 0) ok = ok && wait(PV_HALF + i * L::BUFFERS + turn, use);
-            ok = __all_sync(FULL, ok);
-            if (!ok) break;
-            tmem_after_sync();
-#pragma unroll 1
-            for (int d = 0; d < D; d += 16) {
-              uint32_t o[16];
-              tmem_ld16(o_at + d, o);
+              };
               tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * o_scale);
-              tmem_st16(o_at + d, o);
+              tmem_ld32(s_at + half * 64 + 32, sb);
+              if (edge) mask(sa, half * 64);
+              exps(sa, pk);
+              tmem_wait_ld();
+              if (half == 0) tmem_ld32(s_at + 64, sa);
+              if (edge) mask(sb, half * 64 + 32);
+              exps(sb, pk + 16);
+              sum = fma2(sum0, one, sum1);
+              if (BF16) {
+                grown = live && ((high & 0x40004000u) != 0 || m == -CUDART_INF_F);
+              } else {
+                const float top = fmaf(fmaxf(top0, top1), c, lv);
+                grown = live && (top > m + THRESHOLD || (m == -CUDART_INF_F && top > m));
+              }
             }
-            tmem_wait_st();
+            if (!__any_sync(FULL, grown)) break;
+            // The maximum may have grown too far for p to be relative to the old one (rarely but
+            // for a segment's first half): o and l are scaled to it, and p is made anew.
+            tmem_wait_ld();
+            float largest = -CUDART_INF_F;
+#pragma unroll 1
+            for (int e0 = half * 64 + 32; e0 >= half * 64; e0 -= 32) {
+              tmem_ld32(s_at + e0, sb);
+              tmem_wait_ld();
+              if (edge) mask(sb, e0);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) largest = max3(largest, __uint_as_float(sb[e]), __uint_as_float(sb[e + 1]));
+            }
+            const float top = fmaf(largest, c, lv);
+            const bool up = live && (top > m + (THRESHOLD - 1.f) || (m == -CUDART_INF_F && top > m));
+            if (!first && !__any_sync(FULL, up)) break;  // (NaN, or nothing seen so far)
+            float o_scale = 1.f;
+            if (up) {
+              o_scale = m == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
+              l *= o_scale;
+              m = top;
+            }
+            if (!first) {
+              if (j > 0) ok = wait(PV_DONE + i * L::BUFFERS + turn_before, use_before);
+              if (half > 0) ok = ok && wait(PV_HALF + i * L::BUFFERS + turn, use);
+              ok = __all_sync(FULL, ok);
+              if (!ok) break;
+              tmem_after_sync();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 16) {
+                tmem_ld16(o_at + d, sa);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sa[e] = __float_as_uint(__uint_as_float(sa[e]) * o_scale);
+                tmem_st16(o_at + d, sa);
+              }
+              tmem_wait_st();
+            }
+            first = false;
+            tmem_ld32(s_at + half * 64, sa);
           }
-          s_m[R] = m;
-          first = false;
+          if (!ok) break;
+          float u0, u1;
+          unpair(sum, u0, u1);
+          l = BF16 ? l + (u0 + u1) : fmaf(u0 + u1, __fdividef(1.f, mt.v), l);
+          tmem_st32(s_at + half * 32, pk);
+          tmem_wait_st();
+          tmem_before_sync();
+          warp_arrive((half ? P_FULL : P_HALF) + s_buf);
         }
         if (!ok) break;
-        tmem_st32(s_at + half * 32, pk);
-        tmem_wait_st();
-        tmem_before_sync();
-        warp_arrive(P_FULL + (2 * i + half) * L::BUFFERS + turn);
         if ((s_buf += 1 + two) >= L::BUFFERS) s_buf -= L::BUFFERS;
         turn_before = turn;
         use_before = use;
@@ -1126,63 +1098,52 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) break;
-      // ---- the segment's result: half of the dims each
-      s_end[half][R] = make_float2(m, l);
-      warp_arrive(ROWS_MET + i);
-      ok = wait(ROWS_MET + i, met++) && wait(PV_DONE + i * L::BUFFERS + turn_before, use_before);
+      // ---- the segment's result
+      ok = wait(PV_DONE + i * L::BUFFERS + turn_before, use_before);
       ok = __all_sync(FULL, ok);
       if (!ok) break;
-      {
-        const float2 x = s_end[0][R];
-        m = s_end[1][R].x;
-        l = s_end[1][R].y + (x.y == 0.f ? 0.f : x.y * ex2_approx(x.x - m));
-      }
-      {
-        tmem_after_sync();
-        const bool whole = w.whole();
-        const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-        float *part = new_part<D>(a, slot) + half * (D / 8) * (ROWS * 4) + R * 4;
-        const float inv = 1.f / l;  // (a row sees itself: l is 0 only where its scores are all -inf, and then the result is NaN)
+      tmem_after_sync();
+      const bool whole = w.whole();
+      const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+      float *part = new_part<D>(a, slot) + R * 4;
+      const float inv = 1.f / l;  // (a row sees itself: 0 only where its scores are all -inf, and then the result is NaN)
 #pragma unroll 1
-        for (int d = 0; d < D / 2; d += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_at + half * (D / 2) + d, o);
-          tmem_wait_ld();
-          if (R >= w.unit.nrows) continue;
-          if (whole) {
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_at + d, o);
+        tmem_wait_ld();
+        if (R >= w.unit.nrows) continue;
+        if (whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float v[8];
+          for (int e = 0; e < 4; ++e) {
+            float v[8];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(o[8 * e + q]) * inv;
-              reinterpret_cast<uint4 *>(out + d)[e] =
-                  make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4 *>(part + (d / 4 + e) * (ROWS * 4)) =
-                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(o[8 * e + q]) * inv;
+            reinterpret_cast<uint4 *>(out + d)[e] =
+                make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4 *>(part + (d / 4 + e) * (ROWS * 4)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
-        tmem_before_sync();
-        warp_arrive(O_EMPTY + i);
-        if (R < w.unit.nrows) {
-          if (!whole && half == 0) {
-            float *ml = new_part<D>(a, slot) + ROWS * D + R;
-            ml[0] = m;
-            ml[ROWS] = l;
-          }
-          const int n = bad_count[segments % BAD_SEGMENTS];
-          uint32_t any = 0;
-          for (int k = 0; k < n; ++k)
-            for (int q = 0; q < LOADERS; ++q) any |= bad_tiles[segments % BAD_SEGMENTS][k].word[q];
-          if (any)
-            spoil<T, D>(a, bad_tiles[segments % BAD_SEGMENTS], n, w.row.q0, w.row.old, w.h, p, half * (D / 2), whole ? out : nullptr,
-                        part);
-        }
-        warp_arrive(SEGMENT_OVER + segments % BAD_SEGMENTS);
       }
+      tmem_before_sync();
+      warp_arrive(O_EMPTY + i);
+      if (R < w.unit.nrows) {
+        if (!whole) {
+          float *ml = new_part<D>(a, slot) + ROWS * D + R;
+          ml[0] = m;
+          ml[ROWS] = l;
+        }
+        const int n = bad_count[segments % BAD_SEGMENTS];
+        uint32_t any = 0;
+        for (int k = 0; k < n; ++k)
+          for (int q = 0; q < LOADERS; ++q) any |= bad_tiles[segments % BAD_SEGMENTS][k].word[q];
+        if (any)
+          spoil<T, D>(a, bad_tiles[segments % BAD_SEGMENTS], n, w.row.q0, w.row.old, w.h, p, whole ? out : nullptr, part);
+      }
+      warp_arrive(SEGMENT_OVER + segments % BAD_SEGMENTS);
       ++segments;
     }
   }
