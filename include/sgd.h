@@ -672,7 +672,8 @@ typedef struct {
  * the end of the list, in that order too, and a row whose pages, with those wanted
  * by the rows before it, are more than there are gets neither pages nor tokens.
  * All such rows are reported (SGD_KV_ERR_LENGTH, SGD_KV_ERR_ROOM).
- *   keep, fresh DEVICE int32 [B] (B <= SGD_KV_ASSIGN_MAX_ROWS, else SGD_ETOOLARGE).
+ *   keep, fresh DEVICE int32 [B] (B <= SGD_KV_ASSIGN_MAX_ROWS and N <= 2^30, else
+ *            SGD_ETOOLARGE).
  *   seq_lens DEVICE int32 [B]: keep + what it got of fresh (a row that makes no
  *            sense: 0); q_start DEVICE int32 [B + 1].  seq_lens may be keep or fresh.
  *   positions, slots, rows DEVICE int32 [N] or null: of each packed token its

@@ -281,7 +281,7 @@ int sgd_kv_assign(sgd_kv *x, const sgd_kv_pages *pages, const int32_t *keep, con
                   int32_t *row_ids, void *stream) {
   if (!x || !pages) return SGD_EINVAL;
   if (B < 0 || B > x->cfg.max_batch || N < 0) return SGD_EINVAL;
-  if (B > SGD_KV_ASSIGN_MAX_ROWS) return SGD_ETOOLARGE;
+  if (B > SGD_KV_ASSIGN_MAX_ROWS || N > 1 << 30) return SGD_ETOOLARGE;
   if (!pages->block_table || !pages->held || !pages->free || !pages->free_count || !q_start) return SGD_EINVAL;
   if (B > 0 && (!keep || !fresh || !seq_lens)) return SGD_EINVAL;
   KvAssignArgs a{};
@@ -304,8 +304,10 @@ int sgd_kv_assign(sgd_kv *x, const sgd_kv_pages *pages, const int32_t *keep, con
   a.err = x->d_err;
   const DeviceScope on(x->device);
   if (!on.ok()) return SGD_ECUDA;
-  x->launches++;
-  return check_cuda(launch_kv_assign(a, (cudaStream_t)stream));
+  int launches = 0;
+  const cudaError_t e = launch_kv_assign(a, (cudaStream_t)stream, &launches);
+  x->launches += launches;
+  return check_cuda(e);
 }
 
 int sgd_kv_get_error(sgd_kv *x, uint32_t *flags, int clear) {

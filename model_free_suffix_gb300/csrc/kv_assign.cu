@@ -7,10 +7,11 @@
 // it is prefix sums over the rows (new tokens, pages back, pages wanted), so the
 // result does not depend on the order in which threads run.
 //
-// One cluster: every CTA computes all the sums (rows are few: 16 bytes each) and
-// keeps the rows' places in shared memory, then takes its share of the rows'
+// One cluster of eight CTAs, every one of which computes all the sums (rows are few: 12
+// bytes each), keeps the rows' places in shared memory and takes its share of the rows'
 // pages and of the tokens.  Two cluster barriers: nothing is written before all
 // CTAs have read the state, nothing taken before all given pages are on the list.
+// Many tokens (prompts) get a second kernel, of as many CTAs as they fill.
 #include <cooperative_groups.h>
 
 #include "kv_internal.h"
@@ -21,11 +22,13 @@ namespace cg = cooperative_groups;
 namespace sgd {
 namespace {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int CTAS = 8;            // of the cluster
+// Tokens that the cluster places itself.  ASSIGN_NOTE
+constexpr int OWN_TOKENS = 32768;
 
 struct Row {
-  int keep, held, need;  // tokens that stay; pages before and after
-  int fresh;             // new tokens
+  int keep, held, fresh;  // tokens that stay, pages so far, new tokens
   bool good;
 };
 
@@ -56,13 +59,13 @@ __device__ __forceinline__ long long block_scan(long long x, long long *s, long 
   __syncthreads();  // (the sums of the scan before have been read)
   if (lane == 31) s[warp] = scan;
   __syncthreads();
-  long long w = s[lane];
+  long long w = lane < WARPS ? s[lane] : 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < WARPS; o <<= 1) {
     const long long t = __shfl_up_sync(FULL, w, o);
     if (lane >= o) w += t;
   }
-  *total = __shfl_sync(FULL, w, 31);
+  *total = __shfl_sync(FULL, w, WARPS - 1);
   const long long before = __shfl_sync(FULL, w, max(warp - 1, 0));
   return scan - x + (warp ? before : 0);
 }
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(THREADS, 1) assign_kernel(KvAssignArgs a) {
   int *s_start = s_rows;               // [B + 1] first packed token
   int *s_keep = s_start + a.B + 1;     // [B]
   int *s_held = s_keep + a.B;          // [B] pages before
-  int *s_need = s_held + a.B;          // [B] pages after (-1 - held: a row passed over)
+  int *s_need = s_held + a.B;          // [B] pages after (-1: a row passed over)
   int *s_place = s_need + a.B;         // [B] pages before its own: of those given back, or of those taken
   __shared__ long long s_sum[32];
   cg::cluster_group cluster = cg::this_cluster();
@@ -89,27 +92,32 @@ __global__ void __launch_bounds__(THREADS, 1) assign_kernel(KvAssignArgs a) {
   // what fits the packed tokens
   long long total, mine = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += row_of(a, b).fresh;
+  for (int b = b0; b < b1; ++b) {
+    const Row r = row_of(a, b);
+    s_keep[b] = r.keep;
+    s_held[b] = r.held;
+    s_need[b] = r.good ? 0 : -1;
+    s_start[b] = r.fresh;
+    mine += r.fresh;
+    if (!r.good) bits |= SGD_KV_ERR_LENGTH;
+  }
   long long at = block_scan(mine, s_sum, &total);
   const bool packed = total <= a.N;
   // pages back, pages wanted
   long long back = 0, want = 0;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    Row r = row_of(a, b);
-    if (!r.good) bits |= SGD_KV_ERR_LENGTH;
-    at += r.fresh;
-    if (!packed && r.fresh > 0 && at > a.N) {
-      r.fresh = 0;
+    if (s_need[b] < 0) continue;
+    const int fresh = s_start[b];
+    at += fresh;
+    if (!packed && fresh > 0 && at > a.N) {
+      s_start[b] = 0;
       bits |= SGD_KV_ERR_ROOM;
     }
-    r.need = r.good ? pages_of(a, r.keep + r.fresh) : r.held;
-    s_keep[b] = r.keep;
-    s_held[b] = r.held;
-    s_need[b] = r.good ? r.need : -1;
-    s_start[b] = r.fresh;
-    if (r.need < r.held) back += r.held - r.need;
-    else want += r.need - r.held;
+    const int need = pages_of(a, s_keep[b] + s_start[b]), held = s_held[b];
+    s_need[b] = need;
+    if (need < held) back += held - need;
+    else want += need - held;
   }
   long long back_total, want_total;
   long long back_at = block_scan(back, s_sum, &back_total);
@@ -187,6 +195,10 @@ __global__ void __launch_bounds__(THREADS, 1) assign_kernel(KvAssignArgs a) {
       if (page < 0 || page >= a.num_pages) bits |= SGD_KV_ERR_PAGE;
       a.table[(long long)b * a.max_pages + j] = page;
     }
+  if (a.N > OWN_TOKENS) {
+    if (bits) atomicOr(a.err, bits);
+    return;
+  }
   // the packed tokens
 #pragma unroll 1
   for (int i = cta * THREADS + tid; i < a.N; i += ctas * THREADS) {
@@ -214,6 +226,91 @@ __global__ void __launch_bounds__(THREADS, 1) assign_kernel(KvAssignArgs a) {
   if (bits) atomicOr(a.err, bits);
 }
 
+// The places of many packed tokens, after assign_kernel: a thread's four in a row, the
+// row found for the first of them.
+constexpr int PLACE_THREADS = 256, PLACE_TOKENS = 4 * PLACE_THREADS;
+__global__ void __launch_bounds__(PLACE_THREADS) place_kernel(KvAssignArgs a) {
+  __shared__ int s_row;  // that of the block's first token
+  const int first = blockIdx.x * PLACE_TOKENS, total = __ldg(a.q_start + a.B);
+  const int tid = threadIdx.x;
+  // (a warp's lanes look at 32 starts at a time)
+  if (tid < 32) {
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + tid * step;
+      const uint32_t below = __ballot_sync(FULL, at < hi && __ldg(a.q_start + at) <= first);
+      const int last = 31 - __clz(below | 1);
+      const int from = lo + last * step;
+      hi = min(hi, from + step);
+      lo = from;
+    }
+    if (tid == 0) s_row = lo;
+  }
+  __syncthreads();
+  int i = first + tid * 4, row = s_row;
+  if (i >= a.N) return;
+  if (i < total) {
+    int hi = a.B;
+    // (far from the block's first row only where rows are short: doubling steps, then halving)
+    int step = 1;
+    while (row + step < hi && __ldg(a.q_start + row + step) <= i) {
+      row += step;
+      step <<= 1;
+    }
+    hi = min(hi, row + step);
+    while (hi - row > 1) {
+      const int mid = (row + hi) >> 1;
+      if (__ldg(a.q_start + mid) <= i) row = mid;
+      else hi = mid;
+    }
+  }
+  int rows[4], positions[4], slots[4];
+  uint32_t bits = 0;
+  int start = 0, end = 0, keep = 0, at = -1, page = -1;
+  if (i < total) {
+    start = __ldg(a.q_start + row);
+    end = __ldg(a.q_start + row + 1);
+    keep = a.seq_lens[row] - (end - start);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e, ++i) {
+    rows[e] = slots[e] = -1;
+    positions[e] = 0;
+    if (i >= total) continue;
+    while (i >= end) {
+      start = end;
+      end = __ldg(a.q_start + ++row + 1);
+      keep = a.seq_lens[row] - (end - start);
+      at = -1;
+    }
+    rows[e] = row;
+    positions[e] = keep + i - start;
+    if (at != positions[e] >> a.page_bits) {
+      at = positions[e] >> a.page_bits;
+      page = __ldg(a.table + (long long)row * a.max_pages + at);
+    }
+    if (page < 0 || page >= a.num_pages) bits |= SGD_KV_ERR_PAGE;
+    else slots[e] = (page << a.page_bits) + (positions[e] & ((1 << a.page_bits) - 1));
+  }
+  i -= 4;
+  auto put = [&](int32_t *to, const int (&x)[4]) {
+    if (!to) return;
+    if (i + 4 <= a.N && ((uintptr_t)to & 15) == 0) {
+      *reinterpret_cast<int4 *>(to + i) = make_int4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < a.N) to[i + e] = x[e];
+    }
+  };
+  put(a.rows, rows);
+  put(a.positions, positions);
+  if (a.slots) {
+    put(a.slots, slots);
+    if (bits) atomicOr(a.err, bits);
+  }
+}
+
 constexpr size_t smem_bytes(int B) { return ((size_t)B * 5 + 1) * sizeof(int); }
 
 }  // namespace
@@ -223,18 +320,23 @@ cudaError_t kv_assign_set_limits() {
                               (int)smem_bytes(SGD_KV_ASSIGN_MAX_ROWS));
 }
 
-cudaError_t launch_kv_assign(const KvAssignArgs &a, cudaStream_t st) {
+cudaError_t launch_kv_assign(const KvAssignArgs &a, cudaStream_t st, int *launches) {
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {1, 1, 1};
-  c.gridDim = {1, 1, 1};
+  at[0].val.clusterDim = {CTAS, 1, 1};
+  c.gridDim = {CTAS, 1, 1};
   c.blockDim = {THREADS, 1, 1};
   c.dynamicSmemBytes = smem_bytes(a.B);
   c.stream = st;
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, assign_kernel, a);
+  *launches = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, assign_kernel, a);
+  if (e != cudaSuccess || a.N <= OWN_TOKENS || !(a.positions || a.slots || a.rows)) return e;
+  *launches = 2;
+  place_kernel<<<(unsigned)(((long long)a.N + PLACE_TOKENS - 1) / PLACE_TOKENS), PLACE_THREADS, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace sgd

@@ -96,7 +96,7 @@ size_t kv_new_workspace(int sms);
 cudaError_t kv_new_set_limits();
 cudaError_t launch_kv_new(const KvNewArgs &a, int dtype, cudaStream_t st, int *launches);
 cudaError_t kv_assign_set_limits();
-cudaError_t launch_kv_assign(const KvAssignArgs &a, cudaStream_t st);
+cudaError_t launch_kv_assign(const KvAssignArgs &a, cudaStream_t st, int *launches);
 
 #ifdef __CUDACC__
 // Two e4m3 bytes (the low 16 bits) as two f16: exact, every e4m3 value is one.

@@ -84,7 +84,7 @@ def test_chunk_refuses(lib, handle):
 def test_assign_refuses(lib, handle):
     from model_free_suffix_gb300 import _lib as L
     assert _assign(lib, handle) == L.SGD_OK
-    assert b"launch_kv_assign@0" in lib.fake_seen().replace(b"ERKNS_12KvAssignArgsEP11CUstream_st", b"")
+    assert b"launch_kv_assign" in lib.fake_seen()
     for bad in (dict(table=None), dict(held=None), dict(free=None), dict(count=None), dict(keep=None), dict(new=None),
                 dict(lens=None), dict(starts=None), dict(B=-1), dict(B=9001), dict(N=-1)):
         assert _assign(lib, handle, **bad) == L.SGD_EINVAL, bad
@@ -98,6 +98,14 @@ def test_more_rows_than_a_call_takes(lib, handle):
     for call in (_prompt, _chunk, _assign):
         assert call(lib, handle, B=8193) == L.SGD_ETOOLARGE
         assert call(lib, handle, B=8192) == L.SGD_OK
+
+
+def test_more_tokens_than_a_call_takes(lib, handle):
+    from model_free_suffix_gb300 import _lib as L
+    assert _assign(lib, handle, N=(1 << 30) + 1) == L.SGD_ETOOLARGE
+    for call in (_prompt, _chunk):      # (two query heads a head: 2^30 rows)
+        assert call(lib, handle, N=(1 << 29) + 1) == L.SGD_ETOOLARGE
+        assert call(lib, handle, N=1 << 29) == L.SGD_OK
 
 
 def test_nothing_to_do_launches_nothing(lib, handle):
