@@ -37,10 +37,20 @@ constexpr int LOADERS = 4;
 // Registers a thread by role: together what 512 threads are launched with (128 each).
 constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
 static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
-// How far, as a power of 2, the maximum may grow before o is scaled to it; and what p is
-// multiplied by for f16, so that its range is used to the end (2^15.99 of 2^16), and p
-// keeps all bits down to 2^-21 of the largest, and 2^-33 of it in absolute terms below.
-constexpr float THRESHOLD = 8.f;
+// p and o are relative to m, the maximum as it was when it was last set, and scaled anew
+// only once the maximum has grown by a THRESHOLD more, as powers of 2.  bf16 has the range of 32
+// bits.  f16: p is up to 2^15.99 before that, 2^UP for the maximum as it was; it has all its bits
+// down to 2^-21 of that, and below an error of 2^-33 of it.
+template <typename T>
+struct Range;
+template <>
+struct Range<__nv_bfloat16> {
+  static constexpr float THRESHOLD = 40.f, UP = 1.f - THRESHOLD;  // p < 2: see `high`
+};
+template <>
+struct Range<__half> {
+  static constexpr float THRESHOLD = 8.f, UP = 15.99f - THRESHOLD;
+};
 constexpr int OVERHEAD = 2;   // of a unit, in tiles
 constexpr int LEAST_PART = 2; // tiles of a part
 constexpr int LEAST_SHARE = 4;
@@ -269,7 +279,7 @@ struct Walk {
   Unit unit;
   long long u;
   int b, i, h, blocks;
-  int t0, t1;
+  int t0, t1, shift = 0;
   bool begun = false;
 
   __device__ Walk(const KvNewArgs &a_, const Share &s_) : a(a_), s(s_), u(s_.begin.u), b(s_.begin.b), i(s_.begin.i), h(s_.begin.h) {}
@@ -304,13 +314,22 @@ struct Walk {
   }
   __device__ __forceinline__ bool shape() {
     unit = unit_of(a, row, i);
+    shift = a.window > 0 ? unit.tiles / 2 : 0;
     t1 = u == s.end.u && !s.end.past ? s.end.t : unit.tiles;
     return true;
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == unit.tiles; }
-  __device__ __forceinline__ bool cached(int j) const { return j < unit.c_tiles; }
+  // The list from its middle on where there is a window: a row may see next to nothing of
+  // the tiles at its ends, and its maximum would grow, and o be scaled, after them (a
+  // window of 2048 took 0.65 ms where 0.48 was the time without tiles of first tokens).
+  __device__ __forceinline__ int turned(int j) const {
+    j += shift;
+    return j < unit.tiles ? j : j - unit.tiles;
+  }
+  __device__ __forceinline__ bool cached(int j) const { return turned(j) < unit.c_tiles; }
   // first position of tile j
   __device__ __forceinline__ int at(int j) const {
+    j = turned(j);
     if (j < unit.c_tiles) return (j < unit.c_sink ? j : unit.c_lo + j - unit.c_sink) * TILE;
     j -= unit.c_tiles;
     return row.old + (j < unit.f_sink ? j : unit.f_lo + j - unit.f_sink) * TILE;
@@ -320,8 +339,6 @@ struct Walk {
     return x + TILE - 1 > (cached(j) ? row.old - 1 : unit.p_first) ||
            (a.window > 0 && x <= unit.p_last - a.window && x + TILE > a.sinks);
   }
-  __device__ __forceinline__ int token(int r) const { return row.q0 + (unit.r0 + r) / a.group; }
-  __device__ __forceinline__ int q_head(int r) const { return h * a.group + (unit.r0 + r) % a.group; }
 };
 
 // Parts: [D / 4][ROWS] sums (four dims each), [ROWS] maxima, [ROWS] sums of p; two
@@ -447,28 +464,57 @@ __device__ __forceinline__ uint32_t copy_tile(uint32_t to, const void *base, lon
   return bad;
 }
 
+// What copy_tile<.., true> does, for a tile that TMA has brought.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t check_tile(uint32_t at, int tokens, int tid) {
+  constexpr int C = Plan<D>::CHUNKS, PER = TILE * C / (32 * LOADERS), STEP = 32 * LOADERS / C, IN_WARP = 32 / C;
+  const int c = tid % C, line0 = tid / C;
+  uint32_t bad = 0;
+#pragma unroll 4
+  for (int i = 0; i < PER; ++i) {
+    const int line = line0 + i * STEP;
+    const uint32_t from = chunk_at(at, line, c);
+    const uint4 v = lds128(from);
+    const uint32_t votes = __ballot_sync(FULL, not_finite<T>(v));
+    if (votes) {
+      st_shared16(from, finite_word<T>(v.x), finite_word<T>(v.y), finite_word<T>(v.z), finite_word<T>(v.w));
+#pragma unroll
+      for (int k = 0; k < IN_WARP; ++k)  // (tokens behind the row's are others', and not its concern)
+        if (votes >> (k * C) & ((1u << C) - 1) && (tid & ~31) / C + k + i * STEP < tokens) bad |= 1u << (i * IN_WARP + k);
+    }
+  }
+  return bad;
+}
+
 // The queries of a unit's rows.
 template <typename T, int D>
 __device__ __forceinline__ void copy_queries(const KvNewArgs &a, const Walk &w, uint32_t to, int tid) {
   constexpr int C = Plan<D>::CHUNKS, STEP = 32 * LOADERS / C;
   const int c = tid % C;
-  const unsigned short *q = static_cast<const unsigned short *>(a.q) + c * 8;
-  if (a.q_vec && a.scale >= 0.f) {
+  // (token and head of a row, and by how much they go on: no division a row)
+  int t = (w.unit.r0 + tid / C) / a.group, h = (w.unit.r0 + tid / C) % a.group;
+  const int dt = STEP / a.group, dh = STEP % a.group;
+  const unsigned short *q = static_cast<const unsigned short *>(a.q) + c * 8 + w.row.q0 * a.q_token + w.h * a.group * a.q_head;
+  const bool direct = a.q_vec && a.scale >= 0.f;
+  const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0;  // (the scale is taken without its sign)
 #pragma unroll 4
-    for (int r = tid / C; r < w.unit.nrows; r += STEP) {
-      const unsigned short *from = q + w.token(r) * a.q_token + w.q_head(r) * a.q_head;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(chunk_at(to + (r >> 7) * (M * D * 2), r & 127, c)), "l"(from)
-                   : "memory");
+  for (int r = tid / C; r < w.unit.nrows; r += STEP) {
+    const unsigned short *from = q + t * a.q_token + h * a.q_head;
+    const uint32_t at = chunk_at(to + (r >> 7) * (M * D * 2), r & 127, c);
+    if (direct) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    } else {
+      const uint4 v = load16(from, a.q_vec);
+      st_shared16(at, v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
-    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0;  // (the scale is taken without its sign)
-#pragma unroll 1
-    for (int r = tid / C; r < w.unit.nrows; r += STEP) {
-      const uint4 v = load16(q + w.token(r) * a.q_token + w.q_head(r) * a.q_head, a.q_vec);
-      st_shared16(chunk_at(to + (r >> 7) * (M * D * 2), r & 127, c), v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
+    t += dt;
+    h += dh;
+    if (h >= a.group) {
+      h -= a.group;
+      ++t;
     }
   }
+  if (direct) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Values that are not finite meet p = 0 in rows that do not see their tokens, and 0
@@ -502,7 +548,7 @@ enum Bar {
   S_FULL = 18,             // [row tile][BUFFERS]
   P_HALF = 24, P_FULL = 27,  // [buffer]: p of the first half of the tile's tokens, of the second
   PV_HALF = 30, PV_DONE = 36,  // [row tile][BUFFERS]: the products with them are done
-  O_EMPTY = 42, SEGMENT_OVER = 44, BARS = SEGMENT_OVER + BAD_SEGMENTS
+  O_EMPTY = 42, RAW_AT = 44, SEGMENT_OVER = 45, BARS = SEGMENT_OVER + BAD_SEGMENTS
 };
 
 template <int REGS>
@@ -565,6 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     bar_init(bar(Q_FULL), LOADERS);
     bar_init(bar(Q_EMPTY), 1);
+    bar_init(bar(RAW_AT), 1);
     for (int i = 0; i < 2 * L::BUFFERS; ++i) {
       bar_init(bar(S_FULL + i), 1);
       bar_init(bar(PV_HALF + i), 1);
@@ -714,6 +761,29 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       ++item;
     };
+    // A tile of values with an edge, on its way: checked once the loads behind it are under
+    // way too.  Its slot, tokens, first token, and where what is found goes.
+    bool late = false;
+    uint32_t raw_slot = 0, raw_uses = 0, raw_segment = 0;
+    int raw_tokens = 0, raw_from = 0, raw_index = 0;
+    auto note = [&](uint32_t segment, int index, int from, uint32_t bad) {
+      BadTile &e = bad_tiles[segment % BAD_SEGMENTS][index];
+      if (lane == 0) e.word[wl] = bad;
+      if (wl == 0 && lane == 0) {
+        e.x = from;
+        bad_count[segment % BAD_SEGMENTS] = index + 1;
+      }
+    };
+    auto settle = [&]() {
+      if (!late) return;
+      late = false;
+      ok = ok && wait(RAW_AT, raw_uses++);
+      ok = __all_sync(FULL, ok);
+      if (!ok) return;
+      note(raw_segment, raw_index, raw_from, check_tile<T, D>(ring + raw_slot * L::HALF, raw_tokens, me));
+      async_fence();
+      warp_arrive(FULL_AT + raw_slot);
+    };
     while (ok && w.next(&bits)) {
       if (w.t0 == w.t1) continue;
       if (segments >= BAD_SEGMENTS) {
@@ -759,6 +829,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                                  false, tokens, me);
           done();
         }
+        settle();
+        if (!ok) break;
         if (j == w.t0) {
           if (segments > 0) ok = wait(Q_EMPTY, segments - 1);
           ok = __all_sync(FULL, ok);
@@ -780,27 +852,51 @@ __global__ void __launch_bounds__(THREADS, 1)
           done();
         } else if (a.v_vec && !w.edge(j, x)) {
           by_tma(&vmap, w.row.q0 + from);
+        } else if (!w.edge(j, x)) {
+          copy_tile<T, D, false>(ring + item % STAGES * L::HALF,
+                                 static_cast<const T *>(a.v) + (w.row.q0 + from) * a.v_token + w.h * a.v_head, a.v_token,
+                                 false, tokens, me);
+          done();
         } else {
-          const uint32_t bad = copy_tile<T, D, true>(
-              ring + item % STAGES * L::HALF, static_cast<const T *>(a.v) + (w.row.q0 + from) * a.v_token + w.h * a.v_head,
-              a.v_token, a.v_vec, tokens, me);
-          BadTile *e = nullptr;
           // (at most 7 tiles of a unit have an edge: 3 where its rows' tokens are, 3 where
           // their windows begin, 1 where the first tokens end)
-          if (w.edge(j, x) && bads < BAD_TILES) {
-            e = &bad_tiles[segments % BAD_SEGMENTS][bads++];
-            if (lane == 0) e->word[wl] = bad;
+          const int index = min(bads++, BAD_TILES - 1);
+          if (a.v_vec) {
+            late = true;
+            raw_slot = item % STAGES;
+            raw_segment = segments;
+            raw_tokens = tokens;
+            raw_from = from;
+            raw_index = index;
             if (wl == 0 && lane == 0) {
-              e->x = from;
-              bad_count[segments % BAD_SEGMENTS] = bads;
+              const uint32_t to = ring + raw_slot * L::HALF, b = bar(RAW_AT);
+              bar_expect(b, L::HALF);
+#pragma unroll
+              for (int d = 0; d < D; d += 64) tma_load_3d(to + d * (TILE * 2), &vmap, d, w.h, w.row.q0 + from, b);
             }
+            __syncwarp();
+            ++item;
+          } else {
+            note(segments, index, from,
+                 copy_tile<T, D, true>(ring + item % STAGES * L::HALF,
+                                       static_cast<const T *>(a.v) + (w.row.q0 + from) * a.v_token + w.h * a.v_head, a.v_token,
+                                       false, tokens, me));
+            done();
           }
-          done();
+        }
+        if (!cached && j + 1 < w.t1 && w.cached(j + 1)) {
+          pages(j + 1);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) load8(a.c.k, i);
         }
       }
       ++segments;
     }
+    settle();
     if (!ok) {  // (copies in flight land before the CTA ends, or a bound runs out)
+      if (late)
+        for (int n = 0; n < (1 << 16) && !bar_try(bar(RAW_AT), raw_uses & 1); ++n) {
+        }
       for (int i = 0; i < STAGES; ++i)
         for (int n = 0; n < (1 << 16) && !bar_try(bar(FULL_AT + i), 0) && !bar_try(bar(FULL_AT + i), 1); ++n) {
         }
@@ -928,9 +1024,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t o_at = tmem + lanes + L::O + i * D;
     const float c0 = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);
-    // p is 2^UP times as large as it says.  bf16: an exponent of 1 or more, one bit, then
-    // tells that the maximum has grown by 2^THRESHOLD.  f16: its range is used to the end.
-    constexpr float UP = BF16 ? 1.f - THRESHOLD : 15.99f - THRESHOLD;
+    // p is 2^UP times as large as it says.  bf16: one bit of it, that of an exponent of 1 or
+    // more, tells that the maximum has grown by 2^THRESHOLD.
+    constexpr float UP = Range<T>::UP, THRESHOLD = Range<T>::THRESHOLD;
     Walk w(a, share);
     uint32_t g = 0, segments = 0;
     uint32_t buf = 0;            // of the next segment's first scores

@@ -212,6 +212,40 @@ def test_what_is_not_finite_stays_with_those_that_see_it(KV, bad, which, dtype, 
     kv.close()
 
 
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5)])
+def test_values_that_are_not_finite_in_long_rows(KV, aligned, window, sinks):
+    """In tiles that a unit's rows see in full, in part, or not at all; behind the row's last token; values
+    whose start is off 16 bytes."""
+    counts, H, G, D = [900, 3, 700], 1, 4, 64
+    N = sum(counts)
+    q, k, v = (x.contiguous() for x in _qkv(N, H, G, D, "bf16"))
+    spots = [0, 3, 100, 127, 128, 400, 511, 640, 899, 900, 902, 903, 1500]
+    kv = _handle(KV, H, G, D, len(counts))
+    clean = kv.attend_prompt(q, k, v, _starts(counts), window=window, sinks=sinks).cpu()
+    for i, t in enumerate(spots):
+        v[t, 0, i] = math.nan if i % 2 else math.inf
+    if not aligned:
+        flat = torch.empty(v.numel() + 8, dtype=v.dtype, device="cuda")
+        flat[1:1 + v.numel()] = v.reshape(-1)
+        v = flat[1:1 + v.numel()].view(v.shape)
+    out = kv.attend_prompt(q, k, v, _starts(counts), window=window, sinks=sinks).cpu()
+    at = 0
+    for c in counts:
+        p, j = torch.arange(c)[:, None], torch.arange(c)[None]
+        see = (j <= p) & ((j > p - window) | (j < sinks)) if window else j <= p
+        hit = torch.zeros(c, D, dtype=torch.bool)
+        for i, t in enumerate(spots):
+            if at <= t < at + c:
+                hit[:, i] |= see[:, t - at]
+        got = out[at:at + c]
+        assert bool((~got.isfinite()).eq(hit[:, None]).all())
+        assert torch.equal(got[~hit[:, None].expand_as(got)], clean[at:at + c][~hit[:, None].expand_as(got)])
+        at += c
+    assert kv.get_error() == 0
+    kv.close()
+
+
 def test_bad_starts_are_reported(KV):
     from model_free_suffix_gb300 import _lib as L
     H, G, D = 1, 2, 64
