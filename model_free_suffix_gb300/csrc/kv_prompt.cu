@@ -240,8 +240,8 @@ __device__ const Share &share_of(const KvNewArgs &a, int *first, uint32_t *bits)
     __syncthreads();
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-      const long long pos = all * (g + k) / ctas;
-      const int h = (int)(pos / total);
+      const long long pos = quotient(all * (g + k), ctas);
+      const int h = (int)quotient(pos, total);
       const long long in = pos - h * total;
       if (h < a.c.heads && c0 < c1 && before <= in && in < before + mine) {
         int b = b_from, c = c0;
@@ -548,7 +548,9 @@ enum Bar {
   S_FULL = 18,             // [row tile][BUFFERS]
   P_HALF = 24, P_FULL = 27,  // [buffer]: p of the first half of the tile's tokens, of the second
   PV_HALF = 30, PV_DONE = 36,  // [row tile][BUFFERS]: the products with them are done
-  O_EMPTY = 42, RAW_AT = 44, SEGMENT_OVER = 45, BARS = SEGMENT_OVER + BAD_SEGMENTS
+  O_EMPTY = 42,
+  RAW_AT = 44,             // [slot]: values that came to be checked (see `settle`)
+  SEGMENT_OVER = 52, BARS = SEGMENT_OVER + BAD_SEGMENTS
 };
 
 template <int REGS>
@@ -608,10 +610,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       bar_init(bar(FULL_AT + i), LOADERS);
       bar_init(bar(EMPTY_AT + i), 1);
+      bar_init(bar(RAW_AT + i), 1);
     }
     bar_init(bar(Q_FULL), LOADERS);
     bar_init(bar(Q_EMPTY), 1);
-    bar_init(bar(RAW_AT), 1);
     for (int i = 0; i < 2 * L::BUFFERS; ++i) {
       bar_init(bar(S_FULL + i), 1);
       bar_init(bar(PV_HALF + i), 1);
@@ -764,7 +766,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // A tile of values with an edge, on its way: checked once the loads behind it are under
     // way too.  Its slot, tokens, first token, and where what is found goes.
     bool late = false;
-    uint32_t raw_slot = 0, raw_uses = 0, raw_segment = 0;
+    // (Its barrier is its slot's: one warp may be several tiles ahead of another, but not a
+    // whole round of slots.  parities: of the slots' next uses.)
+    uint32_t raw_slot = 0, parities = 0, raw_segment = 0;
     int raw_tokens = 0, raw_from = 0, raw_index = 0;
     auto note = [&](uint32_t segment, int index, int from, uint32_t bad) {
       BadTile &e = bad_tiles[segment % BAD_SEGMENTS][index];
@@ -777,7 +781,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto settle = [&]() {
       if (!late) return;
       late = false;
-      ok = ok && wait(RAW_AT, raw_uses++);
+      ok = ok && wait(RAW_AT + raw_slot, parities >> raw_slot);
+      parities ^= 1u << raw_slot;
       ok = __all_sync(FULL, ok);
       if (!ok) return;
       note(raw_segment, raw_index, raw_from, check_tile<T, D>(ring + raw_slot * L::HALF, raw_tokens, me));
@@ -869,7 +874,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             raw_from = from;
             raw_index = index;
             if (wl == 0 && lane == 0) {
-              const uint32_t to = ring + raw_slot * L::HALF, b = bar(RAW_AT);
+              const uint32_t to = ring + raw_slot * L::HALF, b = bar(RAW_AT + raw_slot);
               bar_expect(b, L::HALF);
 #pragma unroll
               for (int d = 0; d < D; d += 64) tma_load_3d(to + d * (TILE * 2), &vmap, d, w.h, w.row.q0 + from, b);
@@ -895,7 +900,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     settle();
     if (!ok) {  // (copies in flight land before the CTA ends, or a bound runs out)
       if (late)
-        for (int n = 0; n < (1 << 16) && !bar_try(bar(RAW_AT), raw_uses & 1); ++n) {
+        for (int n = 0; n < (1 << 16) && !bar_try(bar(RAW_AT + raw_slot), parities >> raw_slot & 1); ++n) {
         }
       for (int i = 0; i < STAGES; ++i)
         for (int n = 0; n < (1 << 16) && !bar_try(bar(FULL_AT + i), 0) && !bar_try(bar(FULL_AT + i), 1); ++n) {
@@ -1003,7 +1008,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const Unit u = unit_of(a, r, share.end.i);
         join.parts = 2;
         for (int g = blockIdx.x + 2; g < share.ctas; ++g) {
-          const long long into = share.all * g / share.ctas - share.u_at;
+          const long long into = quotient(share.all * g, share.ctas) - share.u_at;
           if (into >= OVERHEAD + share.end_tiles) break;
           Cut c;
           place_cut(c, into, share.end_tiles);
@@ -1248,43 +1253,65 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tmem_after_sync();
   if (warp == W_ISSUE) tmem_free(tmem, 512);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// The parts of the units that cuts went through: 32 rows a block, lanes along rows.
+// The parts of the units that cuts went through: 32 rows a block, lanes along rows, a
+// warp's share of the dims each.  The parts' weights first, then the sums with all of a
+// warp's dims of several parts in flight (with one load after the other a chunk of 100
+// tokens over 2000, in five parts, took 15 us here, half of its attention).
 constexpr int JOIN_THREADS = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ KvNewArgs a) {
+  constexpr int W = JOIN_THREADS / 32, E = D / 4 / W;  // float4s of a warp
+  extern __shared__ float s_w[];                       // [parts][32]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join join = *join_of(a, blockIdx.x);
-  const int R = blockIdx.y * 32 + (threadIdx.x & 31);
-  if (R >= join.nrows || join.parts == 0) return;
+  const int R = blockIdx.y * 32 + lane;
+  if (join.parts == 0 || (int)blockIdx.y * 32 >= join.nrows) return;
   auto slot = [&](int p) { return new_part<D>(a, 2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)); };
-  float top = -CUDART_INF_F, l = 0.f;
-  for (int p = 0; p < join.parts; ++p) top = fmaxf(top, slot(p)[ROWS * D + R]);
-  const float base = top == -CUDART_INF_F ? 0.f : top;
-  for (int p = 0; p < join.parts; ++p) {
+  float *s_l = s_w + join.parts * 32;
+  for (int p = warp; p < join.parts; p += W) {
     const float *ml = slot(p) + ROWS * D + R;
-    l = fmaf(ml[ROWS], ex2_approx(ml[0] - base), l);
+    s_w[p * 32 + lane] = ml[0];
+    s_l[p * 32 + lane] = ml[ROWS];
   }
+  __syncthreads();
+  float top = -CUDART_INF_F, l = 0.f;
+  for (int p = 0; p < join.parts; ++p) top = fmaxf(top, s_w[p * 32 + lane]);
+  const float base = top == -CUDART_INF_F ? 0.f : top;
+  for (int p = 0; p < join.parts; ++p) l = fmaf(s_l[p * 32 + lane], ex2_approx(s_w[p * 32 + lane] - base), l);
+  float4 x[E] = {};
+#pragma unroll 4
+  for (int p = 0; p < join.parts; ++p) {
+    const float *from = slot(p) + (warp * E * ROWS + R) * 4;
+    const float k = ex2_approx(s_w[p * 32 + lane] - base);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float4 v = *reinterpret_cast<const float4 *>(from + e * (ROWS * 4));
+      x[e].x = fmaf(v.x, k, x[e].x);
+      x[e].y = fmaf(v.y, k, x[e].y);
+      x[e].z = fmaf(v.z, k, x[e].z);
+      x[e].w = fmaf(v.w, k, x[e].w);
+    }
+  }
+  if (R >= join.nrows) return;
   const float inv = 1.f / l;
   const int row = join.r0 + R;
   T *out = static_cast<T *>(a.out) +
-           ((long long)(join.q0 + row / a.group) * a.q_heads + join.h * a.group + row % a.group) * D;
-#pragma unroll 1
-  for (int d = threadIdx.x >> 5; d < D / 4; d += JOIN_THREADS / 32) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = 0; p < join.parts; ++p) {
-      const float *from = slot(p);
-      const float4 v = *reinterpret_cast<const float4 *>(from + (d * ROWS + R) * 4);
-      const float k = ex2_approx(from[ROWS * D + R] - base);
-      x.x = fmaf(v.x, k, x.x);
-      x.y = fmaf(v.y, k, x.y);
-      x.z = fmaf(v.z, k, x.z);
-      x.w = fmaf(v.w, k, x.w);
-    }
-    *reinterpret_cast<uint2 *>(out + d * 4) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
-  }
+           ((long long)(join.q0 + row / a.group) * a.q_heads + join.h * a.group + row % a.group) * D + warp * E * 4;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    *reinterpret_cast<uint2 *>(out + e * 4) = make_uint2(pack2<T>(x[e].x * inv, x[e].y * inv), pack2<T>(x[e].z * inv, x[e].w * inv));
 }
+// (a unit has at most as many parts as there are CTAs)
+constexpr int join_smem(int ctas) { return ctas * 32 * 2 * 4; }
+
+// Within what the workspace and the join's shared memory are laid out for.
+constexpr int NEW_MAX_CTAS = 190;
+static_assert(join_smem(NEW_MAX_CTAS) <= 48 * 1024 && NEW_MAX_CTAS <= MAX_CTAS, "the parts' weights");
+int new_ctas(int sms) { return sms < NEW_MAX_CTAS ? sms : NEW_MAX_CTAS; }
 
 template <typename T, int D>
 cudaError_t launch(KvNewArgs a, cudaStream_t st, int *launches) {
@@ -1292,13 +1319,23 @@ cudaError_t launch(KvNewArgs a, cudaStream_t st, int *launches) {
   // (strides that a map does not take: the loading warps copy the tiles)
   a.k_vec = a.k_vec && kv_make_token_map(&k, a.k, D, a.c.heads, a.r.N, a.k_head, a.k_token, TILE);
   a.v_vec = a.v_vec && kv_make_token_map(&v, a.v, D, a.c.heads, a.r.N, a.v_head, a.v_token, TILE);
-  const int ctas = a.sms < MAX_CTAS ? a.sms : MAX_CTAS;
+  const int ctas = new_ctas(a.sms);
   new_kernel<T, D><<<ctas, THREADS, Plan<D>::SMEM, st>>>(a, k, v);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   *launches = 2;
-  join_kernel<T, D><<<dim3(ctas, ROWS / 32), JOIN_THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  // (launched while the first kernel ends, it waits there for its results)
+  cudaLaunchConfig_t c = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.gridDim = dim3(ctas, ROWS / 32);
+  c.blockDim = dim3(JOIN_THREADS);
+  c.dynamicSmemBytes = join_smem(ctas);
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, join_kernel<T, D>, a);
 }
 
 template <typename T, int D>
@@ -1309,7 +1346,7 @@ cudaError_t limit() {
 }  // namespace
 
 size_t kv_new_workspace(int sms) {
-  const size_t ctas = sms < MAX_CTAS ? sms : MAX_CTAS;
+  const size_t ctas = new_ctas(sms);
   return (size_t)MAX_CTAS * 8 + MAX_CTAS * 32 + ctas * 2 * (ROWS * (128 + 2) * 4);
 }
 

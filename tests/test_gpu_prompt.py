@@ -271,6 +271,14 @@ def test_many_rows(KV):
     _prompt(KV, counts, 1, 2, 64, "bf16")
 
 
+@pytest.mark.parametrize("dtype,D,H,G,window", [("f16", 64, 3, 3, 0), ("bf16", 128, 2, 4, 150)])
+def test_many_ragged_rows(KV, dtype, D, H, G, window):
+    """Units of one and of two row tiles in turn, most of one or two tiles of keys: every role runs ahead of
+    the others as far as it can."""
+    counts = [1 + int(400 * ((i * 0.6180339887) % 1.0)) for i in range(110)]
+    _prompt(KV, counts, H, G, D, dtype, window=window, sinks=2)
+
+
 def test_graphs_streams_and_repetition(KV):
     """Captured calls replay with new lengths; another stream; the same bits each time."""
     H, G, D = 2, 4, 128
