@@ -910,93 +910,114 @@ __global__ void __launch_bounds__(THREADS, 1)
     fewer_registers<REGS_OTHER>();
     if (warp == W_ISSUE) {
       // The whole warp walks, so that addresses and counters are the warp's (in its
-      // uniform registers, where the products take them from); one thread issues.
+      // uniform registers, where the products take them from); one thread issues.  What it
+      // executes from one p to the next scores adds to every tile's time: little.
       constexpr uint32_t QK = product16(BF16, TILE, false), PV = product16(BF16, D, true), HIGH = operand_high(1024);
+      constexpr uint32_t SLOT = L::HALF / 16;
       Walk w(a, share);
-      uint32_t item = 0, segments = 0, segs1 = 0;
-      uint32_t s_buf = 0, p_buf = 0, p_use = 0;  // of the products in turn: the buffer, and how often it was used before
-      uint32_t s_bar0 = 0, s_bar1 = 0, p_bar0 = 0, p_bar1 = 0;  // of either row tile: the barriers of its next scores, its next p
-      bool ok = true;
-      auto wait_all = [&](int which, uint32_t parity) {
-        const uint32_t b = bar(which);
-        if (__all_sync(FULL, bar_try(b, parity & 1))) return true;
-        return (bool)__all_sync(FULL, wait(which, parity));
+      const uint32_t bars0 = smem_addr(bars);
+      auto ready = [&](uint32_t at, uint32_t parity) {
+        if (__all_sync(FULL, bar_try(bars0 + at * 8, parity))) return true;
+        return (bool)__all_sync(FULL, wait(at, parity));
       };
       const uint32_t q_low = operand_low(q_at, 0), k_low = operand_low(ring, 0), v_low = operand_low(ring, TILE * 128);
-      auto qk = [&](int i, uint32_t slot) {
-        const uint32_t q = q_low + i * (M * D * 2 / 16), k = k_low + slot * (L::HALF / 16);
-#pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
-          const uint32_t off = ((e / 4) * (TILE * 128) + (e % 4) * 32) / 16;
-          mma_ss(tmem + L::S + s_buf * TILE, q + off, k + off, HIGH, QK, e > 0);
-        }
-      };
-      // half of the tile's tokens at a time: the first products run while the second half of p is made
-      auto pv = [&](int i, uint32_t slot, int half, bool add) {
-        const uint32_t v = v_low + slot * (L::HALF / 16) + half * (64 * 128 / 16), p = tmem + L::S + p_buf * TILE + half * 32,
-                       o = tmem + L::O + i * D;
-        mma_ts(o, p, v, HIGH, PV, add);
-#pragma unroll
-        for (int e = 1; e < 4; ++e) mma_ts(o, p + e * 8, v + e * (2048 / 16), HIGH, PV, true);
-      };
+      // (half of a tile's tokens at a time: the products with the first run while p of the second is made)
+      // the next keys' and values' slots, and the parity of their barriers
+      uint32_t ks = 0, k_par = 0, vs = 1, v_par = 0;
+      // of the products in turn: the buffer of the next scores, of the next p, and its parity
+      uint32_t s_buf = 0, p_buf = 0, p_par = 0;
+      // of either row tile: the barriers of its next scores and of its next products with p
+      uint32_t s_bar0 = 0, s_bar1 = 0, p_bar0 = 0, p_bar1 = 0;
+      uint32_t segments = 0, segs1 = 0;
+      bool ok = true;
       while (ok && w.next(&bits)) {
-        const int n = __shfl_sync(FULL, w.t1 - w.t0, 0);
+        const int n = __reduce_max_sync(FULL, w.t1 - w.t0);
         if (n == 0) continue;
-        const int two = __shfl_sync(FULL, w.unit.nrows, 0) > M, all = n << two;
-        ok = wait_all(Q_FULL, segments);
-        // the x-th product q k^T of the segment: row tile x & two of key tile x >> two
-        auto issue_qk = [&](int x) {
-          const int i = x & two, j = x >> two;
-          const uint32_t ki = item + 2 * j, ks = ki % STAGES;
-          if (i == 0) ok = ok && wait_all(FULL_AT + ks, ki / STAGES);
+        const uint32_t two = __reduce_max_sync(FULL, (uint32_t)(w.unit.nrows > M));
+        ok = ready(Q_FULL, segments & 1);
+        // scores: row tile qi, key tile qj
+        uint32_t qi = 0;
+        int qj = 0;
+        auto scores = [&]() {
+          if (qi == 0) ok = ok && ready(FULL_AT + ks, k_par);
           if (!ok) return;
           tmem_after_sync();
           if (elect_one()) {
-            qk(i, ks);
-            mma_commit(bar(S_FULL + (i ? L::BUFFERS + s_bar1 : s_bar0)));
-            if (i == two) mma_commit(bar(EMPTY_AT + ks));
-            if (x + 1 == all) mma_commit(bar(Q_EMPTY));
+            const uint32_t q = q_low + qi * (M * D * 2 / 16), k = k_low + ks * SLOT, to = tmem + L::S + s_buf * TILE;
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t off = ((e / 4) * (TILE * 128) + (e % 4) * 32) / 16;
+              mma_ss(to, q + off, k + off, HIGH, QK, e > 0);
+            }
+            mma_commit(bars0 + (S_FULL + (qi ? L::BUFFERS + s_bar1 : s_bar0)) * 8);
+            if (qi == two) {
+              mma_commit(bars0 + (EMPTY_AT + ks) * 8);
+              if (qj + 1 == n) mma_commit(bars0 + Q_EMPTY * 8);
+            }
           }
           __syncwarp();
-          if (++s_buf == L::BUFFERS) s_buf = 0;
-          uint32_t &s_bar = i ? s_bar1 : s_bar0;
-          if (++s_bar == L::BUFFERS) s_bar = 0;
+          if (qi) s_bar1 = s_bar1 + 1 == L::BUFFERS ? 0 : s_bar1 + 1;
+          else s_bar0 = s_bar0 + 1 == L::BUFFERS ? 0 : s_bar0 + 1;
+          s_buf = s_buf + 1 == L::BUFFERS ? 0 : s_buf + 1;
+          if (qi == two) {
+            qi = 0;
+            ++qj;
+            ks += 2;
+            if (ks >= STAGES) {
+              ks = 0;
+              k_par ^= 1;
+            }
+          } else {
+            qi = 1;
+          }
         };
-        for (int x = 0; x < min(all, L::BUFFERS); ++x) issue_qk(x);
-        for (int x = 0; ok && x < all; ++x) {
-          const int i = x & two, j = x >> two;
-          const uint32_t vi = item + 2 * j + 1, vs = vi % STAGES;
-          if (i == 0) ok = wait_all(FULL_AT + vs, vi / STAGES);
-          ok = ok && wait_all(P_HALF + p_buf, p_use);
-          if (ok && j == 0) {
-            const uint32_t before = i ? segs1 : segments;
-            if (before > 0) ok = wait_all(O_EMPTY + i, before - 1);
+#pragma unroll 1
+        for (int x = 0; x < L::BUFFERS && qj < n; ++x) scores();
+#pragma unroll 1
+        for (int j = 0; ok && j < n; ++j) {
+          ok = ready(FULL_AT + vs, v_par);
+#pragma unroll 1
+          for (uint32_t i = 0; ok && i <= two; ++i) {
+            if (j == 0) {
+              const uint32_t before = i ? segs1 : segments;
+              if (before > 0) ok = ready(O_EMPTY + i, (before - 1) & 1);
+            }
+            ok = ok && ready(P_HALF + p_buf, p_par);
+            if (!ok) break;
+            const uint32_t v = v_low + vs * SLOT, p = tmem + L::S + p_buf * TILE, o = tmem + L::O + i * D;
+            const uint32_t of = (i ? L::BUFFERS + p_bar1 : p_bar0) * 8;
+            tmem_after_sync();
+            if (elect_one()) {
+              mma_ts(o, p, v, HIGH, PV, j > 0);
+#pragma unroll
+              for (int e = 1; e < 4; ++e) mma_ts(o, p + e * 8, v + e * (2048 / 16), HIGH, PV, true);
+              mma_commit(bars0 + PV_HALF * 8 + of);
+            }
+            __syncwarp();
+            ok = ready(P_FULL + p_buf, p_par);
+            if (!ok) break;
+            tmem_after_sync();
+            if (elect_one()) {
+#pragma unroll
+              for (int e = 4; e < TILE / 16; ++e) mma_ts(o, p + e * 8, v + e * (2048 / 16), HIGH, PV, true);
+              mma_commit(bars0 + PV_DONE * 8 + of);
+              if (i == two) mma_commit(bars0 + (EMPTY_AT + vs) * 8);
+            }
+            __syncwarp();
+            if (i) p_bar1 = p_bar1 + 1 == L::BUFFERS ? 0 : p_bar1 + 1;
+            else p_bar0 = p_bar0 + 1 == L::BUFFERS ? 0 : p_bar0 + 1;
+            if (++p_buf == L::BUFFERS) {
+              p_buf = 0;
+              p_par ^= 1;
+            }
+            if (qj < n) scores();
           }
-          if (!ok) break;
-          tmem_after_sync();
-          if (elect_one()) {
-            pv(i, vs, 0, j > 0);
-            mma_commit(bar(PV_HALF + (i ? L::BUFFERS + p_bar1 : p_bar0)));
+          vs += 2;
+          if (vs >= STAGES) {
+            vs = 1;
+            v_par ^= 1;
           }
-          __syncwarp();
-          ok = wait_all(P_FULL + p_buf, p_use);
-          if (!ok) break;
-          tmem_after_sync();
-          if (elect_one()) {
-            pv(i, vs, 1, true);
-            mma_commit(bar(PV_DONE + (i ? L::BUFFERS + p_bar1 : p_bar0)));
-            if (i == two) mma_commit(bar(EMPTY_AT + vs));
-          }
-          __syncwarp();
-          uint32_t &p_bar = i ? p_bar1 : p_bar0;
-          if (++p_bar == L::BUFFERS) p_bar = 0;
-          if (++p_buf == L::BUFFERS) {
-            p_buf = 0;
-            ++p_use;
-          }
-          if (x + L::BUFFERS < all) issue_qk(x + L::BUFFERS);
         }
-        item += 2 * n;
         ++segments;
         segs1 += two;
       }
