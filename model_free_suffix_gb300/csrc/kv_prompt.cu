@@ -35,7 +35,7 @@ constexpr int WARPS = 16, THREADS = 32 * WARPS;
 constexpr int W_LOAD = 8, W_ISSUE = 12, W_JOIN = 13;
 constexpr int LOADERS = 4;
 // Registers a thread by role: together what 512 threads are launched with (128 each).
-constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
+constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 112;
 static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
 // p and o are relative to m, the maximum as it was when it was last set, and scaled anew
 // only once the maximum has grown by a THRESHOLD more, as powers of 2.  bf16 has the range of 32
@@ -51,9 +51,9 @@ template <>
 struct Range<__half> {
   static constexpr float THRESHOLD = 8.f, UP = 15.99f - THRESHOLD;
 };
-constexpr int OVERHEAD = 2;   // of a unit, in tiles
+constexpr int OVERHEAD = 3;   // of a unit, in tiles
 constexpr int LEAST_PART = 2; // tiles of a part
-constexpr int LEAST_SHARE = 4;
+constexpr int LEAST_SHARE = 3;
 constexpr int META = 16;      // outlasts how far the loaders run ahead
 constexpr int BAD_SEGMENTS = 4, BAD_TILES = 8;
 
