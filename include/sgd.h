@@ -553,7 +553,8 @@ typedef struct {
                                      sgd_kv_attend are 0 where only its length is wrong).
                                      A first position below 0: the row reads as 0. Outputs
                                      of sgd_kv_read from out_start[B] on are 0           */
-#define SGD_KV_ERR_WAIT      0x8u /* sgd_kv_attend: a copy never arrived; results are not valid */
+#define SGD_KV_ERR_WAIT      0x8u /* sgd_kv_attend and its kind: a copy never arrived; results are not
+                                     valid                                               */
 #define SGD_KV_ERR_ROOM      0x10u /* sgd_kv_assign: new tokens of a row had no place among the
                                      call's N, or no free pages: the row got none of them */
 #define SGD_KV_ERR_NONFINITE 0x4u /* written as the largest magnitude (infinities) or 0 (NaN) */

@@ -898,13 +898,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       ++segments;
     }
     settle();
-    if (!ok) {  // (copies in flight land before the CTA ends, or a bound runs out)
-      if (late)
-        for (int n = 0; n < (1 << 16) && !bar_try(bar(RAW_AT + raw_slot), parities >> raw_slot & 1); ++n) {
-        }
-      for (int i = 0; i < STAGES; ++i)
-        for (int n = 0; n < (1 << 16) && !bar_try(bar(FULL_AT + i), 0) && !bar_try(bar(FULL_AT + i), 1); ++n) {
-        }
+    if (!ok) {
+      // (Copies in flight land before the CTA ends: they take microseconds.  Their barriers
+      // may never complete, since other warps arrive at them too.)
+      for (int n = 0; n < (1 << 12); ++n) __nanosleep(256);
     }
   } else if (warp >= W_ISSUE) {
     fewer_registers<REGS_OTHER>();
