@@ -12,6 +12,14 @@
 // pages and of the tokens.  Two cluster barriers: nothing is written before all
 // CTAs have read the state, nothing taken before all given pages are on the list.
 // Many tokens (prompts) get a second kernel, of as many CTAs as they fill.
+//
+// Nothing here is bound by bytes but the places of prompts' tokens (12 bytes each): a call
+// of a serving step is a chain of launch, one read of the rows, four prefix sums, two
+// cluster barriers and the reads of tables and list.  Measured, a call: 4 rows 4 us, 256
+// rows of 1..17 tokens 8 to 9, 1024 rows of which 256 give up or get 8192 tokens'
+// pages (half of the calls place a million tokens) 26.  One CTA of 1024 threads took 28 and 616
+// for the latter two; clusters of four CTAs 9 and 34, of 256 threads a CTA 9 and 34, of 1024
+// 10 and 24.
 #include <cooperative_groups.h>
 
 #include "kv_internal.h"
@@ -24,7 +32,8 @@ namespace {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int CTAS = 8;            // of the cluster
-// Tokens that the cluster places itself.  ASSIGN_NOTE
+// Tokens that the cluster places itself: at some 20000 a step a second kernel took 8.8 us
+// a call against 7.8, at 96000 its own 16 against 9.
 constexpr int OWN_TOKENS = 32768;
 
 struct Row {

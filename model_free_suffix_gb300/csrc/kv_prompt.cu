@@ -19,6 +19,24 @@
 // The tiles of all units, one after the other, are cut into equal shares, one
 // per CTA; a unit that a cut goes through leaves parts, which a second kernel
 // joins in their order (no atomics: the result does not depend on timing).
+//
+// Numbers.  Products of 16-bit values and p, sums, maxima and outputs in 32 bits; p is
+// rounded to the values' type for the second product (2^-8 of it for bf16, 2^-11 for f16:
+// the tensor cores take both operands in one type), the sum of p before that.  Cached keys
+// and values go to 16 bits exactly (see `widen`).
+//
+// What bounds it.  Per tile and two row tiles the products take 2048 cycles at a dim of
+// 128, 1024 at 64, and the exponentials 1024; from p to the next scores of a row tile lie
+// both products (1024 cycles) and some 300 of latency, and its exponentials, alone, take the
+// thread of a row some 1600 to 2000.  So a tile takes about 3100 cycles either way: 32768 tokens,
+// 32 query heads of 128 in groups of four, 6.5 ms, 1350 TFLOP/s; at a dim of 64 800.
+// Tried and slower or no faster, the same 32768 tokens in ms: two threads a row, half of
+// a tile's tokens each, meeting once a tile (6.6, chunks over the cache 30% slower: 16
+// softmax warps leave the loading ones few registers and turns) or finishing in turn (9.6);
+// all p of a tile at once (6.5, short prompts and chunks 10% slower); s read twice, for its
+// maximum and for p (8.1); the first half of the next scores before the products with p (7.3: N =
+// 64 reads the queries from shared memory twice as often); the issuing thread alone in a
+// divergent branch (8.1: operands go through vector registers).
 #include <math_constants.h>
 
 #include "kv_attend.cuh"
@@ -34,7 +52,9 @@ constexpr int WARPS = 16, THREADS = 32 * WARPS;
 // (warps 0 to W_LOAD - 1: softmax)
 constexpr int W_LOAD = 8, W_ISSUE = 12, W_JOIN = 13;
 constexpr int LOADERS = 4;
-// Registers a thread by role: together what 512 threads are launched with (128 each).
+// Registers a thread by role: together what 512 threads are launched with (128 each).  With
+// 168 and 88 chunks of a step took 1.40 ms against 1.24 (the loading warps spill), with 136 and
+// 120 1.28 (the softmax ones do).
 constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 112;
 static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
 // p and o are relative to m, the maximum as it was when it was last set, and scaled anew
@@ -51,9 +71,10 @@ template <>
 struct Range<__half> {
   static constexpr float THRESHOLD = 8.f, UP = 15.99f - THRESHOLD;
 };
-constexpr int OVERHEAD = 3;   // of a unit, in tiles
-constexpr int LEAST_PART = 2; // tiles of a part
-constexpr int LEAST_SHARE = 3;
+// What a unit costs beside its tiles, in tiles; the fewest tiles of a part; the least work that
+// is worth a CTA.  Measured: one prompt of 200 tokens 19 us with (3, 2, 3), 25 with 2 or 5 in the
+// first or last place; a step's prompts 1.36 ms, 1.40 with 2 in the first.
+constexpr int OVERHEAD = 3, LEAST_PART = 2, LEAST_SHARE = 3;
 constexpr int META = 16;      // outlasts how far the loaders run ahead
 constexpr int BAD_SEGMENTS = 4, BAD_TILES = 8;
 
