@@ -453,6 +453,57 @@ def test_captured_chunks_of_two_graphs_share_a_handle(KV):
             assert torch.equal(o, w)
 
 
+def test_places_beyond_32_bits(KV):
+    """Queries and results of more than 2^31 elements, and pages behind the first 4 GiB of a cache."""
+    N, H, G, D, c = (1 << 18) + 300, 1, 64, 128, 300
+    kv = _handle(KV, H, G, D, 1)
+    q = torch.empty(N, H * G, D, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.empty(N, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x = _qkv(c, H, G, D, "bf16")
+    for big, small in zip((q, k, v), x):
+        big[N - c:] = small
+    out = kv.attend_prompt(q, k, v, _i32([N - c, N]))
+    want = kv.attend_prompt(*x, _starts([c]))
+    assert torch.equal(out[N - c:], want)
+    _check_rows(want[:40], *(y[:40] for y in x), [40], H, G, D, D ** -0.5, 0, 0)
+    assert kv.get_error() == 0
+    kv.close()
+    del q, k, v, out
+    pages = (1 << 32) // (8 * 128 * 128) + 40
+    big = _handle(KV, 8, 1, 128, 1, num_pages=pages, page_size=128, max_pages_per_row=3)
+    small = _handle(KV, 8, 1, 128, 1, num_pages=3, page_size=128, max_pages_per_row=3)
+    q, k, v = _qkv(200, 8, 1, 128, "bf16", seed=3)
+    tables = torch.tensor([[pages - 1, 5, pages - 17]]).int().cuda(), _i32([[0, 1, 2]])
+    outs = []
+    for kv, table in zip((big, small), tables):
+        kv.write(k, v, table, _i32([200]), _i32([0, 200]))
+        outs.append(kv.attend_chunk(q, k, v, table, _i32([384]), _i32([0, 184])))
+        assert kv.get_error() == 0
+        kv.close()
+    assert torch.equal(outs[0][:184], outs[1][:184])
+
+
+def test_two_handles_on_two_streams(KV):
+    """Calls of different handles at the same time."""
+    c = Chunks(KV, [700, 50, 3000], [300, 200, 100], 64, 2, 4, 128, "bf16")
+    want_c = c.check(200, 4)
+    H, G, D, counts = 3, 2, 64, [700, 33, 512]
+    q, k, v = _qkv(sum(counts), H, G, D, "f16")
+    kv, starts = _handle(KV, H, G, D, 3), _starts(counts)
+    want_p = kv.attend_prompt(q, k, v, starts)
+    lens, cstarts = _i32(c.lens), _starts(c.counts)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        got[0].append(c.kv.attend_chunk(c.q, c.k, c.v, c.dev_table, lens, cstarts, window=200, sinks=4,
+                                        out=torch.empty_like(want_c), stream=streams[0]))
+        got[1].append(kv.attend_prompt(q, k, v, starts, out=torch.empty_like(want_p), stream=streams[1]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want_c) for x in got[0]) and all(torch.equal(x, want_p) for x in got[1])
+    assert c.kv.get_error() == 0 and kv.get_error() == 0
+
+
 # ---- a server's steps --------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (60, 3)])
