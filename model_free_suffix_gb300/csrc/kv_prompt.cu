@@ -1123,6 +1123,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t gone = mt.gone >> (e0 / 16);
           if (gone & 1) see &= 0xffff0000u;
           if (gone & 2) see &= 0xffffu;
+          if (__all_sync(FULL, see == 0xffffffffu)) return;  // (half of an edge's tile, mostly)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!(see >> e & 1)) s[e] = 0xff800000u;
