@@ -58,14 +58,15 @@ constexpr int LOADERS = 4;
 constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 112;
 static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
 // p and o are relative to m, the maximum as it was when it was last set, and scaled anew
-// only once the maximum has grown by a THRESHOLD more, as powers of 2.  bf16 has the range of 32
-// bits.  f16: p is up to 2^15.99 before that, 2^UP for the maximum as it was; it has all its bits
+// only once the maximum has grown by a THRESHOLD more, as powers of 2.  bf16 has the range of
+// 32 bits; p is that much smaller, and so is o, which loses bits of values below 2^-111.
+// f16: p is up to 2^15.99 before that, 2^UP for the maximum as it was; it has all its bits
 // down to 2^-21 of that, and below an error of 2^-33 of it.
 template <typename T>
 struct Range;
 template <>
 struct Range<__nv_bfloat16> {
-  static constexpr float THRESHOLD = 40.f, UP = 1.f - THRESHOLD;  // p < 2: see `high`
+  static constexpr float THRESHOLD = 16.f, UP = 1.f - THRESHOLD;  // p < 2: see `high`
 };
 template <>
 struct Range<__half> {

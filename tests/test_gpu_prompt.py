@@ -113,6 +113,34 @@ def test_scales(KV, scale):
     _prompt(KV, [140, 40], 2, 2, 64, "bf16", scale=scale)
 
 
+@pytest.mark.parametrize("power", [-100, -60, 60, 100])
+def test_values_of_any_size(KV, power):
+    """bfloat16 has the range of 32 bits: values of 2^power give results of that size."""
+    counts, H, G, D = [300, 70], 1, 2, 64
+    q, k, v = _qkv(sum(counts), H, G, D, "bf16")
+    kv = _handle(KV, H, G, D, len(counts))
+    plain = kv.attend_prompt(q, k, v, _starts(counts))
+    out = kv.attend_prompt(q, k, v * 2.0 ** power, _starts(counts))
+    assert torch.equal(out.double(), plain.double() * 2.0 ** power)
+    kv.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_scores_that_grow_along_a_row(KV, dtype):
+    """Maxima far above those of the tiles before, in one half of a tile or the other, again and again."""
+    counts, H, G, D = [900, 260], 1, 2, 64
+    q, k, v = _qkv(sum(counts), H, G, D, dtype, size=1.0)
+    step = torch.arange(sum(counts), device="cuda") // 50
+    k = (k.float() * 0.25 + step[:, None, None] * 0.5).to(k.dtype)
+    q = (q.float() * 0.25 + 0.5).to(q.dtype)
+    kv = _handle(KV, H, G, D, len(counts))
+    for window in (0, 333):
+        out = kv.attend_prompt(q, k, v, _starts(counts), window=window)
+        _check_rows(out, q, k, v, counts, H, G, D, D ** -0.5, window, 0)
+    assert kv.get_error() == 0
+    kv.close()
+
+
 def test_long_rows(KV):
     """Several hundred tiles in one launch, cut in shares."""
     _prompt(KV, [3000, 2, 1501], 1, 2, 128, "bf16")
