@@ -198,12 +198,14 @@ __global__ void __launch_bounds__(THREADS, 1) assign_kernel(KvAssignArgs a) {
     return from < a.num_pages ? a.free[from] : -1;
   };
 #pragma unroll 1
-  for (int b = rank; b < a.B; b += warps)
+  for (int b = rank; b < a.B; b += warps) {
+    if (s_need[b] < 0) continue;  // (what it holds may be below 0, and no place of the table)
     for (int j = s_held[b] + lane; j < s_need[b]; j += 32) {
       const int page = taken_page(b, j);
       if (page < 0 || page >= a.num_pages) bits |= SGD_KV_ERR_PAGE;
       a.table[(long long)b * a.max_pages + j] = page;
     }
+  }
   if (a.N > OWN_TOKENS) {
     if (bits) atomicOr(a.err, bits);
     return;

@@ -178,6 +178,36 @@ def test_damaged_state_is_reported(KV):
     assert kv.get_error(clear=True) & L.KV_ERR_PAGE and plan.slots.tolist() == [-1] * 4
 
 
+@pytest.mark.parametrize("held", [-1, -2, -7, -2 ** 31])
+def test_a_row_that_holds_less_than_nothing(KV, held):
+    """It is passed over: its row of the table, those beside it and what lies around the table stay as they were."""
+    from model_free_suffix_gb300 import _lib as L
+    B, width, around = 5, 6, 4
+    kv = KV(num_pages=40, page_size=16, kv_heads=1, head_dim=64, max_batch=B, max_pages_per_row=width)
+    pages = kv.new_pages()
+    tables = torch.full((around + B + around, width), -77, dtype=torch.int32, device="cuda")
+    lists = torch.full((40 + 40 + 40,), -55, dtype=torch.int32, device="cuda")
+    tables[around:around + B], lists[40:80] = pages.block_table, pages.free
+    pages.block_table, pages.free = tables[around:around + B], lists[40:80]
+    kv.assign(pages, _i32([0] * B), _i32([40, 50, 33, 1, 16]), 200)
+    assert kv.get_error() == 0
+    before, free, count = tables.clone(), lists.clone(), pages.free_count.item()
+    for row in (0, 2, 4):
+        for keep, new in ((0, 0), (0, 90), (16, 1)):
+            at = pages.held.clone()
+            at[row] = held
+            pages.held.copy_(at)
+            keeps, news = [40, 50, 33, 1, 16], [0] * B
+            keeps[row], news[row] = keep, new
+            plan = kv.assign(pages, _i32(keeps), _i32(news), 100)
+            assert kv.get_error(clear=True) == L.KV_ERR_LENGTH
+            keeps[row] = 0
+            assert plan.seq_lens.tolist() == keeps and plan.q_start.tolist() == [0] * (B + 1)
+            assert torch.equal(tables, before) and torch.equal(lists, free) and pages.free_count.item() == count
+            assert pages.held.tolist() == at.tolist()
+            pages.held.copy_(_i32([3, 4, 3, 1, 1]))
+
+
 def test_outputs_that_are_left_out_and_lengths_in_place(KV):
     p = Pair(KV, 40, 16, 4, 8)
     from model_free_suffix_gb300 import PagePlan
