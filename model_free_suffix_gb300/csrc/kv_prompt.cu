@@ -37,6 +37,7 @@
 // maximum and for p (8.1); the first half of the next scores before the products with p (7.3: N =
 // 64 reads the queries from shared memory twice as often); the issuing thread alone in a
 // divergent branch (8.1: operands go through vector registers).
+#include <float.h>
 #include <math_constants.h>
 
 #include "kv_attend.cuh"
@@ -57,20 +58,36 @@ constexpr int LOADERS = 4;
 // 120 1.28 (the softmax ones do).
 constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 112;
 static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
-// p and o are relative to m, the maximum as it was when it was last set, and scaled anew
-// only once the maximum has grown by a THRESHOLD more, as powers of 2.  bf16 has the range of
-// 32 bits; p is that much smaller, and so is o, which loses bits of values below 2^-111.
-// f16: p is up to 2^15.99 before that, 2^UP for the maximum as it was; it has all its bits
-// down to 2^-21 of that, and below an error of 2^-33 of it.
+// p and o are relative to a reference, the maximum as it was when it was last set, for which p
+// is 2^UP.  It is set anew, and o scaled to it, only where the types' range asks for it:
+// bf16 has the range of 32 bits, but values may be up to 2^128.  o is at most the sum l of p
+// (and 2^-8 of it) times the largest value, so l stays below 1.  p is that much smaller, and so
+// is o, which loses bits of values below 2^-111.
+// f16: p is up to 2^15.99 (< 65504) before that, 2^UP for the maximum as it was; it has all its
+// bits down to 2^-21 of that, and below an error of 2^-33 of it.  (o is within 2^63.)
 template <typename T>
 struct Range;
 template <>
 struct Range<__nv_bfloat16> {
-  static constexpr float THRESHOLD = 16.f, UP = 1.f - THRESHOLD;  // p < 2: see `high`
+  static constexpr float UP = -15.f, THRESHOLD = 0.f;  // (l tells)
 };
 template <>
 struct Range<__half> {
   static constexpr float THRESHOLD = 8.f, UP = 15.99f - THRESHOLD;
+};
+// bf16: the largest l, and by how much the reference rises where l is of many tokens rather than of
+// a larger one, as a power of 2.  Either type: how much larger one makes other references of the
+// warp rise as well (so that fewer tiles are done twice).
+constexpr float L_MOST = 0.98f, RISE = 14.f, WITH = 1.f;
+// References of this size on (as powers of 2) are far: 32 bits hold them too coarsely (2^-12 here),
+// and p is made from the difference of the scores, for which a half of a tile is gone over twice: with
+// such rows in every warp a step's prompts take 3.4 ms, not 1.34.
+constexpr float FAR = 4096.f;
+// A row's reference: the score (with the scale that its tile's keys were brought to; -inf: none yet) and what
+// is added to its exponent (log2 of the values' scale, RISEs).
+struct __align__(16) Reference {
+  float s, add;
+  int far;
 };
 // What a unit costs beside its tiles, in tiles; the fewest tiles of a part; the least work that
 // is worth a CTA.  Measured: one prompt of 200 tokens 19 us with (3, 2, 3), 25 with 2 or 5 in the
@@ -363,8 +380,8 @@ struct Walk {
   }
 };
 
-// Parts: [D / 4][ROWS] sums (four dims each), [ROWS] maxima, [ROWS] sums of p; two
-// for each CTA, of the unit that its share begins within (0) and ends within (1).
+// Parts: [D / 4][ROWS] results (four dims each) and what they weigh, 2^(s c + add): [ROWS] s,
+// [ROWS] add; two for each CTA, of the unit that its share begins within (0) and ends within (1).
 struct Join {
   int parts, q0, r0, nrows, h;
 };
@@ -604,6 +621,24 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
+// 1 / x of a power of two within 2^+-126: exact
+__device__ __forceinline__ float inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
+// Rows' 64 scores at s_at less `at` and `less`.  (Out of the way: inlined it slowed down what is
+// around it, by up to 3%.)
+__device__ __noinline__ void lift(uint32_t s_at, float at, float less) {
+#pragma unroll 1
+  for (int e0 = 0; e0 < 64; e0 += 16) {
+    uint32_t s[16];
+    tmem_ld16(s_at + e0, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - at - less);
+    tmem_st16(s_at + e0, s);
+  }
+  tmem_wait_st();
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     new_kernel(const __grid_constant__ KvNewArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -616,6 +651,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ Meta meta[META];
   __shared__ BadTile bad_tiles[BAD_SEGMENTS][BAD_TILES];
   __shared__ int bad_count[BAD_SEGMENTS];
+  __shared__ Reference references[ROWS];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL, tid >> 5, 0);
@@ -1069,9 +1105,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t o_at = tmem + lanes + L::O + i * D;
     const float c0 = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);
-    // p is 2^UP times as large as it says.  bf16: one bit of it, that of an exponent of 1 or
-    // more, tells that the maximum has grown by 2^THRESHOLD.
     constexpr float UP = Range<T>::UP, THRESHOLD = Range<T>::THRESHOLD;
+    Reference &reference = references[R];
     Walk w(a, share);
     uint32_t g = 0, segments = 0;
     uint32_t buf = 0;            // of the next segment's first scores
@@ -1100,6 +1135,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         continue;
       }
       const bool live = R < w.unit.nrows;
+      // the reference's exponent; -inf: there is none yet, or a far one
       float m = live ? -CUDART_INF_F : 0.f, l = 0.f;  // (what rows that are not there hold does not matter)
       uint32_t turn_before = 0, use_before = 0;
 #pragma unroll 1
@@ -1113,7 +1149,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (j > 0) tmem_ld32(s_at, sa);
         const Meta &mt = meta[g % META];
         const int edge = mt.edge;
-        // z = s c; m is kept relative to z + log2 V, V the scale that the tile's values were brought to
+        // z = s c; m is that of z + log2 V, V the scale that the tile's values were brought to
         const float c = BF16 ? c0 : fmaxf(c0 * mt.k, 1e-37f), lv = BF16 ? 0.f : __log2f(mt.v);
         const uint64_t c2 = pair64(c, c), one = pair64(1.f, 1.f);
         // -inf in place of what the row does not see, of 32 tokens from e0 on
@@ -1134,15 +1170,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         // three roles run has to stay in the instruction cache.)
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          bool first = j + half == 0;  // (of a segment: there is no m yet)
-          uint64_t sum = 0;
+          bool first = j + half == 0;  // (of a segment: there is no reference yet)
+          bool lifted = false;         // scores of rows with a far reference are relative to it
+          float sum = 0.f;
           while (true) {
             bool grown = first;
             if (!first) {
               const float base = (m == -CUDART_INF_F ? 0.f : m) - UP - lv;
               const uint64_t b2 = pair64(-base, -base);
               uint64_t sum0 = 0, sum1 = 0;
-              uint32_t high = 0;
               float top0 = -CUDART_INF_F, top1 = -CUDART_INF_F;
               // 32 tokens' p relative to m as it is, and their sum
               auto exps = [&](const uint32_t (&s)[32], uint32_t *to) {
@@ -1161,7 +1197,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                   sum1 = fma2(pair64(y[2], y[3]), one, sum1);
                   to[e / 2] = pack2<T>(y[0], y[1]);
                   to[e / 2 + 1] = pack2<T>(y[2], y[3]);
-                  if (BF16) high |= to[e / 2] | to[e / 2 + 1];
                 }
               };
               tmem_wait_ld();
@@ -1172,17 +1207,20 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (half == 0) tmem_ld32(s_at + 64, sa);
               if (edge) mask(sb, half * 64 + 32);
               exps(sb, pk + 16);
-              sum = fma2(sum0, one, sum1);
+              float u0, u1;
+              unpair(fma2(sum0, one, sum1), u0, u1);
+              sum = u0 + u1;
               if (BF16) {
-                grown = live && ((high & 0x40004000u) != 0 || m == -CUDART_INF_F);
+                grown = live && (l + sum > L_MOST || m == -CUDART_INF_F);
               } else {
                 const float top = fmaf(fmaxf(top0, top1), c, lv);
                 grown = live && (top > m + THRESHOLD || (m == -CUDART_INF_F && top > m));
               }
             }
             if (!__any_sync(FULL, grown)) break;
-            // The maximum may have grown too far for p to be relative to the old one (rarely but
-            // for a segment's first half): o and l are scaled to it, and p is made anew.
+            if (lifted) break;  // (NaN, or nothing seen so far)
+            // p would be too large for the reference as it is (rarely but for a segment's first half):
+            // the reference rises, o and l are scaled to it, and p is made anew.
             tmem_wait_ld();
             float largest = -CUDART_INF_F;
 #pragma unroll 1
@@ -1193,16 +1231,32 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) largest = max3(largest, __uint_as_float(sb[e]), __uint_as_float(sb[e + 1]));
             }
-            const float top = fmaf(largest, c, lv);
-            const bool up = live && (top > m + (THRESHOLD - 1.f) || (m == -CUDART_INF_F && top > m));
-            if (!first && !__any_sync(FULL, up)) break;  // (NaN, or nothing seen so far)
+            Reference ref{-CUDART_INF_F, 0.f, 0};
+            if (live && !first) ref = reference;
+            const bool none = ref.s == -CUDART_INF_F;
+            // the exponent of the largest p
+            const float y = ref.far ? fmaf(largest - (BF16 ? ref.s : ref.s * inverse(mt.k)), c, lv - ref.add + UP) : fmaf(largest, c, UP - m + lv);
+            const bool must = !none && (BF16 ? l + (ref.far ? 64.f * ex2_approx(y) : sum) > L_MOST : y > UP + THRESHOLD);
+            const bool rising = __any_sync(FULL, must && largest < CUDART_INF_F);
+            const bool up = must || (live && (none ? largest > -CUDART_INF_F : rising && y > UP + WITH));
+            if (!first && !__any_sync(FULL, up || ref.far)) break;  // (NaN, or nothing seen so far)
             float o_scale = 1.f;
             if (up) {
-              o_scale = m == -CUDART_INF_F ? 0.f : ex2_approx(m - top);
+              if (none || !BF16 || y > UP + 1.f) {
+                o_scale = none ? 0.f : ex2_approx(UP - y);
+                m = fmaxf(fmaf(largest, c, lv), -FLT_MAX);
+                ref = Reference{BF16 ? largest : largest * mt.k, lv, fabsf(m) >= FAR};
+                if (ref.far) m = -CUDART_INF_F;
+              } else {
+                o_scale = ex2_approx(-RISE);
+                ref.add += RISE;
+                m += RISE;
+              }
               l *= o_scale;
-              m = top;
             }
-            if (!first) {
+            if (live) reference = ref;
+            __syncwarp();
+            if (!first && __any_sync(FULL, up)) {
               if (j > 0) ok = wait(PV_DONE + i * L::BUFFERS + turn_before, use_before);
               if (half > 0) ok = ok && wait(PV_HALF + i * L::BUFFERS + turn, use);
               ok = __all_sync(FULL, ok);
@@ -1219,12 +1273,16 @@ __global__ void __launch_bounds__(THREADS, 1)
               tmem_wait_st();
             }
             first = false;
+            if (__any_sync(FULL, ref.far)) {
+              // scores relative to such references, so that m does not matter
+              const float at = ref.far ? (BF16 ? ref.s : ref.s * inverse(mt.k)) : 0.f, less = ref.far ? __fdividef(ref.add, c) : 0.f;
+              lift(s_at + half * 64, at, less);
+              lifted = true;
+            }
             tmem_ld32(s_at + half * 64, sa);
           }
           if (!ok) break;
-          float u0, u1;
-          unpair(sum, u0, u1);
-          l = BF16 ? l + (u0 + u1) : fmaf(u0 + u1, __fdividef(1.f, mt.v), l);
+          l = BF16 ? l + sum : fmaf(sum, __fdividef(1.f, mt.v), l);
           tmem_st32(s_at + half * 32, pk);
           tmem_wait_st();
           tmem_before_sync();
@@ -1248,7 +1306,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool whole = w.whole();
       const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
       float *part = new_part<D>(a, slot) + R * 4;
-      const float inv = 1.f / l;  // (a row sees itself: 0 only where its scores are all -inf, and then the result is NaN)
+      const bool nothing = !whole && live && reference.s == -CUDART_INF_F;
+      // (a row sees itself: 0 only where its scores are all -inf, and then the result is NaN)
+      const float inv = nothing ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
@@ -1267,7 +1327,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4 *>(part + (d / 4 + e) * (ROWS * 4)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            *reinterpret_cast<float4 *>(part + (d / 4 + e) * (ROWS * 4)) =
+                make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv, __uint_as_float(o[4 * e + 2]) * inv,
+                            __uint_as_float(o[4 * e + 3]) * inv);
         }
       }
       tmem_before_sync();
@@ -1275,8 +1337,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (R < w.unit.nrows) {
         if (!whole) {
           float *ml = new_part<D>(a, slot) + ROWS * D + R;
-          ml[0] = m;
-          ml[ROWS] = l;
+          ml[0] = reference.s;
+          ml[ROWS] = nothing ? 0.f : reference.add + __log2f(l);
         }
         const int n = bad_count[segments % BAD_SEGMENTS];
         uint32_t any = 0;
@@ -1305,29 +1367,39 @@ constexpr int JOIN_THREADS = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ KvNewArgs a) {
   constexpr int W = JOIN_THREADS / 32, E = D / 4 / W;  // float4s of a warp
-  extern __shared__ float s_w[];                       // [parts][32]
+  extern __shared__ float s_w[];                       // [parts][32] each of the parts' s and add
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join join = *join_of(a, blockIdx.x);
   const int R = blockIdx.y * 32 + lane;
   if (join.parts == 0 || (int)blockIdx.y * 32 >= join.nrows) return;
   auto slot = [&](int p) { return new_part<D>(a, 2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)); };
-  float *s_l = s_w + join.parts * 32;
+  float *s_add = s_w + join.parts * 32;
   for (int p = warp; p < join.parts; p += W) {
-    const float *ml = slot(p) + ROWS * D + R;
-    s_w[p * 32 + lane] = ml[0];
-    s_l[p * 32 + lane] = ml[ROWS];
+    const float *weight = slot(p) + ROWS * D + R;
+    s_w[p * 32 + lane] = weight[0];
+    s_add[p * 32 + lane] = weight[ROWS];
   }
   __syncthreads();
-  float top = -CUDART_INF_F, l = 0.f;
-  for (int p = 0; p < join.parts; ++p) top = fmaxf(top, s_w[p * 32 + lane]);
-  const float base = top == -CUDART_INF_F ? 0.f : top;
-  for (int p = 0; p < join.parts; ++p) l = fmaf(s_l[p * 32 + lane], ex2_approx(s_w[p * 32 + lane] - base), l);
+  // relative to the largest, by differences (see FAR)
+  const float c0 = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);
+  float s0 = s_w[lane], add0 = s_add[lane], all = 0.f;
+  for (int p = 1; p < join.parts; ++p) {
+    const float s = s_w[p * 32 + lane], add = s_add[p * 32 + lane];
+    if (fmaf(s - s0, c0, add - add0) > 0.f) {
+      s0 = s;
+      add0 = add;
+    }
+  }
+  auto weight = [&](int p) { return ex2_approx(fmaf(s_w[p * 32 + lane] - s0, c0, s_add[p * 32 + lane] - add0)); };
+  for (int p = 0; p < join.parts; ++p) all += weight(p);
+  // (weights that add up to 1: no sum beyond the largest value)
+  const float inv = 1.f / all;
   float4 x[E] = {};
 #pragma unroll 4
   for (int p = 0; p < join.parts; ++p) {
     const float *from = slot(p) + (warp * E * ROWS + R) * 4;
-    const float k = ex2_approx(s_w[p * 32 + lane] - base);
+    const float k = weight(p) * inv;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float4 v = *reinterpret_cast<const float4 *>(from + e * (ROWS * 4));
@@ -1338,13 +1410,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     }
   }
   if (R >= join.nrows) return;
-  const float inv = 1.f / l;
   const int row = join.r0 + R;
   T *out = static_cast<T *>(a.out) +
            ((long long)(join.q0 + row / a.group) * a.q_heads + join.h * a.group + row % a.group) * D + warp * E * 4;
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    *reinterpret_cast<uint2 *>(out + e * 4) = make_uint2(pack2<T>(x[e].x * inv, x[e].y * inv), pack2<T>(x[e].z * inv, x[e].w * inv));
+    *reinterpret_cast<uint2 *>(out + e * 4) = make_uint2(pack2<T>(x[e].x, x[e].y), pack2<T>(x[e].z, x[e].w));
 }
 // (a unit has at most as many parts as there are CTAs)
 constexpr int join_smem(int ctas) { return ctas * 32 * 2 * 4; }
