@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(THREADS, 1) assign_kernel(KvAssignArgs a) {
         taken += more;
       }
     } else {
-      s_place[b] = (int)back_at;
+      s_place[b] = (int)min(back_at, (long long)a.num_pages);  // (more are only where held is wrong, and go nowhere)
       back_at -= more;
     }
     mine += s_start[b];

@@ -208,6 +208,27 @@ def test_a_row_that_holds_less_than_nothing(KV, held):
             pages.held.copy_(_i32([3, 4, 3, 1, 1]))
 
 
+def test_rows_that_claim_more_pages_than_32_bits_count(KV):
+    """8192 rows of 2^18 pages each, of a cache of 1000: the list takes the first and no others."""
+    from model_free_suffix_gb300 import _lib as L
+    B, width, N = 8192, (1 << 18) + 7, 1000
+    kv = KV(num_pages=N, page_size=16, kv_heads=1, head_dim=64, max_batch=B, max_pages_per_row=width)
+    pages = kv.new_pages()
+    pages.block_table.fill_(3)
+    pages.block_table[0, :N] = torch.arange(N, dtype=torch.int32, device="cuda")
+    lists = torch.full((3 * N,), -55, dtype=torch.int32, device="cuda")
+    pages.free = lists[N:2 * N]
+    pages.held.fill_(width)
+    pages.free_count.zero_()
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    plan = kv.assign(pages, zero, zero, 1)
+    assert kv.get_error(clear=True) == L.KV_ERR_PAGE
+    assert pages.free.tolist() == list(range(N)) and pages.free_count.tolist() == [N]
+    assert bool((lists[:N] == -55).all()) and bool((lists[2 * N:] == -55).all())
+    assert not bool(pages.held.any()) and bool((pages.block_table == -1).all()) and plan.q_start[-1].item() == 0
+    kv.close()
+
+
 def test_outputs_that_are_left_out_and_lengths_in_place(KV):
     p = Pair(KV, 40, 16, 4, 8)
     from model_free_suffix_gb300 import PagePlan
