@@ -630,7 +630,8 @@ int sgd_kv_attend(sgd_kv *kv, const sgd_kv_layer *layer, const void *q, int32_t 
  *   out  DEVICE dtype [N, q_heads, head_dim], contiguous, 16-byte aligned.
  * Infinities and NaN in q, k or v reach the tokens that see them, and no others.
  * Tokens from q_start[B] on belong to no row: nothing is read or written there.
- * Rows with bad starts are passed over and reported (SGD_KV_ERR_LENGTH).
+ * Rows with bad starts are passed over and reported (SGD_KV_ERR_LENGTH); where starts
+ * that descend again let rows claim far more than N tokens together, all are.
  * B <= SGD_KV_NEW_MAX_ROWS and N * (q_heads / kv_heads) <= 2^30, else SGD_ETOOLARGE. */
 #define SGD_KV_NEW_MAX_ROWS 8192
 int sgd_kv_attend_prompt(sgd_kv *kv, const void *q, const void *k, const void *v, int32_t dtype,

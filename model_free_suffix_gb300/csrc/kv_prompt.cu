@@ -246,6 +246,12 @@ __device__ const Share &share_of(const KvNewArgs &a, int *first, uint32_t *bits)
   }
   __syncthreads();
   const long long blocks = total;
+  // Rows that overlap may claim any number of units, with what counts them beyond 32 bits; those that
+  // do not have no more than this many.  (The same for all threads.)
+  if (blocks > ((long long)a.r.N * a.group + (long long)(ROWS - 1) * B) / ROWS) {
+    *bits |= SGD_KV_ERR_LENGTH;
+    return s;
+  }
   const int c0 = (int)(blocks * tid / THREADS), c1 = (int)(blocks * (tid + 1) / THREADS);
   int b_from = 0;
   mine = 0;

@@ -1,4 +1,5 @@
-"""Attention of prompts and chunks at the ends of its types' range: scores far from 0, values next to the largest.
+"""Attention of prompts and chunks at the ends of its types' range (scores far from 0, values next to the largest)
+and of what counts its work.
 
 The scores here are exact in 32 bits (few products, few bits each), so nothing of the bound of
 test_gpu_prompt.py grows with them: with results u |want| for their rounding, u sum_j p_j |v_j| for that of
@@ -196,4 +197,35 @@ def test_large_queries_and_keys_give_finite_results(KV, dtype, size):
     for scale in (1.0, -0.125):
         out = kv.attend_prompt(q.cuda(), k.cuda(), v.cuda(), _starts(counts), scale=scale).cpu()
         assert bool(out.isfinite().all()) and float(out.abs().max()) <= float(v.abs().max()) * (1 + 2.0 ** -6)
+    kv.close()
+
+
+@pytest.mark.parametrize("chunk", [False, True])
+def test_rows_that_claim_the_same_tokens_again_and_again(KV, chunk):
+    """Starts that descend: far more work than the call's tokens are.  It is reported, and nothing is written."""
+    from model_free_suffix_gb300 import _lib as L
+    N, H, G, D, B = 2000, 1, 4, 64, 33
+    kv = KV(num_pages=4, page_size=64, kv_heads=H, head_dim=D, q_heads=H * G, max_batch=B, max_pages_per_row=40)
+    g = torch.Generator().manual_seed(7)
+    q, k, v = (torch.randn(N, h, D, generator=g).bfloat16().cuda() for h in (H * G, H, H))
+    out = torch.full_like(q, 7.0)
+
+    def call(starts, lens):
+        if not chunk:
+            return kv.attend_prompt(q, k, v, _i32(starts), out=out)
+        table = torch.full((B, 40), -1, dtype=torch.int32, device="cuda")
+        return kv.attend_chunk(q, k, v, table, _i32(lens), _i32(starts), out=out)
+
+    call([0, N] * 17, [N, 0] * 16 + [N])
+    assert kv.get_error(clear=True) == L.KV_ERR_LENGTH and bool((out == 7).all())
+    # (rows that follow one another may have many more units than their tokens fill)
+    counts = [61] * 32 + [48]
+    call([0] + list(itertools.accumulate(counts)), counts)
+    assert kv.get_error() == 0
+    at = 0
+    for c in counts:
+        x = slice(at, at + c)
+        want, mass = R.attend(q[x].cpu().double().view(c, H, G, D), k[x].cpu().double(), v[x].cpu().double(), 0, D ** -0.5)
+        _check(out[x], want.reshape(c, H * G, D), mass.reshape(c, H * G, D), at)
+        at += c
     kv.close()
