@@ -1170,6 +1170,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!(see >> e & 1)) s[e] = 0xff800000u;
+          __syncwarp();
         };
         // Half of the tokens at a time, so that the products with the first run beside the
         // exponentials of the second.  (Loops rather than straight code: what 16 warps in
@@ -1320,8 +1321,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t o[32];
         tmem_ld32(o_at + d, o);
         tmem_wait_ld();
-        if (R >= w.unit.nrows) continue;
-        if (whole) {
+        if (R >= w.unit.nrows) {
+          // (nowhere to go)
+        } else if (whole) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float v[8];
@@ -1337,6 +1339,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv, __uint_as_float(o[4 * e + 2]) * inv,
                             __uint_as_float(o[4 * e + 3]) * inv);
         }
+        __syncwarp();  // (a warp's rows may end within it, and the next load is the whole warp's)
       }
       tmem_before_sync();
       warp_arrive(O_EMPTY + i);
