@@ -338,6 +338,35 @@ def test_graphs_streams_and_repetition(KV):
     kv.close()
 
 
+def test_one_handle_on_several_streams_in_turn(KV):
+    """Calls of one handle must not overlap: each stream waits for the one before it."""
+    H, G, D = 2, 4, 128
+    q, k, v = _qkv(1200, H, G, D, "bf16")
+    kv = _handle(KV, H, G, D, 3)
+    counts = [[500, 400, 300], [100, 1000, 90], [1200, 0, 0], [7, 600, 593]]
+    want = [kv.attend_prompt(q, k, v, _starts(c)).clone() for c in counts]
+    starts, out = _starts(counts[0]), torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.attend_prompt(q, k, v, starts, out=out)
+    main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    for _ in range(3):
+        for c, w in zip(counts, want):
+            n = sum(c)
+            starts.copy_(_starts(c))
+            graph.replay()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                again = kv.attend_prompt(q, k, v, starts)
+            other = torch.empty_like(q)
+            side.wait_stream(main)
+            kv.attend_prompt(q, k, v, starts, out=other, stream=side)
+            main.wait_stream(side)
+            assert all(torch.equal(x[:n], w[:n]) for x in (out, again, other))
+    assert kv.get_error() == 0
+    kv.close()
+
+
 # ---- chunks over the cache ---------------------------------------------------------------------------
 
 class Chunks:
