@@ -475,11 +475,12 @@ __device__ __forceinline__ uint4 load16(const unsigned short *p, bool vec) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A tile of the caller's keys or values by the loading warps themselves: `tokens` of
-// them, 0 behind.  CHECK: values that are not finite are taken out; returns
+// A tile of the caller's keys or values by the loading warps themselves, where TMA does not take it
+// (off 16 bytes: 8192 tokens, 32 query heads of 128 in groups of four, 2.07 ms against 0.48):
+// `tokens` of them, 0 behind.  CHECK: values that are not finite are taken out; returns
 // the bits of this warp's tokens that had some.
 template <typename T, int D, bool CHECK>
-__device__ __forceinline__ uint32_t copy_tile(uint32_t to, const void *base, long long stride, bool vec, int tokens, int tid) {
+__device__ __forceinline__ uint32_t copy_tile(uint32_t to, const void *base, long long stride, int tokens, int tid) {
   constexpr int C = Plan<D>::CHUNKS, PER = TILE * C / (32 * LOADERS), STEP = 32 * LOADERS / C, IN_WARP = 32 / C;
   const int c = tid % C, line0 = tid / C;
   const unsigned short *p = static_cast<const unsigned short *>(base) + line0 * stride + c * 8;
@@ -490,7 +491,7 @@ __device__ __forceinline__ uint32_t copy_tile(uint32_t to, const void *base, lon
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = make_uint4(0, 0, 0, 0);
-      if (line0 + (i0 + i) * STEP < tokens) v[i] = load16(p + (long long)(i0 + i) * STEP * stride, vec);
+      if (line0 + (i0 + i) * STEP < tokens) v[i] = load16(p + (long long)(i0 + i) * STEP * stride, false);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           copy_tile<T, D, false>(ring + item % STAGES * L::HALF,
                                  static_cast<const T *>(a.k) + (w.row.q0 + from) * a.k_token + w.h * a.k_head, a.k_token,
-                                 false, tokens, me);
+                                 tokens, me);
           done();
         }
         settle();
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (!w.edge(j, x)) {
           copy_tile<T, D, false>(ring + item % STAGES * L::HALF,
                                  static_cast<const T *>(a.v) + (w.row.q0 + from) * a.v_token + w.h * a.v_head, a.v_token,
-                                 false, tokens, me);
+                                 tokens, me);
           done();
         } else {
           // (at most 7 tiles of a unit have an edge: 3 where its rows' tokens are, 3 where
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             note(segments, index, from,
                  copy_tile<T, D, true>(ring + item % STAGES * L::HALF,
                                        static_cast<const T *>(a.v) + (w.row.q0 + from) * a.v_token + w.h * a.v_head, a.v_token,
-                                       false, tokens, me));
+                                       tokens, me));
             done();
           }
         }
