@@ -54,8 +54,8 @@ constexpr int WARPS = 16, THREADS = 32 * WARPS;
 constexpr int W_LOAD = 8, W_ISSUE = 12, W_JOIN = 13;
 constexpr int LOADERS = 4;
 // Registers a thread by role: together what 512 threads are launched with (128 each).  With
-// 168 and 88 chunks of a step took 1.40 ms against 1.24 (the loading warps spill), with 136 and
-// 120 1.28 (the softmax ones do).
+// 168 and 88 chunks of a step took 1.59 ms against 1.27 (the loading warps spill), with 152 and 104
+// 1.29 and a step's prompts 1.37 against 1.33, with 136 and 120 chunks 1.39 (the softmax ones do).
 constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 112;
 static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <= THREADS * 128, "the pool of the launch");
 // p and o are relative to a reference, the maximum as it was when it was last set, for which p
@@ -90,9 +90,10 @@ struct __align__(16) Reference {
   int far;
 };
 // What a unit costs beside its tiles, in tiles; the fewest tiles of a part; the least work that
-// is worth a CTA.  Measured: one prompt of 200 tokens 19 us with (3, 2, 3), 25 with 2 or 5 in the
-// first or last place; a step's prompts 1.36 ms, 1.40 with 2 in the first.
-constexpr int OVERHEAD = 3, LEAST_PART = 2, LEAST_SHARE = 3;
+// is worth a CTA.  Measured: a step's prompts 1.33 ms, 1.36 with 2 or 5 in the first place; one
+// prompt of 200 tokens 18.6 us, 18.9 with 3 in the last and 24.7 with 5, a chunk of 68 over 2032
+// 32.0, 33.5 and 36.7.
+constexpr int OVERHEAD = 3, LEAST_PART = 2, LEAST_SHARE = 2;
 constexpr int META = 16;      // outlasts how far the loaders run ahead
 constexpr int BAD_SEGMENTS = 4, BAD_TILES = 8;
 
