@@ -13,6 +13,11 @@ calls fit together.  Per step
 
 The host decides only what it knows anyway: which request a row serves, and how many of
 its tokens a step takes.
+
+One call for all rows is the simplest, not the fastest, where most of many rows decode: with
+254 rows of one token and 2 of 512 over 1024 to 4096 it takes 1.16 ms.  Such a server keeps the
+rows that decode in front, and after the write gives them to `attend` and the others alone to
+`attend_chunk` (slices of the table, the lengths and the starts, these from 0 again): 0.31 ms.
 """
 from __future__ import annotations
 

@@ -15,7 +15,7 @@
 //
 // Nothing here is bound by bytes but the places of prompts' tokens (12 bytes each): a call
 // of a serving step is a chain of launch, one read of the rows, four prefix sums, two
-// cluster barriers and the reads of tables and list.  Measured, a call: 4 rows 4 us, 256
+// cluster barriers and the reads of tables and list.  Measured, a call: 4 rows 5 us, 256
 // rows of 1..17 tokens 8 to 9, 1024 rows of which 256 give up or get 8192 tokens'
 // pages (half of the calls place a million tokens) 26.  One CTA of 1024 threads took 28 and 616
 // for the latter two; clusters of four CTAs 9 and 34, of 256 threads a CTA 9 and 34, of 1024

@@ -28,9 +28,12 @@
 // What bounds it.  Per tile and two row tiles the products take 2048 cycles at a dim of
 // 128, 1024 at 64, and the exponentials 1024; from p to the next scores of a row tile lie
 // both products (1024 cycles) and some 300 of latency, and its exponentials, alone, take the
-// thread of a row some 1600 to 2000.  So a tile takes about 3100 cycles either way: 32768 tokens,
-// 32 query heads of 128 in groups of four, 6.5 ms, 1350 TFLOP/s; at a dim of 64 800.
-// Tried and slower or no faster, the same 32768 tokens in ms: two threads a row, half of
+// thread of a row some 1600 to 2000.  That is 2900 to 3300 cycles a tile; measured 3800 with all that
+// a unit costs: 32768 tokens, 32 query heads of 128 in groups of four, 6.3 ms at 2070 MHz, 1390
+// TFLOP/s; calls one after the other, which the power limit holds at some 1980 MHz, 6.6 ms, 1330.  At a
+// dim of 64 5.6 ms, 780.  A tile of the cache takes 1.8 times as long: without its conversion
+// a chunk of 1391 tokens over 31377 took 0.79 ms, not 0.97.
+// Tried and slower or no faster, the same 32768 tokens in ms, 6.5 then: two threads a row, half of
 // a tile's tokens each, meeting once a tile (6.6, chunks over the cache 30% slower: 16
 // softmax warps leave the loading ones few registers and turns) or finishing in turn (9.6);
 // all p of a tile at once (6.5, short prompts and chunks 10% slower); s read twice, for its
@@ -62,7 +65,7 @@ static_assert(32 * W_LOAD * REGS_SOFTMAX + 32 * (WARPS - W_LOAD) * REGS_OTHER <=
 // is 2^UP.  It is set anew, and o scaled to it, only where the types' range asks for it:
 // bf16 has the range of 32 bits, but values may be up to 2^128.  o is at most the sum l of p
 // (and 2^-8 of it) times the largest value, so l stays below 1.  p is that much smaller, and so
-// is o, which loses bits of values below 2^-111.
+// is o, which loses bits of values below 2^-111 (2^-97 in rows whose reference rose for the sake of l).
 // f16: p is up to 2^15.99 (< 65504) before that, 2^UP for the maximum as it was; it has all its
 // bits down to 2^-21 of that, and below an error of 2^-33 of it.  (o is within 2^63.)
 template <typename T>
@@ -1372,8 +1375,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // The parts of the units that cuts went through: 32 rows a block, lanes along rows, a
 // warp's share of the dims each.  The parts' weights first, then the sums with all of a
-// warp's dims of several parts in flight (with one load after the other a chunk of 100
-// tokens over 2000, in five parts, took 15 us here, half of its attention).
+// warp's dims of several parts in flight (with one load after the other a chunk of 68
+// tokens over 2032, in five parts, took 15 us here, half of its attention).
 constexpr int JOIN_THREADS = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ KvNewArgs a) {

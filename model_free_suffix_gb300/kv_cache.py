@@ -224,7 +224,8 @@ class KVCache:
         new tokens are the last ones of its seq_lens[b], those before them are read from
         the cache, and their own keys and values are taken from k and v (whether they
         have been written makes no difference).  For rows of many new tokens what attend
-        is for rows of few."""
+        is for rows of few: up to some 32 tokens in groups of four query heads attend is
+        faster, for single ones five times."""
         B = self._rows(block_table, seq_lens, q_start)
         args, out, scale = self._new_tokens(q, k, v, out, scale)
         t = self._t
@@ -256,7 +257,8 @@ class KVCache:
         (`pages` changes), and the packed tokens get their places.  keep after a
         verification is what was accepted; keep = new = 0 ends a row.  `total`: the room
         for packed tokens (`out` has its own).  Rows that the room or the free pages do
-        not suffice for get no new tokens, and get_error tells."""
+        not suffice for get no new tokens, and get_error tells; what they want counts
+        against the rows behind them all the same, so let in prompts that fit."""
         B = keep.shape[0]
         if out is None:
             if total is None:
